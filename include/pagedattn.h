@@ -16,8 +16,10 @@
  *   pa_copy_blocks        whole-block copies for copy-on-write (tutorial §5
  *                         "Copy-on-write sharing"; subroutine-cs article §3);
  *
- * plus pa_decode_slots (the slot of each sequence's newest token, the
- * tutorial's PhysicalIndex, §4) and a host-side block manager (pa_bm_*,
+ * plus pa_rope_append (norm, rotation and cache write in one pass), an 8-bit
+ * cache with its own write, decode and expansion (pa_rope_append_q8,
+ * pa_decode_q8, pa_expand_blocks_q8), pa_decode_slots (the slot of each sequence's
+ * newest token, the tutorial's PhysicalIndex, §4) and a host-side block manager (pa_bm_*,
  * tutorial §4 "Tiny example": allocate / free / fork / append).
  *
  * Conventions for every device call
@@ -387,6 +389,127 @@ pa_status pa_swap_blocks(void* const* dst_pools, const void* const* src_pools, i
                          const int32_t* block_pairs, int num_pairs, int64_t block_bytes,
                          int src_num_blocks, int dst_num_blocks, int32_t* status_dev,
                          cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotated cache writes and the 8-bit cache                                  */
+/* ------------------------------------------------------------------------ */
+/*
+ * The pages have no counterpart to this section: it is what a serving step does
+ * around the cache (per-head norms, rotary positions, an 8-bit KV cache).
+ */
+
+/*
+ * Norm and rotation of the new tokens' queries and keys, and the cache write,
+ * in one pass.  Sequence b's new tokens are rows q_start[b] .. q_start[b+1]-1 of
+ * q, key and value; they are its LAST n_b tokens (as in pa_prefill), already
+ * counted in seq_lens: row q_start[b] + i is position seq_lens[b] - n_b + i and
+ * goes to that position's slot.  For every query and key head row x:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight          (weight non-NULL; RMS norm)
+ *   (y_a, y_b) -> (y_a c_j - y_b s_j, y_b c_j + y_a s_j),   j < rotary_dim / 2
+ * with the pair (a, b) = (j, j + rotary_dim / 2), or (2j, 2j + 1) with
+ * interleaved != 0; elements from rotary_dim on are not rotated.  c_j and s_j are
+ * cos_sin[position][j] and cos_sin[position][rotary_dim / 2 + j].  fp32
+ * throughout, rounded once to the storage type.  Values are bit copies.
+ *   q_out        [total_q, num_q_heads, head_dim], packed; may be q itself when q
+ *                is packed; any other overlap with q, key or value is rejected
+ *   q            [total_q, num_q_heads, head_dim], token stride q_token_stride
+ *                elements (0 = packed); key / value [total_q, num_kv_heads,
+ *                head_dim], token stride kv_token_stride (0 = packed).  Strides
+ *                are multiples of 8 elements: slices of one projection's output
+ *                can be passed as they are.
+ *   q_weight, k_weight  [head_dim] storage type, each nullable (no norm)
+ *   cos_sin      [max_position, rotary_dim] fp32; rotary_dim a multiple of 16 up
+ *                to head_dim, or 0 (no rotation; cos_sin may be NULL)
+ *   positions    [total_q] int32 or NULL: the row of cos_sin for each token, where
+ *                it is not its place in the sequence
+ *   q_start      [num_seqs + 1] int32 as in pa_prefill, or NULL: one new token per
+ *                sequence (a decode step; total_q = num_seqs), and an empty
+ *                sequence's row is left alone
+ * A sequence with n_b > seq_lens[b], seq_lens[b] > max_blocks * block_size or rows
+ * outside [0, total_q), and a token whose row of cos_sin is out of range, are
+ * skipped (q_out and pool rows untouched; reported in checked mode); a bad block
+ * id skips the cache write of its tokens (reported).  Rows behind the last
+ * sequence are left alone.  Two tokens with the same slot are a caller error.
+ * Supported: fp16 / bf16, head_dim 64 or 128, block_size 8/16/32/64, any head
+ * counts; q_out, q, key, value, weights, cos_sin and pools 16-byte aligned.
+ */
+pa_status pa_rope_append(void* q_out, void* k_pool, void* v_pool, const void* q, const void* key,
+                         const void* value, const void* q_weight, const void* k_weight, float eps,
+                         const float* cos_sin, int max_position, int rotary_dim, int interleaved,
+                         const int32_t* positions, const int32_t* block_tables,
+                         const int32_t* seq_lens, const int32_t* q_start, int num_seqs,
+                         int total_q, int64_t q_token_stride, int64_t kv_token_stride,
+                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int max_blocks, int num_blocks, int dtype, int32_t* status_dev,
+                         cudaStream_t stream);
+
+/*
+ * The 8-bit cache.  k_pool / v_pool hold e4m3 codes, [num_blocks, num_kv_heads,
+ * block_size, head_dim] (one head's rows of a block are contiguous), k_scale /
+ * v_scale [num_blocks, num_kv_heads] fp32; a stored value is code * scale.  The
+ * writer's scales are powers of two: s(a) is the smallest 2^e, e >= -64, with
+ * a <= 448 * 2^e.  Readers take any positive finite scale.  Copy-on-write and
+ * swaps of such blocks are pa_copy_blocks_multi / pa_swap_blocks (they move
+ * bytes; the scale rows are one more pool when num_kv_heads is a multiple of 4).
+ *
+ * pa_rope_append_q8: pa_rope_append into it.  In each block and head, with a the
+ * largest finite magnitude of the rows this call writes there (a key's after its
+ * norm and rotation, from fp32),
+ *   - a block written from its row 0 on gets the scale s(a);
+ *   - a block with older rows below the first new one gets max(old scale, s(a)),
+ *     and if that is larger, the older rows' codes are brought to it (code *
+ *     old / new, rounded to nearest even: exact but for subnormal codes).
+ * New rows are rounded to nearest even from fp32; infinities become the largest
+ * code, NaN stays NaN.  Rows behind the newest are left as they were.  q_out and
+ * the other arguments and errors are those of pa_rope_append.
+ */
+pa_status pa_rope_append_q8(void* q_out, void* k_pool, void* v_pool, float* k_scale,
+                            float* v_scale, const void* q, const void* key, const void* value,
+                            const void* q_weight, const void* k_weight, float eps,
+                            const float* cos_sin, int max_position, int rotary_dim,
+                            int interleaved, const int32_t* positions,
+                            const int32_t* block_tables, const int32_t* seq_lens,
+                            const int32_t* q_start, int num_seqs, int total_q,
+                            int64_t q_token_stride, int64_t kv_token_stride, int num_q_heads,
+                            int num_kv_heads, int head_dim, int block_size, int max_blocks,
+                            int num_blocks, int dtype, int32_t* status_dev, cudaStream_t stream);
+
+/*
+ * pa_decode over the 8-bit cache: the same result definition over
+ * K = code * k_scale, V = code * v_scale, fp32 softmax and sums; out and q
+ * [num_seqs, num_q_heads, head_dim] fp16 or bf16.  max_seq_len, scale, bad lengths
+ * and empty sequences as in pa_decode; a bad block id's keys and values read as
+ * zeros (reported in checked mode).  workspace: at least
+ * pa_decode_q8_workspace_bytes(...) bytes (0 for invalid arguments), 256-byte
+ * aligned, contents arbitrary, not shared by calls that overlap on the GPU.
+ * Supported: fp16 / bf16, head_dim 64 or 128, block_size 8/16/32/64, num_q_heads a
+ * multiple of num_kv_heads.
+ */
+size_t pa_decode_q8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int max_seq_len);
+pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, const void* v_pool,
+                       const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                       const int32_t* seq_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                       int head_dim, int block_size, int max_blocks, int num_blocks,
+                       int max_seq_len, float scale, int dtype, void* workspace,
+                       size_t workspace_bytes, int32_t* status_dev, cudaStream_t stream);
+
+/*
+ * Blocks of the 8-bit cache back to 16 bits: for each pair (src, dst), block dst of
+ * the 16-bit pools ([dst_num_blocks, block_size, num_kv_heads, head_dim], dtype) =
+ * block src of the 8-bit cache, every row, code * scale rounded to the storage type
+ * (exact for bf16 and a power-of-two scale; saturated to the type's largest value).
+ * pa_prefill runs over an 8-bit prefix this way: its blocks are expanded into a
+ * staging pool of one layer.  block_pairs [num_pairs, 2] int32 in device memory; a
+ * block id out of range skips its pair (reported in checked mode); a dst that
+ * appears twice is a caller error.
+ */
+pa_status pa_expand_blocks_q8(void* k_pool, void* v_pool, const void* k_pool8, const void* v_pool8,
+                              const float* k_scale, const float* v_scale,
+                              const int32_t* block_pairs, int num_pairs, int num_kv_heads,
+                              int head_dim, int block_size, int src_num_blocks,
+                              int dst_num_blocks, int dtype, int32_t* status_dev,
+                              cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Host block manager                                                        */

@@ -10,6 +10,7 @@ Contents
                  blocks-needed / append / physical index) plus copy-on-write
   attention      fp64 decode attention over a paged KV pool
   cache_ops      byte-exact cache write (reshape_and_cache) and block copy
+  cache_q8       fp64 norm and rotation of new tokens, the 8-bit cache
   brute          pure-Python loops for tiny cases (math.exp, no numpy)
   scenarios      the decode workloads' pool layouts, built through the
                  block manager from a seed

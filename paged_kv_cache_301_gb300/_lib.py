@@ -53,6 +53,16 @@ SIGNATURES = {
     "pa_append_tokens": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_int, c_int64, c_int, c_int, c_int, c_int, c_int,
                                  c_int, c_void_p, c_void_p]),
+    "pa_rope_append": (c_int, [c_void_p] * 8 + [c_float, c_void_p, c_int, c_int, c_int] +
+                       [c_void_p] * 4 + [c_int, c_int, c_int64, c_int64] + [c_int] * 7 +
+                       [c_void_p, c_void_p]),
+    "pa_rope_append_q8": (c_int, [c_void_p] * 10 + [c_float, c_void_p, c_int, c_int, c_int] +
+                          [c_void_p] * 4 + [c_int, c_int, c_int64, c_int64] + [c_int] * 7 +
+                          [c_void_p, c_void_p]),
+    "pa_decode_q8_workspace_bytes": (c_size_t, [c_int] * 6),
+    "pa_decode_q8": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_float, c_int, c_void_p, c_size_t,
+                                                            c_void_p, c_void_p]),
+    "pa_expand_blocks_q8": (c_int, [c_void_p] * 7 + [c_int] * 7 + [c_void_p, c_void_p]),
     "pa_stream_read": (c_int, [c_void_p, c_size_t, c_void_p, c_void_p]),
     "pa_decode_slots": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                 c_void_p, c_void_p]),

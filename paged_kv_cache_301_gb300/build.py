@@ -30,6 +30,7 @@ SOURCES = [
     "pa_decode_tc.cu",
     "pa_decode_tcg.cu", "pa_blocks.cu", "pa_prefill_tc.cu", "pa_prefill_simt.cu",
     "pa_stream.cu",
+    "pa_rope.cu", "pa_decode_q8.cu", "pa_expand_q8.cu",
 ]
 HEADERS = [
     os.path.join(ROOT, "include", "pagedattn.h"),

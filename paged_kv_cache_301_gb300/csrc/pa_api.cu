@@ -70,7 +70,7 @@ extern "C" const char* pa_status_string(int status) {
   }
 }
 
-extern "C" int pa_version(void) { return 100; }
+extern "C" int pa_version(void) { return 200; }
 
 extern "C" size_t pa_decode_workspace_bytes(int num_seqs, int num_q_heads, int head_dim,
                                             int max_seq_len, int partition_tokens) {
