@@ -1,99 +1,956 @@
-// pa_decode_q8: decode attention over the 8-bit cache (pa_q8.cuh).
+// pa_decode_q8: decode attention over the 8-bit cache (pa_q8.cuh), on the
+// Blackwell tensor cores (tcgen05 + TMEM) with TMA loads.
 //
 //   out = sum_t p_t V_t / sum_t p_t,   p_t = 2^(s_t - m),
 //   s_t = log2(e) * scale * q . K_t,   K_t = code * k_scale[block][head], V_t alike
 //
-// The plain kernel: one CTA per (sequence, query head) walks the sequence 512
-// tokens at a time.  A thread takes a token's score, the CTA's threads share
-// the running maximum and sum, then a thread takes one element of the output.
+// Bound: the cache's bytes, 2 per (token, KV head, dim), over HBM bandwidth.  So
+// the codes go from HBM to shared memory to the tensor cores as they are, and
+// everything 16- or 32-bit is brought to them:
+//   - q is split into three e4m3 digits of four bits, q = s (d0 + d1/16 + d2/256)
+//     with s a power of two: 12 bits, which is all of bf16's 8 and fp16's 11;
+//   - the softmax weights, times the block's V scale over the largest V scale of
+//     the tile, are split the same way: 2^-12 of each weight (a single e4m3
+//     weight would be off by 2^-4), and 2^-26 of the largest.
+// Products of digits are exact and the sums are fp32.  K scales multiply the
+// finished scores.
+//
+// The cache rows are the M side of both products, so that the G query heads of a
+// KV head are columns and no row is wasted:
+//   S^T[128 x N] = K_tile[128 x 128 B] . Qdigits^T          (one column per digit and head)
+//   O^T[128 B x N] = V_tile^T . Pdigits^T
+// A tile is 128 rows of 128 bytes: 128 tokens at head_dim 128.  At head_dim 64 a
+// row is two tokens; the digits of q appear in two sets of columns, one with
+// zeros over the second half of the row and one over the first, and of O^T only
+// the quarter where token parity and column set agree is used.
+//
+// Work: the tiles of all (sequence, KV head, head chunk) items in a row, cut into
+// equal windows, one per CTA (two CTAs per SM).  An item that a window boundary
+// cuts leaves partial (m, l, acc) in the workspace; the combine kernel joins
+// them: M = max m, out = sum acc 2^(m - M) / sum l 2^(m - M).
+//
+// Roles (224 threads): warp 0 block ids and TMA; warp 1 TMEM and MMA issue; warp 2
+// q digits; warps 3-6 softmax and sums, one thread per tile row, then one per
+// row of O^T.  K and V tiles alternate in a ring of 16 KB stages.  Every wait is
+// bounded; one that runs out sets an abort flag, copies and MMAs in flight are
+// drained, TMEM is freed and PA_ERR_TIMEOUT is reported through status_dev.
 #include <math.h>
 #include <math_constants.h>
 
+#include <mutex>
+
 #include "pa_common.cuh"
+#include "pa_internal.h"
 #include "pa_q8.cuh"
+#include "pa_sm100.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kChunk = 512;
-constexpr int kThreads = 128;
+using namespace sm100;
 
-struct DecodeQ8Args {
+constexpr int kThreads = 224;
+constexpr int kTileRows = 128;
+constexpr int kStageBytes = kTileRows * 128;
+constexpr int kMaxGrid = 320;                  // CTAs at most (two per SM)
+constexpr uint64_t kLimitNs = 2000000000ull;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+struct Q8Args {
   void* out;
   const void* q;
-  const uint8_t* k_pool;
-  const uint8_t* v_pool;
   const float* k_scale;
   const float* v_scale;
   const int32_t* tables;
   const int32_t* lens;
   int B, Hq, H, bs, max_blocks, num_blocks, max_seq_len;
+  int chunks, hch;               // chunks of a KV head's query heads, heads per chunk
+  int rows_total;                // 128-byte rows of a pool
   float scale_log2;
+  int dtype;
+  int4* info;                    // [grid]: sequence, item of it, first tile, tiles
+  float* ws_m;                   // [2 grid, hch]
+  float* ws_l;
+  float* ws_acc;                 // [2 grid, hch, D]
   int32_t* status_dev;
 };
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) decode_q8_plain_kernel(const DecodeQ8Args a) {
-  __shared__ float s_q[D], s_p[kChunk], s_red[kThreads / 32];
+// Columns of one digit set: three digits of GP heads for each token of a row.
+template <int D, int GP>
+struct Shape {
+  static constexpr int kTpr = 128 / D;                         // tokens per row
+  static constexpr int kTokens = kTileRows * kTpr;             // tokens per tile
+  static constexpr int kUsed = 3 * GP * kTpr;
+  static constexpr int kN = (kUsed + 15) / 16 * 16;
+  static constexpr int kStages = kN <= 16 ? 6 : 5;             // two CTAs fit an SM
+  static constexpr uint32_t kCols = 4 * kN <= 64 ? 64 : (4 * kN <= 128 ? 128 : 256);
+  static constexpr int kOperand = kN * 128;                    // bytes of a digit operand
+  static constexpr int kQOff = kStages * kStageBytes;
+  static constexpr int kPOff = kQOff + 2 * kOperand;
+  static constexpr int kTailOff = kPOff + 2 * kOperand;
+};
+
+template <int D, int GP>
+struct Tail {
+  uint64_t full[6], empty[6];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], red_bar[2];
+  uint64_t sum_bar, drain;
+  float qscale[2][GP];
+  float red[2][4][GP + 1];       // per warp: heads' maxima, the largest V scale
+  float lred[4][GP];
+  float half[D == 64 ? GP * 64 : 1];   // the other parity's sums (head_dim 64)
+  int sums[kThreads];
+  int start[4];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <int D, int GP>
+constexpr int smem_bytes() {
+  return Shape<D, GP>::kTailOff + (int)sizeof(Tail<D, GP>) + 1024;   // + alignment slack
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int row,
+                                         uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(row), "l"(policy)
+      : "memory");
+}
+
+// The first C columns from t on of this warp's 32 lanes, rounded up to what is
+// loaded at once; loads and wait are one statement, so nothing reads them early.
+template <int C>
+__device__ __forceinline__ void load_cols(uint32_t t, float* v);
+
+template <>
+__device__ __forceinline__ void load_cols<4>(uint32_t t, float* v) {
+  uint32_t r[4];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(t)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <>
+__device__ __forceinline__ void load_cols<8>(uint32_t t, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7])
+      : "r"(t)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <>
+__device__ __forceinline__ void load_cols<16>(uint32_t t, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <>
+__device__ __forceinline__ void load_cols<24>(uint32_t t, float* v) {
+  uint32_t r[24];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%25];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23])
+      : "r"(t), "r"(t + 16)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 24; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <>
+__device__ __forceinline__ void load_cols<32>(uint32_t t, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <>
+__device__ __forceinline__ void load_cols<48>(uint32_t t, float* v) {
+  uint32_t r[48];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%48];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, [%49];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47])
+      : "r"(t), "r"(t + 32)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 48; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Columns loaded for n used ones.
+constexpr int cols_for(int n) {
+  return n <= 4 ? 4 : (n <= 8 ? 8 : (n <= 16 ? 16 : (n <= 24 ? 24 : (n <= 32 ? 32 : 48))));
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The three digits of x (|x| <= 448): x = d0 + d1 / 16 + d2 / 256 up to 2^-12 |x|
+// or 2^-18.  For two values at once; digit i of the first in byte 0 of d[i].
+__device__ __forceinline__ void digits2(float x, float y, uint32_t (&d)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    d[i] = e4m3x2(x, y);
+    if (i < 2) {
+      const float2 v = e4m3_widen2(d[i]);
+      x = (x - v.x) * 16.f;
+      y = (y - v.y) * 16.f;
+    }
+  }
+}
+
+// Byte `col` of row n of a K-major operand with 128-byte rows and 128-byte swizzle.
+__device__ __forceinline__ int swizzled(int n, int col) {
+  return n * 128 + (((col >> 4) ^ (n & 7)) << 4) + (col & 15);
+}
+
+__device__ __forceinline__ int clamp_len(const Q8Args& a, int b) {
+  return max(0, min(a.lens[b], a.max_seq_len));
+}
+
+// Walks a window's tiles in order: sequences, then their items (KV head and head
+// chunk), then tiles.
+template <int TOKENS>
+struct Walk {
+  int b, L, nt, item, j, left;
+
+  __device__ __forceinline__ void next(const Q8Args& a, int items) {
+    --left;
+    if (++j < nt) return;
+    j = 0;
+    if (++item < items) return;
+    item = 0;
+    do {
+      ++b;
+      L = b < a.B && left > 0 ? clamp_len(a, b) : 0;
+      nt = (L + TOKENS - 1) / TOKENS;
+    } while (nt == 0 && left > 0 && b < a.B);
+    if (nt == 0) left = 0;
+  }
+};
+
+template <int D, int GP>
+__global__ void __launch_bounds__(kThreads, 2)
+decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const Q8Args a) {
+  using S = Shape<D, GP>;
+  constexpr int TPR = S::kTpr, TOKENS = S::kTokens, N = S::kN, R = S::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Tail<D, GP>* tail = reinterpret_cast<Tail<D, GP>*>(smem + S::kTailOff);
+  volatile int* abort_flag = &tail->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int items = a.H * a.chunks, G = a.Hq / a.H;
+
+  allow_next_grid();
+  if (tid == 0) {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&tail->full[i], 1);
+      mbar_init(&tail->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tail->q_full[i], 1);
+      mbar_init(&tail->q_empty[i], 5);       // MMA + four softmax warps
+      mbar_init(&tail->s_full[i], 1);
+      mbar_init(&tail->p_full[i], 4);
+      mbar_init(&tail->o_full[i], 1);
+      mbar_init(&tail->red_bar[i], 4);
+    }
+    mbar_init(&tail->sum_bar, 4);
+    mbar_init(&tail->drain, 1);
+    tail->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tail->tmem, S::kCols);
+    tmem_relinquish();
+  }
+  // digit operands: columns that no head uses, and the halves that stay zero
+  for (int i = tid; i < 4 * S::kOperand / 16; i += kThreads)
+    reinterpret_cast<uint4*>(smem + S::kQOff)[i] = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
+  wait_prior_grid();
+
+  // this CTA's window of the tiles of all items
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += (clamp_len(a, b) + TOKENS - 1) / TOKENS;
+  tail->sums[tid] = mine;
+  if (tid < 4) tail->start[tid] = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {                            // exclusive scan, seven entries a lane
+    constexpr int E = kThreads / 32;
+    int v[E], sum = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      v[i] = sum;
+      sum += tail->sums[lane * E + i];
+    }
+    int scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(kAll, scan, o);
+      if (lane >= o) scan += up;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) tail->sums[lane * E + i] = scan - sum + v[i];
+    if (lane == 31) tail->start[3] = scan;
+  }
+  __syncthreads();
+  const int64_t work = (int64_t)tail->start[3] * items;
+  const int64_t ctas = work < (int64_t)gridDim.x ? work : (int64_t)gridDim.x;
+  const bool in = (int64_t)blockIdx.x < ctas;
+  const int64_t w0 = in ? work * blockIdx.x / ctas : 0;
+  const int64_t w1 = in ? work * (blockIdx.x + 1) / ctas : 0;
+  if (in) {
+    const int t = (int)(w0 / items), before = tail->sums[tid];
+    if (before <= t && t < before + mine) {
+      int b = b0, sum = before, nt = 0;
+      for (;; ++b) {
+        nt = (clamp_len(a, b) + TOKENS - 1) / TOKENS;
+        if (t < sum + nt || b + 1 >= b1) break;
+        sum += nt;
+      }
+      const int at = (int)(w0 - (int64_t)sum * items);
+      tail->start[0] = b;
+      tail->start[1] = at / nt;
+      tail->start[2] = at - at / nt * nt;
+    }
+  }
+  __syncthreads();
+  Walk<TOKENS> walk;
+  walk.b = tail->start[0];
+  walk.item = tail->start[1];
+  walk.j = tail->start[2];
+  walk.left = (int)(w1 - w0);
+  walk.L = in ? clamp_len(a, walk.b) : 0;
+  walk.nt = (walk.L + TOKENS - 1) / TOKENS;
+  if (tid == 0) a.info[blockIdx.x] = make_int4(walk.b, walk.item, walk.j, walk.left);
+  // lengths out of range are reported; empty sequences get zero rows
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const int L = a.lens[b];
+    if ((L < 0 || L > a.max_seq_len) && tid == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+    if (L <= 0 || a.max_seq_len == 0) {
+      uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (int64_t)b * a.Hq * D);
+      for (int i = tid; i < a.Hq * (D / 8); i += kThreads) row[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  const uint32_t tmem = tail->tmem;
+  const uint32_t ring = smem_addr(smem), qb = smem_addr(smem + S::kQOff),
+                 pb = smem_addr(smem + S::kPOff);
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ block ids, TMA --
+    const uint64_t policy = policy_evict_first();
+    const int per_tile = TOKENS / a.bs, block_rows = a.bs / TPR;
+    int stage = 0, phase = 0, used = 0;
+    // a lane's block of the tile that w stands at
+    auto block_of = [&](const Walk<TOKENS>& w) -> int {
+      if (w.left <= 0 || w.j * TOKENS + lane * a.bs >= w.L || lane >= per_tile) return -1;
+      return a.tables[(int64_t)w.b * a.max_blocks + w.j * per_tile + lane];
+    };
+    int id = block_of(walk);
+    while (walk.left > 0) {
+      const int n = min(TOKENS, walk.L - walk.j * TOKENS);
+      const int nb = (n + a.bs - 1) / a.bs;
+      const int h = walk.item / a.chunks;
+      int row = a.rows_total;                   // outside the pool: the copy reads zeros
+      if (lane < nb) {
+        if (id >= 0 && id < a.num_blocks) row = (id * a.H + h) * block_rows;
+        else report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+      }
+      walk.next(a, items);
+      id = block_of(walk);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (lane == 0) {
+          ok = mbar_wait(&tail->empty[stage], phase ^ 1, abort_flag, kLimitNs);
+          if (ok) mbar_arrive_expect_tx(&tail->full[stage], (uint32_t)(nb * block_rows * 128));
+        }
+        ok = __shfl_sync(kAll, (int)ok, 0) != 0;
+        if (!ok) break;
+        if (lane < nb)
+          tma_rows(smem + stage * kStageBytes + lane * block_rows * 128, kv ? &map_v : &map_k,
+                   &tail->full[stage], row, policy);
+        ++used;
+        if (++stage == R) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      report(a.status_dev, PA_ERR_TIMEOUT);
+    }
+    if (*abort_flag && lane == 0) {             // copies in flight land before the CTA ends
+      for (int i = max(0, used - R); i < used; ++i)
+        mbar_wait_drain(&tail->full[i % R], (i / R) & 1, kLimitNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issue --
+    constexpr uint32_t idesc_s = idesc_f16(0, 0, 0, kTileRows, N);    // e4m3, K-major x K-major
+    constexpr uint32_t idesc_o = idesc_f16(0, 1, 0, 128, N);          // V MN-major
+    if (lane == 0) {
+      int use = 0, t = 0, seg = 0;              // ring uses, tiles, segments so far
+      int pv = -1;                              // tile whose P . V is still to be issued
+      bool fresh = true;
+      auto wait_ring = [&](int u) {
+        return mbar_wait(&tail->full[u % R], (u / R) & 1, abort_flag, kLimitNs);
+      };
+      auto issue_pv = [&](int p) -> bool {
+        const int u = 2 * p + 1, slot = p & 1;
+        if (!wait_ring(u)) return false;
+        if (!mbar_wait(&tail->p_full[slot], (p >> 1) & 1, abort_flag, kLimitNs)) return false;
+        tc_fence_after();
+        const uint32_t va = ring + (u % R) * kStageBytes, pa_ = pb + slot * S::kOperand;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f8(tmem + (2 + slot) * N, smem_desc_sw128(va + k * 32 * 128, kStageBytes, 1024),
+                 smem_desc_sw128(pa_ + k * 32, 16, 1024), idesc_o, k > 0);
+        mma_commit(&tail->empty[u % R]);
+        mma_commit(&tail->o_full[slot]);
+        return true;
+      };
+      while (walk.left > 0 && ok) {
+        const int slot = t & 1, qs = seg & 1;
+        // whichever is ready first: the last tile's P . V, or this tile's K
+        const uint64_t t0 = globaltimer();
+        for (int spin = 0;; ++spin) {
+          if (pv >= 0 && mbar_test(&tail->p_full[pv & 1], (pv >> 1) & 1) &&
+              mbar_test(&tail->full[(2 * pv + 1) % R], ((2 * pv + 1) / R) & 1)) {
+            ok = issue_pv(pv);
+            pv = -1;
+          }
+          if (!ok) break;
+          if ((!fresh || mbar_test(&tail->q_full[qs], (seg >> 1) & 1)) &&
+              mbar_test(&tail->full[use % R], (use / R) & 1))
+            break;
+          if (*abort_flag || ((spin & 63) == 63 && globaltimer() - t0 > kLimitNs)) {
+            ok = false;
+            break;
+          }
+        }
+        if (!ok) break;
+        // head_dim 64, an odd end: the last row's second token is no token, and 0 times
+        // whatever stands there has to be 0
+        if (TPR == 2) {
+          const int n = walk.L - walk.j * TOKENS;
+          if (n < TOKENS && (n & 1)) {
+            uint8_t* kt = smem + (use % R) * kStageBytes;
+#pragma unroll
+            for (int c = 64; c < 128; c += 16)
+              *reinterpret_cast<uint4*>(kt + swizzled(n >> 1, c)) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+          }
+        }
+        tc_fence_after();
+        const uint32_t ka = ring + (use % R) * kStageBytes, qa = qb + qs * S::kOperand;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f8(tmem + slot * N, smem_desc_sw128(ka + k * 32, 16, 1024),
+                 smem_desc_sw128(qa + k * 32, 16, 1024), idesc_s, k > 0);
+        mma_commit(&tail->empty[use % R]);
+        mma_commit(&tail->s_full[slot]);
+        fresh = walk.j + 1 == walk.nt || walk.left == 1;       // a segment ends here
+        if (fresh) {
+          mma_commit(&tail->q_empty[qs]);
+          ++seg;
+        }
+        if (pv >= 0) ok = issue_pv(pv);
+        pv = t++;
+        use += 2;
+        walk.next(a, items);
+      }
+      if (ok && pv >= 0) ok = issue_pv(pv);
+      if (!ok) {
+        *abort_flag = 1;
+        report(a.status_dev, PA_ERR_TIMEOUT);
+      }
+      if (*abort_flag && t > 0) {               // MMAs in flight end before TMEM is freed
+        mma_commit(&tail->drain);
+        mbar_wait_drain(&tail->drain, 0, kLimitNs);
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------- q digits --
+    constexpr int E = D / 32;                   // elements of a lane
+    int seg = 0;
+    while (walk.left > 0) {
+      const int slot = seg & 1;
+      if (!__all_sync(kAll, mbar_wait(&tail->q_empty[slot], ((seg >> 1) & 1) ^ 1, abort_flag,
+                                      kLimitNs))) {
+        ok = false;
+        break;
+      }
+      const int h = walk.item / a.chunks, g0 = (walk.item - h * a.chunks) * a.hch;
+      const int gn = min(a.hch, G - g0);
+      uint8_t* op = smem + S::kQOff + slot * S::kOperand;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) +
+                          ((int64_t)walk.b * a.Hq + h * G + g0) * (D / 2) + lane * (E / 2);
+      for (int g = 0; g < gn; ++g) {
+        float x[E];
+        float m = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const uint32_t w = q[g * (D / 2) + e];
+          const float2 v =
+              a.dtype == PA_BFLOAT16 ? widen2<PA_BFLOAT16>(w) : widen2<PA_FLOAT16>(w);
+          x[2 * e] = v.x;
+          x[2 * e + 1] = v.y;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          m = fmaxf(m, finite_mag(x[e]));
+          bad |= !(fabsf(x[e]) < CUDART_INF_F);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        bad = __any_sync(kAll, bad);
+        const float s = scale_for(m), inv = 1.f / s;
+        uint32_t d[3], d2[3] = {0, 0, 0};
+        digits2(x[0] * inv, x[1] * inv, d);
+        if (E == 4) digits2(x[E - 2] * inv, x[E - 1] * inv, d2);
+#pragma unroll
+        for (int v = 0; v < TPR; ++v)
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int at = swizzled((v * 3 + i) * GP + g, v * D + lane * E);
+            if (E == 4) *reinterpret_cast<uint32_t*>(op + at) = d[i] | (d2[i] << 16);
+            else *reinterpret_cast<uint16_t*>(op + at) = (uint16_t)d[i];
+          }
+        // a row with an infinity or a NaN has no finite scores
+        if (lane == 0) tail->qscale[slot][g] = bad ? CUDART_NAN_F : s * a.scale_log2;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->q_full[slot]);
+      ++seg;
+      // on to the next segment
+      const int skip = min(walk.nt - walk.j, walk.left) - 1;
+      walk.j += skip;
+      walk.left -= skip;
+      walk.next(a, items);
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      report(a.status_dev, PA_ERR_TIMEOUT);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and sums --
+    const int wq = warp & 3;                    // TMEM lane quarter of this warp
+    const int r = wq * 32 + lane;               // tile row; then row of O^T
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const int par = r / D;                      // head_dim 64: the token parity of this O^T row
+    int t = 0, seg = 0, sums = 0;
+    auto wait_all = [&](uint64_t* bar, int parity) -> bool {
+      return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kLimitNs));
+    };
+    // the scales of this row's block in the tile that w stands at
+    auto scales_of = [&](const Walk<TOKENS>& w, float& ks, float& vs) {
+      ks = vs = 0.f;
+      const int tok = w.j * TOKENS + r * TPR;
+      if (w.left <= 0 || tok >= w.L) return;
+      const int id = a.tables[(int64_t)w.b * a.max_blocks + tok / a.bs];
+      if (id < 0 || id >= a.num_blocks) return;
+      const int64_t at = (int64_t)id * a.H + w.item / a.chunks;
+      ks = a.k_scale[at];
+      vs = a.v_scale[at];
+    };
+    float ks, vs;
+    scales_of(walk, ks, vs);
+    float m[GP], l[GP], acc[GP], alpha[GP], unit = 0.f;   // alpha, unit: of the tile before
+    // acc <- acc 2^(m_before - m) + O_t, with tile t's factors
+    auto add_tile = [&](int tile) -> bool {
+      const int slot = tile & 1;
+      if (!wait_all(&tail->o_full[slot], (tile >> 1) & 1)) return false;
+      tc_fence_after();
+      float o[cols_for(3 * GP)];
+      load_cols<cols_for(3 * GP)>(tmem + lanes + (2 + slot) * N + par * 3 * GP, o);
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float sum = fmaf(o[2 * GP + g], 1.f / 256.f, fmaf(o[GP + g], 1.f / 16.f, o[g]));
+        acc[g] = fmaf(sum, unit, acc[g] * alpha[g]);
+      }
+      return true;
+    };
+    int j0 = 0;                                 // first tile of the segment
+    bool fresh = true;
+    while (walk.left > 0) {
+      const int slot = t & 1, qs = seg & 1;
+      if (fresh) {
+        if (!wait_all(&tail->q_full[qs], (seg >> 1) & 1)) { ok = false; break; }
+        j0 = walk.j;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          m[g] = -CUDART_INF_F;
+          l[g] = acc[g] = 0.f;
+        }
+      }
+      const Walk<TOKENS> at = walk;
+      const int n = at.L - at.j * TOKENS;       // tokens left from this tile on
+      const bool ends = at.j + 1 == at.nt || at.left == 1;
+      const float ksc = ks, vsc = vs;
+      walk.next(a, items);
+      scales_of(walk, ks, vs);
+
+      if (!wait_all(&tail->s_full[slot], (t >> 1) & 1)) { ok = false; break; }
+      tc_fence_after();
+      float x[TPR][GP];
+      {
+        float s[cols_for(S::kUsed)];
+        load_cols<cols_for(S::kUsed)>(tmem + lanes + slot * N, s);
+#pragma unroll
+        for (int v = 0; v < TPR; ++v)
+#pragma unroll
+          for (int g = 0; g < GP; ++g) {
+            const float* d = s + v * 3 * GP + g;
+            const float sum = fmaf(d[2 * GP], 1.f / 256.f, fmaf(d[GP], 1.f / 16.f, d[0]));
+            // rows behind the end hold anything
+            x[v][g] = r * TPR + v < n ? sum * (tail->qscale[qs][g] * ksc) : -CUDART_INF_F;
+          }
+      }
+      // the tile's maxima over its rows
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float w = warp_max(TPR == 2 ? fmaxf(x[0][g], x[TPR - 1][g]) : x[0][g]);
+        if (lane == g) tail->red[slot][wq][g] = w;
+      }
+      const float wv = warp_max(vsc);
+      if (lane == 0) tail->red[slot][wq][GP] = wv;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->red_bar[slot]);
+      if (!wait_all(&tail->red_bar[slot], (t >> 1) & 1)) { ok = false; break; }
+      float p[TPR][GP], alpha_t[GP];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float top = fmaxf(fmaxf(tail->red[slot][0][g], tail->red[slot][1][g]),
+                                fmaxf(tail->red[slot][2][g], tail->red[slot][3][g]));
+        const float m_new = fmaxf(m[g], top);
+        alpha_t[g] = ex2_approx(m[g] - m_new);
+        m[g] = m_new;
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < TPR; ++v) {
+          p[v][g] = r * TPR + v < n ? ex2_approx(x[v][g] - m_new) : 0.f;
+          sum += p[v][g];
+        }
+        l[g] = fmaf(l[g], alpha_t[g], sum);
+      }
+      // weights in units of the tile's largest V scale, 256 at most
+      const float vmax = fmaxf(fmaxf(tail->red[slot][0][GP], tail->red[slot][1][GP]),
+                               fmaxf(tail->red[slot][2][GP], tail->red[slot][3][GP]));
+      const float to = vmax > 0.f ? vsc * (256.f / vmax) : 0.f;
+      uint8_t* op = smem + S::kPOff + slot * S::kOperand;
+#pragma unroll
+      for (int v = 0; v < TPR; ++v)
+#pragma unroll
+        for (int g = 0; g < GP; g += 2) {
+          uint32_t d[3];
+          digits2(p[v][g] * to, g + 1 < GP ? p[v][g + 1 < GP ? g + 1 : g] * to : 0.f, d);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int row = (v * 3 + i) * GP + g;
+            op[swizzled(row, r)] = (uint8_t)d[i];
+            if (g + 1 < GP) op[swizzled(row + 1, r)] = (uint8_t)(d[i] >> 8);
+          }
+        }
+      // tokens behind the end: zero their V, so that 0 times garbage stays 0
+      if (n < TOKENS) {
+        const int u = 2 * t + 1;
+        if (!wait_all(&tail->full[u % R], (u / R) & 1)) { ok = false; break; }
+        uint8_t* vt = smem + (u % R) * kStageBytes;
+#pragma unroll
+        for (int v = 0; v < TPR; ++v)
+          if (r * TPR + v >= n) {
+#pragma unroll
+            for (int c = 0; c < D; c += 16)
+              *reinterpret_cast<uint4*>(vt + swizzled(r, v * D + c)) = make_uint4(0, 0, 0, 0);
+          }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->p_full[slot]);
+      if (!fresh && !add_tile(t - 1)) { ok = false; break; }
+#pragma unroll
+      for (int g = 0; g < GP; ++g) alpha[g] = alpha_t[g];
+      unit = vmax * (1.f / 256.f);
+      fresh = ends;
+      if (ends) {
+        if (!add_tile(t)) { ok = false; break; }
+        tc_fence_before();
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          float sum = l[g];
+#pragma unroll
+          for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+          if (lane == g) tail->lred[wq][g] = sum;
+          if (D == 64 && par == 1) tail->half[g * 64 + r - 64] = acc[g];
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&tail->q_empty[qs]);
+          mbar_arrive(&tail->sum_bar);
+        }
+        if (!wait_all(&tail->sum_bar, sums & 1)) { ok = false; break; }
+        ++sums;
+        const int h = at.item / a.chunks, g0 = (at.item - h * a.chunks) * a.hch;
+        const int gn = min(a.hch, G - g0);
+        const bool whole = j0 == 0 && at.j + 1 == at.nt;
+        if (r < D) {
+          const int64_t row0 = (int64_t)at.b * a.Hq + h * G + g0;
+          const int64_t part = (2 * (int64_t)blockIdx.x + (seg > 0)) * a.hch;
+#pragma unroll
+          for (int g = 0; g < GP; ++g) {
+            if (g >= gn) continue;
+            const float sum = (tail->lred[0][g] + tail->lred[1][g]) +
+                              (tail->lred[2][g] + tail->lred[3][g]);
+            const float o = acc[g] + (D == 64 ? tail->half[g * 64 + (r & 63)] : 0.f);
+            if (whole) {
+              const float y = o / sum;
+              static_cast<uint16_t*>(a.out)[(row0 + g) * D + r] =
+                  a.dtype == PA_BFLOAT16 ? narrow<PA_BFLOAT16>(y) : narrow<PA_FLOAT16>(y);
+            } else {
+              a.ws_acc[(part + g) * D + r] = o;
+              if (r == 0) {
+                a.ws_m[part + g] = m[g];
+                a.ws_l[part + g] = sum;
+              }
+            }
+          }
+        }
+        // lred and half are written again only after the next segment's first
+        // red_bar, which every warp reaches behind these reads
+        ++seg;
+      }
+      ++t;
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) report(a.status_dev, PA_ERR_TIMEOUT);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kCols);
+  }
+}
+
+// Joins the partials of items that window boundaries cut: CTA c looks at the
+// boundary where window c begins, and joins its item if that boundary is the
+// item's first.  Threads are elements of a head, kJoinThreads / D heads at a time.
+constexpr int kJoinThreads = 512;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, int windows) {
   allow_next_grid();
   wait_prior_grid();
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, h = hq / (a.Hq / a.H);
-  const int tid = threadIdx.x;
-  const int raw = a.lens[b];
-  const int L = max(0, min(raw, a.max_seq_len));
-  if (L != raw && tid == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-  const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)blockIdx.x * D;
-  for (int d = tid; d < D; d += kThreads) s_q[d] = widen2<DT>(q[d]).x * a.scale_log2;
-  __syncthreads();
-  float m = -CUDART_INF_F, l = 0.f, acc = 0.f;
-  for (int t0 = 0; t0 < L; t0 += kChunk) {
-    const int n = min(kChunk, L - t0);
-    float top = -CUDART_INF_F;
-    for (int i = tid; i < n; i += kThreads) {
-      const int t = t0 + i;
-      const int32_t blk = a.tables[(int64_t)b * a.max_blocks + t / a.bs];
-      float s = 0.f;
-      if (blk >= 0 && blk < a.num_blocks) {
-        const int64_t tile = (int64_t)blk * a.H + h;
-        const uint32_t* k =
-            reinterpret_cast<const uint32_t*>(a.k_pool + (tile * a.bs + t % a.bs) * D);
-        for (int d = 0; d < D / 4; ++d) {
-          const uint32_t w = k[d];
-          const float2 x = e4m3_widen2(w), y = e4m3_widen2(w >> 16);
-          s += s_q[4 * d] * x.x + s_q[4 * d + 1] * x.y + s_q[4 * d + 2] * y.x +
-               s_q[4 * d + 3] * y.y;
-        }
-        s *= a.k_scale[tile];
-      } else {
-        report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-      }
-      s_p[i] = s;
-      top = fmaxf(top, s);
-    }
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if ((tid & 31) == 0) s_red[tid >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, s_red[w]);
-    const float m_new = fmaxf(m, top), alpha = exp2f(m - m_new);
-    m = m_new;
-    l *= alpha;
-    acc *= alpha;
-    for (int i = 0; i < n; ++i) {
-      const int t = t0 + i;
-      const float p = exp2f(s_p[i] - m);
-      l += p;
-      const int32_t blk = a.tables[(int64_t)b * a.max_blocks + t / a.bs];
-      if (tid < D && blk >= 0 && blk < a.num_blocks) {
-        const int64_t tile = (int64_t)blk * a.H + h;
-        const float v = e4m3_widen2(a.v_pool[(tile * a.bs + t % a.bs) * D + tid]).x;
-        acc += p * (v * a.v_scale[tile]);
-      }
-    }
-    __syncthreads();
+  const int c = (int)blockIdx.x + 1;
+  const int4 at = a.info[c];                   // sequence, item, first tile, tiles
+  if (at.w <= 0 || at.z == 0) return;          // an empty window, or a boundary between items
+  const int4 before = a.info[c - 1];
+  const bool same = before.x == at.x && before.y == at.y;
+  if (same && before.z > 0) return;            // an earlier boundary cuts this item
+  // the parts: the segment of window c - 1 that ends there, then the first segment of
+  // windows c, c + 1, ... as long as they begin inside the item
+  int last = c;
+  while (last + 1 < windows) {
+    const int4 next = a.info[last + 1];
+    if (next.w <= 0 || next.z == 0 || next.x != at.x || next.y != at.y) break;
+    ++last;
   }
-  if (tid < D)
-    static_cast<uint16_t*>(a.out)[(int64_t)blockIdx.x * D + tid] =
-        narrow<DT>(L == 0 ? 0.f : acc / l);
+  const int h = at.y / a.chunks, G = a.Hq / a.H, g0 = (at.y - h * a.chunks) * a.hch;
+  const int gn = min(a.hch, G - g0);
+  const int64_t head = 2 * (int64_t)(c - 1) + (same ? 0 : 1);
+  const int d = threadIdx.x % D;
+  for (int g = threadIdx.x / D; g < gn; g += kJoinThreads / D) {
+    const int64_t p0 = head * a.hch + g;
+    float top = a.ws_m[p0];
+    for (int k = c; k <= last; ++k) top = fmaxf(top, a.ws_m[2 * (int64_t)k * a.hch + g]);
+    float w = ex2_approx(a.ws_m[p0] - top);
+    float l = w * a.ws_l[p0], o = w * a.ws_acc[p0 * D + d];
+#pragma unroll 4
+    for (int k = c; k <= last; ++k) {
+      const int64_t p = 2 * (int64_t)k * a.hch + g;
+      w = ex2_approx(a.ws_m[p] - top);
+      l = fmaf(w, a.ws_l[p], l);
+      o = fmaf(w, a.ws_acc[p * D + d], o);
+    }
+    const float y = o / l;
+    static_cast<uint16_t*>(a.out)[((int64_t)at.x * a.Hq + h * G + g0 + g) * D + d] =
+        a.dtype == PA_BFLOAT16 ? narrow<PA_BFLOAT16>(y) : narrow<PA_FLOAT16>(y);
+  }
+}
+
+// ------------------------------------------------------------------ host side --
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                         cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// A pool as rows of 128 bytes; a box is one block of one head.
+bool encode_pool(CUtensorMap* map, const void* pool, int64_t rows, int block_rows) {
+  const cuuint64_t dims[2] = {128, (cuuint64_t)rows}, strides[1] = {128};
+  const cuuint32_t box[2] = {128, (cuuint32_t)block_rows}, ones[2] = {1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides,
+                     box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+  int chunks, hch;               // of a KV head's query heads
+  int64_t tiles;                 // of the longest sequence allowed
+  size_t m_off, l_off, acc_off, total;
+};
+
+Plan plan_of(int Hq, int H, int D, int max_seq_len) {
+  Plan p;
+  const int G = Hq / H, most = D == 128 ? 16 : 8;
+  p.chunks = (G + most - 1) / most;
+  p.hch = (G + p.chunks - 1) / p.chunks;
+  const int tokens = kTileRows * 128 / D;
+  p.tiles = ((int64_t)max_seq_len + tokens - 1) / tokens;
+  auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const size_t rows = (size_t)2 * kMaxGrid * p.hch;
+  p.m_off = align(kMaxGrid * sizeof(int4));
+  p.l_off = p.m_off + align(rows * sizeof(float));
+  p.acc_off = p.l_off + align(rows * sizeof(float));
+  p.total = p.acc_off + align(rows * D * sizeof(float));
+  return p;
+}
+
+template <int D, int GP>
+cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const Q8Args& a, int grid,
+                          int device, cudaStream_t stream) {
+  constexpr int bytes = smem_bytes<D, GP>();
+  static_assert(2 * (bytes + 1024) <= 233472, "two CTAs fit an SM");
+  static std::mutex lock;
+  static uint64_t done = 0;                    // devices whose attribute is set
+  {
+    std::lock_guard<std::mutex> hold(lock);
+    if (device >= 64 || !(done >> device & 1)) {
+      const cudaError_t e = cudaFuncSetAttribute(
+          decode_q8_kernel<D, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != cudaSuccess) return e;
+      if (device < 64) done |= 1ull << device;
+    }
+  }
+  return launch_pdl(decode_q8_kernel<D, GP>, dim3((unsigned)grid), kThreads, bytes, stream, k, v,
+                    a);
+}
+
+template <int D>
+cudaError_t launch_heads(const CUtensorMap& k, const CUtensorMap& v, const Q8Args& a, int grid,
+                         int device, cudaStream_t stream) {
+  if (a.hch <= 1) return launch_decode<D, 1>(k, v, a, grid, device, stream);
+  if (a.hch <= 2) return launch_decode<D, 2>(k, v, a, grid, device, stream);
+  if (a.hch <= 4) return launch_decode<D, 4>(k, v, a, grid, device, stream);
+  if (a.hch <= 5) return launch_decode<D, 5>(k, v, a, grid, device, stream);
+  if (D == 64 || a.hch <= 8) return launch_decode<D, 8>(k, v, a, grid, device, stream);
+  return launch_decode<128, 16>(k, v, a, grid, device, stream);
 }
 
 }  // namespace
@@ -117,7 +974,7 @@ extern "C" size_t pa_decode_q8_workspace_bytes(int num_seqs, int num_q_heads, in
                                                int head_dim, int block_size, int max_seq_len) {
   if (check_q8(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len) != PA_OK)
     return 0;
-  return 256;
+  return plan_of(num_q_heads, num_kv_heads, head_dim, max_seq_len).total;
 }
 
 extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -140,25 +997,62 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   if ((((uintptr_t)out | (uintptr_t)q | (uintptr_t)k_pool | (uintptr_t)v_pool) & 15u) != 0 ||
       (((uintptr_t)k_scale | (uintptr_t)v_scale) & 3u) != 0)
     return PA_ERR_INVALID_ARG;
-  if (!workspace || ((uintptr_t)workspace & 255u) ||
-      workspace_bytes < pa_decode_q8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                                     block_size, max_seq_len))
+  const Plan p = plan_of(num_q_heads, num_kv_heads, head_dim, max_seq_len);
+  if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.total)
     return PA_ERR_WORKSPACE;
-  const long long rows = (long long)num_seqs * num_q_heads;
-  if (rows > 0x7FFFFFFF) return PA_ERR_INVALID_ARG;
-  const DecodeQ8Args a = {out, q, (const uint8_t*)k_pool, (const uint8_t*)v_pool, k_scale, v_scale,
-                          block_tables, seq_lens, num_seqs, num_q_heads, num_kv_heads, block_size,
-                          max_blocks, num_blocks, max_seq_len,
-                          (float)((double)scale * 1.4426950408889634), status_dev};
-  const dim3 grid((unsigned)rows);
-  cudaError_t e;
-  if (dtype == PA_BFLOAT16)
+  // 32-bit tile counts, rows and grid
+  const int block_rows = block_size * head_dim / 128;
+  const long long rows = (long long)num_blocks * num_kv_heads * block_rows;
+  if (rows >= (1ll << 31) || (long long)num_seqs * p.tiles >= (1ll << 31) ||
+      (long long)num_kv_heads * p.chunks >= (1ll << 20) ||
+      p.tiles * num_kv_heads * p.chunks >= (1ll << 31))
+    return PA_ERR_INVALID_ARG;
+  int device = 0, sms = 0;
+  if (!encode_fn() || cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return PA_ERR_CUDA;
+  CUtensorMap k, v;
+  if (!encode_pool(&k, k_pool, rows, block_rows) || !encode_pool(&v, v_pool, rows, block_rows))
+    return PA_ERR_INVALID_ARG;
+
+  Q8Args a;
+  a.out = out;
+  a.q = q;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.tables = block_tables;
+  a.lens = seq_lens;
+  a.B = num_seqs;
+  a.Hq = num_q_heads;
+  a.H = num_kv_heads;
+  a.bs = block_size;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.max_seq_len = max_seq_len;
+  a.chunks = p.chunks;
+  a.hch = p.hch;
+  a.rows_total = (int)rows;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.dtype = dtype;
+  char* ws = static_cast<char*>(workspace);
+  a.info = reinterpret_cast<int4*>(ws);
+  a.ws_m = reinterpret_cast<float*>(ws + p.m_off);
+  a.ws_l = reinterpret_cast<float*>(ws + p.l_off);
+  a.ws_acc = reinterpret_cast<float*>(ws + p.acc_off);
+  a.status_dev = status_dev;
+
+  const long long work = (long long)num_seqs * p.tiles * num_kv_heads * p.chunks;
+  const long long ctas = 2ll * sms < kMaxGrid ? 2ll * sms : kMaxGrid;
+  const int grid = (int)(work < 1 ? 1 : (work < ctas ? work : ctas));
+  if (work / grid >= (1ll << 31)) return PA_ERR_INVALID_ARG;
+  cudaError_t e = head_dim == 128 ? launch_heads<128>(k, v, a, grid, device, stream)
+                                  : launch_heads<64>(k, v, a, grid, device, stream);
+  // an item of one tile is never cut
+  if (e == cudaSuccess && p.tiles > 1 && grid > 1) {
+    const dim3 joins((unsigned)(grid - 1));
     e = head_dim == 128
-            ? launch_pdl(decode_q8_plain_kernel<PA_BFLOAT16, 128>, grid, kThreads, 0, stream, a)
-            : launch_pdl(decode_q8_plain_kernel<PA_BFLOAT16, 64>, grid, kThreads, 0, stream, a);
-  else
-    e = head_dim == 128
-            ? launch_pdl(decode_q8_plain_kernel<PA_FLOAT16, 128>, grid, kThreads, 0, stream, a)
-            : launch_pdl(decode_q8_plain_kernel<PA_FLOAT16, 64>, grid, kThreads, 0, stream, a);
+            ? launch_pdl(join_q8_kernel<128>, joins, kJoinThreads, 0, stream, a, grid)
+            : launch_pdl(join_q8_kernel<64>, joins, kJoinThreads, 0, stream, a, grid);
+  }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -61,10 +61,10 @@ __global__ void __launch_bounds__(kExpandThreads) expand_q8_kernel(const ExpandA
     if (i < a.vecs) {
       const int d = i % RV, rh = i / RV, h = rh % a.H, row = rh / a.H;
       const int64_t at = from + (int64_t)(h * a.bs + row) * RV + d;
-      w[u][0] = __ldg(a.k8 + at);
-      w[u][1] = __ldg(a.v8 + at);
-      s[u][0] = __ldg(a.k_scale + (int64_t)src * a.H + h);
-      s[u][1] = __ldg(a.v_scale + (int64_t)src * a.H + h);
+      w[u][0] = a.k8[at];
+      w[u][1] = a.v8[at];
+      s[u][0] = a.k_scale[(int64_t)src * a.H + h];
+      s[u][1] = a.v_scale[(int64_t)src * a.H + h];
     }
   }
 #pragma unroll

@@ -129,15 +129,15 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], bool any_norm, const 
     if (weight) {
       const float r = rsqrtf(ss * (1.f / D) + eps);
       float w[8];
-      widen8<DT>(__ldg(reinterpret_cast<const uint4*>(weight) + li), w);
+      widen8<DT>(reinterpret_cast<const uint4*>(weight)[li], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
     }
   }
   if (interleaved) {
     if (angles && li * 8 < R) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(angles) + li);
-      const float4 s = __ldg(reinterpret_cast<const float4*>(angles + R / 2) + li);
+      const float4 c = reinterpret_cast<const float4*>(angles)[li];
+      const float4 s = reinterpret_cast<const float4*>(angles + R / 2)[li];
       const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -158,7 +158,7 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], bool any_norm, const 
       const int at = first ? li : partner;
       const float4* cp = reinterpret_cast<const float4*>(angles) + at * 2;
       const float4* sp = reinterpret_cast<const float4*>(angles + R / 2) + at * 2;
-      const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
+      const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
       const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
       const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
       const float sign = first ? -1.f : 1.f;
