@@ -10,8 +10,8 @@
 //   - q is split into three e4m3 digits of four bits, q = s (d0 + d1/16 + d2/256)
 //     with s a power of two: 12 bits, which is all of bf16's 8 and fp16's 11;
 //   - the softmax weights, times the block's V scale over the largest V scale of
-//     the tile, are split the same way: 2^-12 of each weight (a single e4m3
-//     weight would be off by 2^-4), and 2^-26 of the largest.
+//     the tile, are rounded to fp16 and split the same way: 2^-11 of each weight (a
+//     single e4m3 weight would be off by 2^-4), and 2^-26 of the largest.
 // Products of digits are exact and the sums are fp32.  K scales multiply the
 // finished scores.
 //
@@ -63,12 +63,13 @@ struct Q8Args {
   const float* v_scale;
   const int32_t* tables;
   const int32_t* lens;
-  int B, Hq, H, bs, max_blocks, num_blocks, max_seq_len;
+  int B, Hq, H, bs, bs_shift, max_blocks, num_blocks, max_seq_len;
   int chunks, hch;               // chunks of a KV head's query heads, heads per chunk
   int rows_total;                // 128-byte rows of a pool
   float scale_log2;
   int dtype;
   int4* info;                    // [grid]: sequence, item of it, first tile, tiles
+  int64_t* total;                // tiles of all items
   float* ws_m;                   // [2 grid, hch]
   float* ws_l;
   float* ws_acc;                 // [2 grid, hch, D]
@@ -97,10 +98,14 @@ struct Tail {
   uint64_t sum_bar, drain;
   float qscale[2][GP];
   float red[2][4][GP + 1];       // per warp: heads' maxima, the largest V scale
-  float lred[4][GP];
+  struct alignas(8) {            // per warp: heads' running maxima, then 2^(before - now)
+    float now[2 * GP];
+  } top[4][2];
+  float lred[2][4][GP];          // of a finished segment, per warp: weights' sums
+  float mred[2][GP];             // ... and the maxima
   float half[D == 64 ? GP * 64 : 1];   // the other parity's sums (head_dim 64)
   int sums[kThreads];
-  int start[4];
+  int start[5];                  // window's first sequence, item, tile; its length; all tiles
   uint32_t tmem;
   int abort_flag;
 };
@@ -245,18 +250,6 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // The three digits of x (|x| <= 448): x = d0 + d1 / 16 + d2 / 256 up to 2^-12 |x|
 // or 2^-18.  For two values at once; digit i of the first in byte 0 of d[i].
 __device__ __forceinline__ void digits2(float x, float y, uint32_t (&d)[3]) {
@@ -271,6 +264,24 @@ __device__ __forceinline__ void digits2(float x, float y, uint32_t (&d)[3]) {
   }
 }
 
+// The same of two values held as fp16 (11 bits, so exact up to 2^-18).
+__device__ __forceinline__ void digits2(__half2 x, uint32_t (&d)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    d[i] = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E4M3);
+    if (i < 2) {
+      const __half2 v(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)d[i], __NV_E4M3));
+      x = __hmul2(__hsub2(x, v), __half2half2(__float2half(16.f)));
+    }
+  }
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Byte `col` of row n of a K-major operand with 128-byte rows and 128-byte swizzle.
 __device__ __forceinline__ int swizzled(int n, int col) {
   return n * 128 + (((col >> 4) ^ (n & 7)) << 4) + (col & 15);
@@ -280,18 +291,20 @@ __device__ __forceinline__ int clamp_len(const Q8Args& a, int b) {
   return max(0, min(a.lens[b], a.max_seq_len));
 }
 
-// Walks a window's tiles in order: sequences, then their items (KV head and head
+// Walks a window's tiles in order: sequences, then their items (KV head, then head
 // chunk), then tiles.
 template <int TOKENS>
 struct Walk {
-  int b, L, nt, item, j, left;
+  int b, L, nt, h, chunk, j, left;
 
-  __device__ __forceinline__ void next(const Q8Args& a, int items) {
+  __device__ __forceinline__ void next(const Q8Args& a) {
     --left;
     if (++j < nt) return;
     j = 0;
-    if (++item < items) return;
-    item = 0;
+    if (++chunk < a.chunks) return;
+    chunk = 0;
+    if (++h < a.H) return;
+    h = 0;
     do {
       ++b;
       L = b < a.B && left > 0 ? clamp_len(a, b) : 0;
@@ -374,10 +387,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) tail->sums[lane * E + i] = scan - sum + v[i];
-    if (lane == 31) tail->start[3] = scan;
+    if (lane == 31) tail->start[4] = scan;
   }
   __syncthreads();
-  const int64_t work = (int64_t)tail->start[3] * items;
+  const int64_t work = (int64_t)tail->start[4] * items;
   const int64_t ctas = work < (int64_t)gridDim.x ? work : (int64_t)gridDim.x;
   const bool in = (int64_t)blockIdx.x < ctas;
   const int64_t w0 = in ? work * blockIdx.x / ctas : 0;
@@ -385,9 +398,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   if (in) {
     const int t = (int)(w0 / items), before = tail->sums[tid];
     if (before <= t && t < before + mine) {
-      int b = b0, sum = before, nt = 0;
+      int b = b0, sum = before, nt = 0, len = 0;
       for (;; ++b) {
-        nt = (clamp_len(a, b) + TOKENS - 1) / TOKENS;
+        len = clamp_len(a, b);
+        nt = (len + TOKENS - 1) / TOKENS;
         if (t < sum + nt || b + 1 >= b1) break;
         sum += nt;
       }
@@ -395,25 +409,21 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       tail->start[0] = b;
       tail->start[1] = at / nt;
       tail->start[2] = at - at / nt * nt;
+      tail->start[3] = len;
     }
   }
   __syncthreads();
   Walk<TOKENS> walk;
   walk.b = tail->start[0];
-  walk.item = tail->start[1];
+  walk.h = tail->start[1] / a.chunks;
+  walk.chunk = tail->start[1] - walk.h * a.chunks;
   walk.j = tail->start[2];
   walk.left = (int)(w1 - w0);
-  walk.L = in ? clamp_len(a, walk.b) : 0;
+  walk.L = tail->start[3];
   walk.nt = (walk.L + TOKENS - 1) / TOKENS;
-  if (tid == 0) a.info[blockIdx.x] = make_int4(walk.b, walk.item, walk.j, walk.left);
-  // lengths out of range are reported; empty sequences get zero rows
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int L = a.lens[b];
-    if ((L < 0 || L > a.max_seq_len) && tid == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-    if (L <= 0 || a.max_seq_len == 0) {
-      uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (int64_t)b * a.Hq * D);
-      for (int i = tid; i < a.Hq * (D / 8); i += kThreads) row[i] = make_uint4(0, 0, 0, 0);
-    }
+  if (tid == 0) {
+    a.info[blockIdx.x] = make_int4(walk.b, tail->start[1], walk.j, walk.left);
+    if (blockIdx.x == 0) *a.total = work;
   }
   const uint32_t tmem = tail->tmem;
   const uint32_t ring = smem_addr(smem), qb = smem_addr(smem + S::kQOff),
@@ -423,7 +433,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   if (warp == 0) {
     // ------------------------------------------------------------ block ids, TMA --
     const uint64_t policy = policy_evict_first();
-    const int per_tile = TOKENS / a.bs, block_rows = a.bs / TPR;
+    const int per_tile = TOKENS >> a.bs_shift, block_rows = a.bs / TPR;
     int stage = 0, phase = 0, used = 0;
     // a lane's block of the tile that w stands at
     auto block_of = [&](const Walk<TOKENS>& w) -> int {
@@ -433,14 +443,14 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     int id = block_of(walk);
     while (walk.left > 0) {
       const int n = min(TOKENS, walk.L - walk.j * TOKENS);
-      const int nb = (n + a.bs - 1) / a.bs;
-      const int h = walk.item / a.chunks;
+      const int nb = (n + a.bs - 1) >> a.bs_shift;
+      const int h = walk.h;
       int row = a.rows_total;                   // outside the pool: the copy reads zeros
       if (lane < nb) {
         if (id >= 0 && id < a.num_blocks) row = (id * a.H + h) * block_rows;
         else report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
       }
-      walk.next(a, items);
+      walk.next(a);
       id = block_of(walk);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
@@ -471,19 +481,19 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issue --
+    // K . q of tile t, then V . p of tile t - 1: the softmax of a tile runs while the
+    // tensor cores have the next tile's scores.
     constexpr uint32_t idesc_s = idesc_f16(0, 0, 0, kTileRows, N);    // e4m3, K-major x K-major
     constexpr uint32_t idesc_o = idesc_f16(0, 1, 0, 128, N);          // V MN-major
     if (lane == 0) {
-      int use = 0, t = 0, seg = 0;              // ring uses, tiles, segments so far
-      int pv = -1;                              // tile whose P . V is still to be issued
+      int t = 0, seg = 0;
       bool fresh = true;
-      auto wait_ring = [&](int u) {
-        return mbar_wait(&tail->full[u % R], (u / R) & 1, abort_flag, kLimitNs);
-      };
       auto issue_pv = [&](int p) -> bool {
         const int u = 2 * p + 1, slot = p & 1;
-        if (!wait_ring(u)) return false;
-        if (!mbar_wait(&tail->p_full[slot], (p >> 1) & 1, abort_flag, kLimitNs)) return false;
+        // the weights are there, and with them: S of tile p and O of tile p - 2 are read
+        if (!mbar_wait(&tail->full[u % R], (u / R) & 1, abort_flag, kLimitNs) ||
+            !mbar_wait(&tail->p_full[slot], (p >> 1) & 1, abort_flag, kLimitNs))
+          return false;
         tc_fence_after();
         const uint32_t va = ring + (u % R) * kStageBytes, pa_ = pb + slot * S::kOperand;
 #pragma unroll
@@ -494,32 +504,17 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
         mma_commit(&tail->o_full[slot]);
         return true;
       };
-      while (walk.left > 0 && ok) {
-        const int slot = t & 1, qs = seg & 1;
-        // whichever is ready first: the last tile's P . V, or this tile's K
-        const uint64_t t0 = globaltimer();
-        for (int spin = 0;; ++spin) {
-          if (pv >= 0 && mbar_test(&tail->p_full[pv & 1], (pv >> 1) & 1) &&
-              mbar_test(&tail->full[(2 * pv + 1) % R], ((2 * pv + 1) / R) & 1)) {
-            ok = issue_pv(pv);
-            pv = -1;
-          }
-          if (!ok) break;
-          if ((!fresh || mbar_test(&tail->q_full[qs], (seg >> 1) & 1)) &&
-              mbar_test(&tail->full[use % R], (use / R) & 1))
-            break;
-          if (*abort_flag || ((spin & 63) == 63 && globaltimer() - t0 > kLimitNs)) {
-            ok = false;
-            break;
-          }
-        }
+      while (walk.left > 0) {
+        const int slot = t & 1, qs = seg & 1, u = 2 * t;
+        ok = (!fresh || mbar_wait(&tail->q_full[qs], (seg >> 1) & 1, abort_flag, kLimitNs)) &&
+             mbar_wait(&tail->full[u % R], (u / R) & 1, abort_flag, kLimitNs);
         if (!ok) break;
         // head_dim 64, an odd end: the last row's second token is no token, and 0 times
         // whatever stands there has to be 0
         if (TPR == 2) {
           const int n = walk.L - walk.j * TOKENS;
           if (n < TOKENS && (n & 1)) {
-            uint8_t* kt = smem + (use % R) * kStageBytes;
+            uint8_t* kt = smem + (u % R) * kStageBytes;
 #pragma unroll
             for (int c = 64; c < 128; c += 16)
               *reinterpret_cast<uint4*>(kt + swizzled(n >> 1, c)) = make_uint4(0, 0, 0, 0);
@@ -527,29 +522,30 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
           }
         }
         tc_fence_after();
-        const uint32_t ka = ring + (use % R) * kStageBytes, qa = qb + qs * S::kOperand;
+        const uint32_t ka = ring + (u % R) * kStageBytes, qa = qb + qs * S::kOperand;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mma_f8(tmem + slot * N, smem_desc_sw128(ka + k * 32, 16, 1024),
                  smem_desc_sw128(qa + k * 32, 16, 1024), idesc_s, k > 0);
-        mma_commit(&tail->empty[use % R]);
+        mma_commit(&tail->empty[u % R]);
         mma_commit(&tail->s_full[slot]);
         fresh = walk.j + 1 == walk.nt || walk.left == 1;       // a segment ends here
         if (fresh) {
           mma_commit(&tail->q_empty[qs]);
           ++seg;
         }
-        if (pv >= 0) ok = issue_pv(pv);
-        pv = t++;
-        use += 2;
-        walk.next(a, items);
+        if (t > 0) ok = issue_pv(t - 1);
+        if (!ok) break;
+        ++t;
+        walk.next(a);
       }
-      if (ok && pv >= 0) ok = issue_pv(pv);
+      if (ok && t > 0) ok = issue_pv(t - 1);
       if (!ok) {
         *abort_flag = 1;
         report(a.status_dev, PA_ERR_TIMEOUT);
       }
-      if (*abort_flag && t > 0) {               // MMAs in flight end before TMEM is freed
+      // every MMA and its arrivals end before TMEM is freed and the CTA ends
+      if (in) {
         mma_commit(&tail->drain);
         mbar_wait_drain(&tail->drain, 0, kLimitNs);
       }
@@ -565,8 +561,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
         ok = false;
         break;
       }
-      const int h = walk.item / a.chunks, g0 = (walk.item - h * a.chunks) * a.hch;
-      const int gn = min(a.hch, G - g0);
+      const int h = walk.h, g0 = walk.chunk * a.hch, gn = min(a.hch, G - g0);
       uint8_t* op = smem + S::kQOff + slot * S::kOperand;
       const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) +
                           ((int64_t)walk.b * a.Hq + h * G + g0) * (D / 2) + lane * (E / 2);
@@ -613,7 +608,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       const int skip = min(walk.nt - walk.j, walk.left) - 1;
       walk.j += skip;
       walk.left -= skip;
-      walk.next(a, items);
+      walk.next(a);
+    }
+    // lengths out of range are reported; empty sequences get zero rows
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      const int L = a.lens[b];
+      if ((L < 0 || L > a.max_seq_len) && lane == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+      if (L <= 0 || a.max_seq_len == 0) {
+        uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (int64_t)b * a.Hq * D);
+        for (int i = lane; i < a.Hq * (D / 8); i += 32) row[i] = make_uint4(0, 0, 0, 0);
+      }
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -621,11 +625,13 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     }
   } else {
     // ------------------------------------------------------------ softmax and sums --
+    // Iteration t: weights of tile t; sums of tile t - 1, whose product has had most of
+    // an iteration's time; scores and maxima of tile t + 1.  So neither the exchange of
+    // the maxima nor a product is waited for as soon as it is asked for.
     const int wq = warp & 3;                    // TMEM lane quarter of this warp
     const int r = wq * 32 + lane;               // tile row; then row of O^T
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const int par = r / D;                      // head_dim 64: the token parity of this O^T row
-    int t = 0, seg = 0, sums = 0;
     auto wait_all = [&](uint64_t* bar, int parity) -> bool {
       return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kLimitNs));
     };
@@ -634,110 +640,203 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       ks = vs = 0.f;
       const int tok = w.j * TOKENS + r * TPR;
       if (w.left <= 0 || tok >= w.L) return;
-      const int id = a.tables[(int64_t)w.b * a.max_blocks + tok / a.bs];
+      const int id = a.tables[(int64_t)w.b * a.max_blocks + (tok >> a.bs_shift)];
       if (id < 0 || id >= a.num_blocks) return;
-      const int64_t at = (int64_t)id * a.H + w.item / a.chunks;
+      const int64_t at = (int64_t)id * a.H + w.h;
       ks = a.k_scale[at];
       vs = a.v_scale[at];
     };
-    float ks, vs;
-    scales_of(walk, ks, vs);
-    float m[GP], l[GP], acc[GP], alpha[GP], unit = 0.f;   // alpha, unit: of the tile before
-    // acc <- acc 2^(m_before - m) + O_t, with tile t's factors
-    auto add_tile = [&](int tile) -> bool {
-      const int slot = tile & 1;
-      if (!wait_all(&tail->o_full[slot], (tile >> 1) & 1)) return false;
+    // where this row's byte of operand row n goes, by n & 7
+    uint8_t* put[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) put[c] = smem + S::kPOff + (((r >> 4) ^ c) << 4) + (r & 15);
+    float x[TPR][GP];                           // scores of the tile ahead
+    float l[GP], acc[GP], unit = 0.f;           // unit: of the tile behind
+    float m_lane = -CUDART_INF_F;               // head `lane`: the running maximum
+    int t = 0, seg = 0;                         // tile; segment of tile t
+
+    // scores of tile u (n tokens left, segment sg) and their maxima, posted for all warps
+    auto score_tile = [&](int u, int n, int sg, bool first, float ks, float vs) -> bool {
+      const int slot = u & 1, qs = sg & 1;
+      if (first && !wait_all(&tail->q_full[qs], (sg >> 1) & 1)) return false;
+      if (!wait_all(&tail->s_full[slot], (u >> 1) & 1)) return false;
       tc_fence_after();
-      float o[cols_for(3 * GP)];
-      load_cols<cols_for(3 * GP)>(tmem + lanes + (2 + slot) * N + par * 3 * GP, o);
+      float s[cols_for(S::kUsed)];
+      load_cols<cols_for(S::kUsed)>(tmem + lanes + slot * N, s);
+      // heads in pairs (two-wide fp32 arithmetic); a last odd one is paired with itself
+      const uint64_t c16 = f2_pack(1.f / 16.f, 1.f / 16.f), c256 = f2_pack(1.f / 256.f, 1.f / 256.f);
+      const uint64_t ks2 = f2_pack(ks, ks);
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        const float sum = fmaf(o[2 * GP + g], 1.f / 256.f, fmaf(o[GP + g], 1.f / 16.f, o[g]));
-        acc[g] = fmaf(sum, unit, acc[g] * alpha[g]);
-      }
-      return true;
-    };
-    int j0 = 0;                                 // first tile of the segment
-    bool fresh = true;
-    while (walk.left > 0) {
-      const int slot = t & 1, qs = seg & 1;
-      if (fresh) {
-        if (!wait_all(&tail->q_full[qs], (seg >> 1) & 1)) { ok = false; break; }
-        j0 = walk.j;
+      for (int g = 0; g < GP; g += 2) {
+        const int g1 = g + 1 < GP ? g + 1 : g;
+        const uint64_t f = f2_mul(f2_pack(tail->qscale[qs][g], tail->qscale[qs][g1]), ks2);
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
-          m[g] = -CUDART_INF_F;
-          l[g] = acc[g] = 0.f;
+        for (int v = 0; v < TPR; ++v) {
+          const float* d = s + v * 3 * GP;
+          const uint64_t sum =
+              f2_fma(f2_pack(d[2 * GP + g], d[2 * GP + g1]), c256,
+                     f2_fma(f2_pack(d[GP + g], d[GP + g1]), c16, f2_pack(d[g], d[g1])));
+          float x0, x1;
+          f2_unpack(f2_mul(sum, f), x0, x1);
+          // rows behind the end hold anything
+          const bool live = r * TPR + v < n;
+          x[v][g] = live ? x0 : -CUDART_INF_F;
+          if (g1 > g) x[v][g1] = live ? x1 : -CUDART_INF_F;
         }
       }
-      const Walk<TOKENS> at = walk;
-      const int n = at.L - at.j * TOKENS;       // tokens left from this tile on
-      const bool ends = at.j + 1 == at.nt || at.left == 1;
-      const float ksc = ks, vsc = vs;
-      walk.next(a, items);
-      scales_of(walk, ks, vs);
-
-      if (!wait_all(&tail->s_full[slot], (t >> 1) & 1)) { ok = false; break; }
-      tc_fence_after();
-      float x[TPR][GP];
-      {
-        float s[cols_for(S::kUsed)];
-        load_cols<cols_for(S::kUsed)>(tmem + lanes + slot * N, s);
-#pragma unroll
-        for (int v = 0; v < TPR; ++v)
-#pragma unroll
-          for (int g = 0; g < GP; ++g) {
-            const float* d = s + v * 3 * GP + g;
-            const float sum = fmaf(d[2 * GP], 1.f / 256.f, fmaf(d[GP], 1.f / 16.f, d[0]));
-            // rows behind the end hold anything
-            x[v][g] = r * TPR + v < n ? sum * (tail->qscale[qs][g] * ksc) : -CUDART_INF_F;
-          }
-      }
-      // the tile's maxima over its rows
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
         const float w = warp_max(TPR == 2 ? fmaxf(x[0][g], x[TPR - 1][g]) : x[0][g]);
         if (lane == g) tail->red[slot][wq][g] = w;
       }
-      const float wv = warp_max(vsc);
+      const float wv = warp_max(vs);
       if (lane == 0) tail->red[slot][wq][GP] = wv;
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->red_bar[slot]);
-      if (!wait_all(&tail->red_bar[slot], (t >> 1) & 1)) { ok = false; break; }
-      float p[TPR][GP], alpha_t[GP];
+      return true;
+    };
+    // acc <- acc 2^(m_before - m) + O, with tile u's factors
+    auto add_tile = [&](int u) -> bool {
+      const int slot = u & 1;
+      if (!wait_all(&tail->o_full[slot], (u >> 1) & 1)) return false;
+      tc_fence_after();
+      float o[cols_for(3 * GP)];
+      load_cols<cols_for(3 * GP)>(tmem + lanes + (2 + slot) * N + par * 3 * GP, o);
+      const uint64_t c16 = f2_pack(1.f / 16.f, 1.f / 16.f), c256 = f2_pack(1.f / 256.f, 1.f / 256.f);
+      const uint64_t unit2 = f2_pack(unit, unit);
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        const float top = fmaxf(fmaxf(tail->red[slot][0][g], tail->red[slot][1][g]),
-                                fmaxf(tail->red[slot][2][g], tail->red[slot][3][g]));
-        const float m_new = fmaxf(m[g], top);
-        alpha_t[g] = ex2_approx(m[g] - m_new);
-        m[g] = m_new;
-        float sum = 0.f;
+      for (int g = 0; g < GP; g += 2) {
+        const int g1 = g + 1 < GP ? g + 1 : g;
+        const uint64_t sum =
+            f2_fma(f2_pack(o[2 * GP + g], o[2 * GP + g1]), c256,
+                   f2_fma(f2_pack(o[GP + g], o[GP + g1]), c16, f2_pack(o[g], o[g1])));
+        const uint64_t was = f2_mul(f2_pack(acc[g], acc[g1]),
+                                    f2_pack(tail->top[wq][slot].now[GP + g],
+                                            tail->top[wq][slot].now[GP + g1]));
+        float y0, y1;
+        f2_unpack(f2_fma(sum, unit2, was), y0, y1);
+        acc[g] = y0;
+        if (g1 > g) acc[g1] = y1;
+      }
+      return true;
+    };
+    // the finished segment sg of (sequence b, item): to out, or to the workspace if cut
+    auto finish = [&](int sg, int b, int h, int chunk, bool whole, bool alone) -> bool {
+      if (D == 64 && par == 1) {
+#pragma unroll
+        for (int g = 0; g < GP; ++g) tail->half[g * 64 + r - 64] = acc[g];
+      }
+      // a tile behind the segment has its red_bar between lred's writes and here
+      if (D == 64 || alone) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->sum_bar);
+        if (!wait_all(&tail->sum_bar, D == 64 ? sg & 1 : 0)) return false;
+      }
+      const int g0 = chunk * a.hch, gn = min(a.hch, G - g0);
+      if (r < D) {
+        const int64_t row0 = (int64_t)b * a.Hq + h * G + g0;
+        const int64_t part = (2 * (int64_t)blockIdx.x + (sg > 0)) * a.hch;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          if (g >= gn) continue;
+          const float* lr = &tail->lred[sg & 1][0][g];
+          const float sum = (lr[0] + lr[GP]) + (lr[2 * GP] + lr[3 * GP]);
+          const float o = acc[g] + (D == 64 ? tail->half[g * 64 + (r & 63)] : 0.f);
+          if (whole) {
+            const float y = __fdividef(o, sum);
+            static_cast<uint16_t*>(a.out)[(row0 + g) * D + r] =
+                a.dtype == PA_BFLOAT16 ? narrow<PA_BFLOAT16>(y) : narrow<PA_FLOAT16>(y);
+          } else {
+            a.ws_acc[(part + g) * D + r] = o;
+            if (r == 0) {
+              a.ws_m[part + g] = tail->mred[sg & 1][g];
+              a.ws_l[part + g] = sum;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < GP; ++g) acc[g] = 0.f;
+      return true;
+    };
+
+    Walk<TOKENS> cur = walk;                    // tile t; walk runs ahead
+    float vs_cur = 0.f, ks_next, vs_next;
+    bool first = true, first_of_item = walk.j == 0;
+    int fin_b = 0, fin_h = 0, fin_chunk = 0;                // the segment that tile t - 1 finished
+    bool fin = false, fin_whole = false;
+#pragma unroll
+    for (int g = 0; g < GP; ++g) l[g] = acc[g] = 0.f;
+    if (cur.left > 0) {
+      float ks;
+      scales_of(cur, ks, vs_cur);
+      walk.next(a);
+      scales_of(walk, ks_next, vs_next);
+      ok = score_tile(0, cur.L - cur.j * TOKENS, 0, true, ks, vs_cur);
+    }
+    while (ok && cur.left > 0) {
+      const int slot = t & 1;
+      const int n = cur.L - cur.j * TOKENS;     // tokens left from this tile on
+      const bool ends = cur.j + 1 == cur.nt || cur.left == 1;
+      const Walk<TOKENS> ahead = walk;          // tile t + 1
+      float ks2 = 0.f, vs2 = 0.f;
+      if (ahead.left > 0) {
+        walk.next(a);
+        scales_of(walk, ks2, vs2);              // tile t + 2
+      }
+      if (first) {
+        m_lane = -CUDART_INF_F;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) l[g] = 0.f;
+      }
+      if (!wait_all(&tail->red_bar[slot], (t >> 1) & 1)) { ok = false; break; }
+      float vmax = 0.f;
+      {
+        const float* red = &tail->red[slot][0][min(lane, GP)];
+        const float top = fmaxf(fmaxf(red[0], red[GP + 1]), fmaxf(red[2 * GP + 2], red[3 * GP + 3]));
+        vmax = __shfl_sync(kAll, top, GP);
+        if (lane < GP) {
+          const float now = fmaxf(m_lane, top);
+          tail->top[wq][slot].now[lane] = now;
+          tail->top[wq][slot].now[GP + lane] = ex2_approx(m_lane - now);
+          m_lane = now;
+        }
+        __syncwarp();
+      }
+      // weights, in units of the tile's largest V scale and 256 at most
+      const float to = vmax > 0.f ? vs_cur * (256.f / vmax) : 0.f;
+      const float* top = tail->top[wq][slot].now;
+      const uint64_t to2 = f2_pack(to, to);
+#pragma unroll
+      for (int g = 0; g < GP; g += 2) {
+        const int g1 = g + 1 < GP ? g + 1 : g;
+        const uint64_t m2 = f2_pack(top[g], top[g1]);
+        uint64_t sum = f2_mul(f2_pack(l[g], l[g1]), f2_pack(top[GP + g], top[GP + g1]));
 #pragma unroll
         for (int v = 0; v < TPR; ++v) {
-          p[v][g] = r * TPR + v < n ? ex2_approx(x[v][g] - m_new) : 0.f;
-          sum += p[v][g];
-        }
-        l[g] = fmaf(l[g], alpha_t[g], sum);
-      }
-      // weights in units of the tile's largest V scale, 256 at most
-      const float vmax = fmaxf(fmaxf(tail->red[slot][0][GP], tail->red[slot][1][GP]),
-                               fmaxf(tail->red[slot][2][GP], tail->red[slot][3][GP]));
-      const float to = vmax > 0.f ? vsc * (256.f / vmax) : 0.f;
-      uint8_t* op = smem + S::kPOff + slot * S::kOperand;
-#pragma unroll
-      for (int v = 0; v < TPR; ++v)
-#pragma unroll
-        for (int g = 0; g < GP; g += 2) {
+          float p0, p1;                         // 0 behind the end
+          f2_unpack(f2_sub(f2_pack(x[v][g], x[v][g1]), m2), p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          const uint64_t p2 = f2_pack(p0, p1);
+          sum = f2_add(sum, p2);
+          float w0, w1;
+          f2_unpack(f2_mul(p2, to2), w0, w1);
           uint32_t d[3];
-          digits2(p[v][g] * to, g + 1 < GP ? p[v][g + 1 < GP ? g + 1 : g] * to : 0.f, d);
+          digits2(__floats2half2_rn(w0, w1), d);
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
             const int row = (v * 3 + i) * GP + g;
-            op[swizzled(row, r)] = (uint8_t)d[i];
-            if (g + 1 < GP) op[swizzled(row + 1, r)] = (uint8_t)(d[i] >> 8);
+            put[row & 7][slot * S::kOperand + row * 128] = (uint8_t)d[i];
+            if (g1 > g)
+              put[(row + 1) & 7][slot * S::kOperand + (row + 1) * 128] = (uint8_t)(d[i] >> 8);
           }
         }
+        float l0, l1;
+        f2_unpack(sum, l0, l1);
+        l[g] = l0;
+        if (g1 > g) l[g1] = l1;
+      }
       // tokens behind the end: zero their V, so that 0 times garbage stays 0
       if (n < TOKENS) {
         const int u = 2 * t + 1;
@@ -755,60 +854,44 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->p_full[slot]);
-      if (!fresh && !add_tile(t - 1)) { ok = false; break; }
-#pragma unroll
-      for (int g = 0; g < GP; ++g) alpha[g] = alpha_t[g];
-      unit = vmax * (1.f / 256.f);
-      fresh = ends;
-      if (ends) {
-        if (!add_tile(t)) { ok = false; break; }
-        tc_fence_before();
+      const int seg_t = seg;
+      if (ends) {                               // what finish() needs of tile t's segment
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
           float sum = l[g];
 #pragma unroll
           for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-          if (lane == g) tail->lred[wq][g] = sum;
-          if (D == 64 && par == 1) tail->half[g * 64 + r - 64] = acc[g];
+          if (lane == g) tail->lred[seg & 1][wq][g] = sum;
         }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&tail->q_empty[qs]);
-          mbar_arrive(&tail->sum_bar);
-        }
-        if (!wait_all(&tail->sum_bar, sums & 1)) { ok = false; break; }
-        ++sums;
-        const int h = at.item / a.chunks, g0 = (at.item - h * a.chunks) * a.hch;
-        const int gn = min(a.hch, G - g0);
-        const bool whole = j0 == 0 && at.j + 1 == at.nt;
-        if (r < D) {
-          const int64_t row0 = (int64_t)at.b * a.Hq + h * G + g0;
-          const int64_t part = (2 * (int64_t)blockIdx.x + (seg > 0)) * a.hch;
-#pragma unroll
-          for (int g = 0; g < GP; ++g) {
-            if (g >= gn) continue;
-            const float sum = (tail->lred[0][g] + tail->lred[1][g]) +
-                              (tail->lred[2][g] + tail->lred[3][g]);
-            const float o = acc[g] + (D == 64 ? tail->half[g * 64 + (r & 63)] : 0.f);
-            if (whole) {
-              const float y = o / sum;
-              static_cast<uint16_t*>(a.out)[(row0 + g) * D + r] =
-                  a.dtype == PA_BFLOAT16 ? narrow<PA_BFLOAT16>(y) : narrow<PA_FLOAT16>(y);
-            } else {
-              a.ws_acc[(part + g) * D + r] = o;
-              if (r == 0) {
-                a.ws_m[part + g] = m[g];
-                a.ws_l[part + g] = sum;
-              }
-            }
-          }
-        }
-        // lred and half are written again only after the next segment's first
-        // red_bar, which every warp reaches behind these reads
+        if (wq == 0 && lane < GP) tail->mred[seg & 1][lane] = m_lane;
+        if (lane == 0) mbar_arrive(&tail->q_empty[seg & 1]);
         ++seg;
       }
+      // what finish() reads is written again only behind the red_bar that score_tile posts
+      if (t > 0 && !add_tile(t - 1)) { ok = false; break; }
+      if (fin && !finish(seg_t - 1, fin_b, fin_h, fin_chunk, fin_whole, false)) { ok = false; break; }
+      if (ahead.left > 0 &&
+          !score_tile(t + 1, ahead.L - ahead.j * TOKENS, seg, ends, ks_next, vs_next)) {
+        ok = false;
+        break;
+      }
+      unit = vmax * (1.f / 256.f);
+      fin = ends;
+      if (ends) {
+        fin_b = cur.b;
+        fin_h = cur.h;
+        fin_chunk = cur.chunk;
+        fin_whole = first_of_item && cur.j + 1 == cur.nt;
+        first_of_item = true;                   // the next segment begins at tile 0
+      }
+      first = ends;
+      cur = ahead;
+      vs_cur = vs_next;
+      ks_next = ks2;
+      vs_next = vs2;
       ++t;
     }
+    if (ok && fin) ok = add_tile(t - 1) && finish(seg - 1, fin_b, fin_h, fin_chunk, fin_whole, true);
     if (!ok) {
       *abort_flag = 1;
       if (lane == 0) report(a.status_dev, PA_ERR_TIMEOUT);
@@ -825,45 +908,59 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
 
 // Joins the partials of items that window boundaries cut: CTA c looks at the
 // boundary where window c begins, and joins its item if that boundary is the
-// item's first.  Threads are elements of a head, kJoinThreads / D heads at a time.
+// item's first.  A warp takes a head's maximum and the parts' weights; then
+// threads are elements of a head, kJoinThreads / D heads at a time.
 constexpr int kJoinThreads = 512;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, int windows) {
+__global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, int grid) {
+  constexpr int TOKENS = kTileRows * 128 / D;
+  __shared__ float s_w[16][kMaxGrid];
   allow_next_grid();
   wait_prior_grid();
   const int c = (int)blockIdx.x + 1;
-  const int4 at = a.info[c];                   // sequence, item, first tile, tiles
+  const int4 at = a.info[c], before = a.info[c - 1];   // sequence, item, first tile, tiles
   if (at.w <= 0 || at.z == 0) return;          // an empty window, or a boundary between items
-  const int4 before = a.info[c - 1];
   const bool same = before.x == at.x && before.y == at.y;
   if (same && before.z > 0) return;            // an earlier boundary cuts this item
-  // the parts: the segment of window c - 1 that ends there, then the first segment of
-  // windows c, c + 1, ... as long as they begin inside the item
-  int last = c;
-  while (last + 1 < windows) {
-    const int4 next = a.info[last + 1];
-    if (next.w <= 0 || next.z == 0 || next.x != at.x || next.y != at.y) break;
-    ++last;
-  }
+  // the parts: the segment of window c - 1 that ends there, then the first segments of
+  // windows c .. last, last holding the item's final tile
+  const int64_t work = *a.total, windows = work < grid ? work : grid;
+  const int nt = (max(0, min(a.lens[at.x], a.max_seq_len)) + TOKENS - 1) / TOKENS;
+  const int64_t end = work * c / windows - at.z + nt;
+  const int last = (int)min((end * windows - 1) / work, windows - 1);
+  const int parts = last - c + 2;
   const int h = at.y / a.chunks, G = a.Hq / a.H, g0 = (at.y - h * a.chunks) * a.hch;
   const int gn = min(a.hch, G - g0);
   const int64_t head = 2 * (int64_t)(c - 1) + (same ? 0 : 1);
+  auto row = [&](int k) { return (k == 0 ? head : 2 * (int64_t)(c + k - 1)) * a.hch; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < gn) {
+    float top = -CUDART_INF_F;
+    for (int k = lane; k < parts; k += 32) {
+      const float m = a.ws_m[row(k) + warp];
+      s_w[warp][k] = m;
+      top = fmaxf(top, m);
+    }
+    top = warp_max(top);
+    float l = 0.f;
+    for (int k = lane; k < parts; k += 32) {
+      const float w = ex2_approx(s_w[warp][k] - top);
+      s_w[warp][k] = w;
+      l = fmaf(w, a.ws_l[row(k) + warp], l);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+    const float inv = 1.f / l;
+    for (int k = lane; k < parts; k += 32) s_w[warp][k] *= inv;
+  }
+  __syncthreads();
   const int d = threadIdx.x % D;
   for (int g = threadIdx.x / D; g < gn; g += kJoinThreads / D) {
-    const int64_t p0 = head * a.hch + g;
-    float top = a.ws_m[p0];
-    for (int k = c; k <= last; ++k) top = fmaxf(top, a.ws_m[2 * (int64_t)k * a.hch + g]);
-    float w = ex2_approx(a.ws_m[p0] - top);
-    float l = w * a.ws_l[p0], o = w * a.ws_acc[p0 * D + d];
-#pragma unroll 4
-    for (int k = c; k <= last; ++k) {
-      const int64_t p = 2 * (int64_t)k * a.hch + g;
-      w = ex2_approx(a.ws_m[p] - top);
-      l = fmaf(w, a.ws_l[p], l);
-      o = fmaf(w, a.ws_acc[p * D + d], o);
-    }
-    const float y = o / l;
+    float y = s_w[g][0] * a.ws_acc[(row(0) + g) * D + d];
+#pragma unroll 8
+    for (int k = 1; k < parts; ++k)
+      y = fmaf(s_w[g][k], a.ws_acc[(2 * (int64_t)(c + k - 1) * a.hch + g) * D + d], y);
     static_cast<uint16_t*>(a.out)[((int64_t)at.x * a.Hq + h * G + g0 + g) * D + d] =
         a.dtype == PA_BFLOAT16 ? narrow<PA_BFLOAT16>(y) : narrow<PA_FLOAT16>(y);
   }
@@ -915,7 +1012,7 @@ Plan plan_of(int Hq, int H, int D, int max_seq_len) {
   p.tiles = ((int64_t)max_seq_len + tokens - 1) / tokens;
   auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
   const size_t rows = (size_t)2 * kMaxGrid * p.hch;
-  p.m_off = align(kMaxGrid * sizeof(int4));
+  p.m_off = align(kMaxGrid * sizeof(int4) + sizeof(int64_t));
   p.l_off = p.m_off + align(rows * sizeof(float));
   p.acc_off = p.l_off + align(rows * sizeof(float));
   p.total = p.acc_off + align(rows * D * sizeof(float));
@@ -1026,6 +1123,7 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   a.Hq = num_q_heads;
   a.H = num_kv_heads;
   a.bs = block_size;
+  a.bs_shift = block_size == 8 ? 3 : (block_size == 16 ? 4 : (block_size == 32 ? 5 : 6));
   a.max_blocks = max_blocks;
   a.num_blocks = num_blocks;
   a.max_seq_len = max_seq_len;
@@ -1036,6 +1134,7 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   a.dtype = dtype;
   char* ws = static_cast<char*>(workspace);
   a.info = reinterpret_cast<int4*>(ws);
+  a.total = reinterpret_cast<int64_t*>(ws + kMaxGrid * sizeof(int4));
   a.ws_m = reinterpret_cast<float*>(ws + p.m_off);
   a.ws_l = reinterpret_cast<float*>(ws + p.l_off);
   a.ws_acc = reinterpret_cast<float*>(ws + p.acc_off);

@@ -5,11 +5,12 @@ Bounds of the decode.  With p the softmax weights, A = sum_t p_t |V_t| per outpu
 and S = max_t scale sum_d |q_d K_td|:
   - a score sums at most 3 x 128 products in fp32: off by at most 384 * 2^-24 S = 2^-15.4 S
     (natural units), a weight by twice that (itself and the normaliser);
-  - a weight may be held as three e4m3 digits of 4 bits: 2^-12 of itself, or 2^-25 of the
+  - a weight may be held as three e4m3 digits of an fp16 number: fp16 has 11 bits, so half
+    a step is 2^-11 of the weight, and the digits, 4 bits each, hold all 11; or 2^-25 of the
     largest weight where that is more (each token adds at most that much of |V|);
   - the sums and the join of splits: fp32, far below; taken as 2^-16 A;
   - the store: half a step of the type.
-So |d| <= eps/2 |ref| + (2^-12 + 2^-14.4 S + 2^-16) A + n 2^-25 max|V| (n tokens) + half
+So |d| <= eps/2 |ref| + (2^-11 + 2^-14.4 S + 2^-16) A + n 2^-25 max|V| (n tokens) + half
 a subnormal step."""
 import numpy as np
 import pytest
@@ -88,7 +89,7 @@ def check_decode(got, q, k, v, tables, lens, scale, dt, rows=None):
         pos = np.arange(lens[b])
         blk = np.asarray(tables[b], dtype=np.int64)[pos // k.shape[1]]
         top = np.abs(v[blk, pos % k.shape[1]]).max()
-        e = (2.0 ** -12 + 2.0 ** -14.4 * size[:, None] + 2.0 ** -16) * mass + \
+        e = (2.0 ** -11 + 2.0 ** -14.4 * size[:, None] + 2.0 ** -16) * mass + \
             lens[b] * 2.0 ** -25 * top
         bad = ~(np.abs(got[b] - ref) <= half * (np.abs(ref) + e) + e + tiny)
         assert not bad.any(), (b, lens[b], int(bad.sum()), np.argwhere(bad)[:3],
@@ -128,6 +129,47 @@ def test_decode_many_sequences(pa):
     b = Batch(lens, 4, 2, 128, 16, "bf16", seed=4)
     out = b.run(pa)
     b.check(out, rows=range(0, 700, 9))
+
+
+@pytest.mark.parametrize("D,G,bs", [(128, 8, 32), (128, 16, 16), (128, 5, 64), (128, 1, 8), (64, 4, 16),
+                                    (64, 8, 8)])
+def test_decode_many_tiles_per_window(pa, D, G, bs):
+    """Tens of tiles to every CTA: the rings and buffers go round many times.  Against the
+    definition in fp64, by torch on the GPU, for some heads of each sequence."""
+    H, lens = 8, [70001, 20000, 31, 45678, 3000, 1]
+    g = torch.Generator("cuda").manual_seed(D + G)
+    used = [-(-n // bs) for n in lens]
+    NB = sum(used) + 3
+    order = torch.randperm(NB, generator=g, device="cuda").to(torch.int32)
+    tables = torch.full((len(lens), max(used)), -1, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(used):
+        tables[b, :n] = order[sum(used[:b]):sum(used[:b + 1])]
+    pools = [torch.empty(NB, H, bs, D, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    for p in pools:
+        for i in range(0, NB, 1024):       # normal values, 100 times
+            x = torch.randn(min(1024, NB - i), H, bs, D, generator=g, device="cuda") * 100
+            p[i:i + 1024] = x.clamp(-448, 448).to(pa.E4M3).view(torch.uint8)
+    sc = [torch.exp2(torch.randint(-9, -5, (NB, H), generator=g, device="cuda").float())
+          for _ in "kv"]
+    q = torch.randn(len(lens), G * H, D, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, float("nan"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_decode_q8(out, q, *pools, *sc, tables, i32(lens), 0.05, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for b, n in enumerate(lens):
+        blk = tables[b, :used[b]].long()
+        for h in (0, 3, H - 1):
+            k, v = ((p[blk, h].view(pa.E4M3).double() * s[blk, h].double()[:, None, None])
+                    .reshape(-1, D)[:n] for p, s in zip(pools, sc))
+            mine = slice(h * G, (h + 1) * G)
+            qd = q[b, mine].double()
+            w = torch.softmax(0.05 * qd @ k.T, -1)
+            ref, mass = w @ v, w @ v.abs()
+            size = 0.05 * (qd.abs() @ k.abs().T).amax(-1, keepdim=True)
+            e = (2.0 ** -11 + 2.0 ** -14.4 * size + 2.0 ** -16) * mass + n * 2.0 ** -25 * v.abs().max()
+            bad = ~((out[b, mine].double() - ref).abs() <= 2.0 ** -8 * (ref.abs() + e) + e)
+            assert not bad.any(), (b, h, int(bad.sum()))
 
 
 def test_decode_any_positive_scale(pa):
