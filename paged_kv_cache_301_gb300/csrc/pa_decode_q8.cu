@@ -56,6 +56,14 @@ constexpr int kMaxGrid = 320;                  // CTAs at most (two per SM)
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
+// Where a CTA's window begins: sequence, item of it, tile; tiles of that item and in
+// the window; tiles of all items.
+struct alignas(16) Window {
+  int b, item, j, nt;
+  int tiles, pad;
+  int64_t total;
+};
+
 struct Q8Args {
   void* out;
   const void* q;
@@ -68,8 +76,7 @@ struct Q8Args {
   int rows_total;                // 128-byte rows of a pool
   float scale_log2;
   int dtype;
-  int4* info;                    // [grid]: sequence, item of it, first tile, tiles
-  int64_t* total;                // tiles of all items
+  Window* info;                  // [grid]
   float* ws_m;                   // [2 grid, hch]
   float* ws_l;
   float* ws_acc;                 // [2 grid, hch, D]
@@ -421,10 +428,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   walk.left = (int)(w1 - w0);
   walk.L = tail->start[3];
   walk.nt = (walk.L + TOKENS - 1) / TOKENS;
-  if (tid == 0) {
-    a.info[blockIdx.x] = make_int4(walk.b, tail->start[1], walk.j, walk.left);
-    if (blockIdx.x == 0) *a.total = work;
-  }
+  if (tid == 0)
+    a.info[blockIdx.x] = {walk.b, tail->start[1], walk.j, walk.nt, walk.left, 0, work};
   const uint32_t tmem = tail->tmem;
   const uint32_t ring = smem_addr(smem), qb = smem_addr(smem + S::kQOff),
                  pb = smem_addr(smem + S::kPOff);
@@ -552,50 +557,56 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------------- q digits --
-    constexpr int E = D / 32;                   // elements of a lane
+    constexpr int W = D / 64;                   // 32-bit words of a lane and head
+    uint32_t now[GP][W], ahead[GP][W];          // this segment's q, and the next one's
+    auto load_q = [&](const Walk<TOKENS>& w, uint32_t (&x)[GP][W]) {
+      const int g0 = w.chunk * a.hch, gn = w.left > 0 ? min(a.hch, G - g0) : 0;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) +
+                          ((int64_t)w.b * a.Hq + w.h * G + g0) * (D / 2) + lane * W;
+#pragma unroll
+      for (int g = 0; g < GP; ++g)
+#pragma unroll
+        for (int e = 0; e < W; ++e) x[g][e] = g < gn ? q[g * (D / 2) + e] : 0u;
+    };
     int seg = 0;
+    load_q(walk, now);
     while (walk.left > 0) {
       const int slot = seg & 1;
+      const int skip = min(walk.nt - walk.j, walk.left) - 1;   // to the segment's last tile
+      walk.j += skip;
+      walk.left -= skip;
+      walk.next(a);
+      load_q(walk, ahead);
       if (!__all_sync(kAll, mbar_wait(&tail->q_empty[slot], ((seg >> 1) & 1) ^ 1, abort_flag,
                                       kLimitNs))) {
         ok = false;
         break;
       }
-      const int h = walk.h, g0 = walk.chunk * a.hch, gn = min(a.hch, G - g0);
       uint8_t* op = smem + S::kQOff + slot * S::kOperand;
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) +
-                          ((int64_t)walk.b * a.Hq + h * G + g0) * (D / 2) + lane * (E / 2);
-      for (int g = 0; g < gn; ++g) {
-        float x[E];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        float2 x[W];
         float m = 0.f;
         bool bad = false;
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          const uint32_t w = q[g * (D / 2) + e];
-          const float2 v =
-              a.dtype == PA_BFLOAT16 ? widen2<PA_BFLOAT16>(w) : widen2<PA_FLOAT16>(w);
-          x[2 * e] = v.x;
-          x[2 * e + 1] = v.y;
+        for (int e = 0; e < W; ++e) {
+          x[e] = a.dtype == PA_BFLOAT16 ? widen2<PA_BFLOAT16>(now[g][e])
+                                        : widen2<PA_FLOAT16>(now[g][e]);
+          m = fmaxf(m, fmaxf(finite_mag(x[e].x), finite_mag(x[e].y)));
+          bad |= !(fabsf(x[e].x) < CUDART_INF_F) || !(fabsf(x[e].y) < CUDART_INF_F);
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          m = fmaxf(m, finite_mag(x[e]));
-          bad |= !(fabsf(x[e]) < CUDART_INF_F);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        const float s = scale_for(warp_max(m)), inv = 1.f / s;
         bad = __any_sync(kAll, bad);
-        const float s = scale_for(m), inv = 1.f / s;
-        uint32_t d[3], d2[3] = {0, 0, 0};
-        digits2(x[0] * inv, x[1] * inv, d);
-        if (E == 4) digits2(x[E - 2] * inv, x[E - 1] * inv, d2);
+        uint32_t d[W][3];
+#pragma unroll
+        for (int e = 0; e < W; ++e) digits2(x[e].x * inv, x[e].y * inv, d[e]);
 #pragma unroll
         for (int v = 0; v < TPR; ++v)
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
-            const int at = swizzled((v * 3 + i) * GP + g, v * D + lane * E);
-            if (E == 4) *reinterpret_cast<uint32_t*>(op + at) = d[i] | (d2[i] << 16);
-            else *reinterpret_cast<uint16_t*>(op + at) = (uint16_t)d[i];
+            uint8_t* to = op + swizzled((v * 3 + i) * GP + g, v * D + lane * 2 * W);
+            if (W == 2) *reinterpret_cast<uint32_t*>(to) = d[0][i] | (d[W - 1][i] << 16);
+            else *reinterpret_cast<uint16_t*>(to) = (uint16_t)d[0][i];
           }
         // a row with an infinity or a NaN has no finite scores
         if (lane == 0) tail->qscale[slot][g] = bad ? CUDART_NAN_F : s * a.scale_log2;
@@ -604,11 +615,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->q_full[slot]);
       ++seg;
-      // on to the next segment
-      const int skip = min(walk.nt - walk.j, walk.left) - 1;
-      walk.j += skip;
-      walk.left -= skip;
-      walk.next(a);
+#pragma unroll
+      for (int g = 0; g < GP; ++g)
+#pragma unroll
+        for (int e = 0; e < W; ++e) now[g][e] = ahead[g][e];
     }
     // lengths out of range are reported; empty sequences get zero rows
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -906,36 +916,51 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   }
 }
 
-// Joins the partials of items that window boundaries cut: CTA c looks at the
-// boundary where window c begins, and joins its item if that boundary is the
-// item's first.  A warp takes a head's maximum and the parts' weights; then
-// threads are elements of a head, kJoinThreads / D heads at a time.
+// Joins the partials of items that window boundaries cut: CTA (c, y) looks at the
+// boundary where window c + 1 begins, and joins kJoinHeads heads of its item if that
+// boundary is the item's first.  Its time is the chain of loads (window, then all
+// partials), so the partials are asked for before the weights are known: a warp
+// takes a head's maximum and weights, the other threads are elements of a head, the
+// parts dealt out to kJoinThreads / D groups of them.
 constexpr int kJoinThreads = 512;
+constexpr int kJoinHeads = 2;
+constexpr int kJoinAhead = 4;                  // parts of a group asked for at once
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, int grid) {
-  constexpr int TOKENS = kTileRows * 128 / D;
-  __shared__ float s_w[16][kMaxGrid];
+  constexpr int GROUPS = kJoinThreads / D;
+  __shared__ float s_w[kJoinHeads][kMaxGrid];
+  __shared__ float s_sum[GROUPS][kJoinHeads][D];
   allow_next_grid();
   wait_prior_grid();
   const int c = (int)blockIdx.x + 1;
-  const int4 at = a.info[c], before = a.info[c - 1];   // sequence, item, first tile, tiles
-  if (at.w <= 0 || at.z == 0) return;          // an empty window, or a boundary between items
-  const bool same = before.x == at.x && before.y == at.y;
-  if (same && before.z > 0) return;            // an earlier boundary cuts this item
+  const Window at = a.info[c], before = a.info[c - 1];
+  if (at.tiles <= 0 || at.j == 0) return;      // an empty window, or a boundary between items
+  const bool same = before.b == at.b && before.item == at.item;
+  if (same && before.j > 0) return;            // an earlier boundary cuts this item
   // the parts: the segment of window c - 1 that ends there, then the first segments of
   // windows c .. last, last holding the item's final tile
-  const int64_t work = *a.total, windows = work < grid ? work : grid;
-  const int nt = (max(0, min(a.lens[at.x], a.max_seq_len)) + TOKENS - 1) / TOKENS;
-  const int64_t end = work * c / windows - at.z + nt;
-  const int last = (int)min((end * windows - 1) / work, windows - 1);
+  const int64_t windows = at.total < grid ? at.total : grid;
+  const int64_t end = at.total * c / windows - at.j + at.nt;
+  const int last = (int)min((end * windows - 1) / at.total, windows - 1);
   const int parts = last - c + 2;
-  const int h = at.y / a.chunks, G = a.Hq / a.H, g0 = (at.y - h * a.chunks) * a.hch;
-  const int gn = min(a.hch, G - g0);
+  const int h = at.item / a.chunks, G = a.Hq / a.H, g0 = (at.item - h * a.chunks) * a.hch;
+  const int first = (int)blockIdx.y * kJoinHeads;
+  const int n = min(min(a.hch, G - g0) - first, kJoinHeads);
+  if (n <= 0) return;
   const int64_t head = 2 * (int64_t)(c - 1) + (same ? 0 : 1);
-  auto row = [&](int k) { return (k == 0 ? head : 2 * (int64_t)(c + k - 1)) * a.hch; };
+  auto row = [&](int k) { return (k == 0 ? head : 2 * (int64_t)(c + k - 1)) * a.hch + first; };
+  const int d = threadIdx.x % D, group = threadIdx.x / D;
+  float x[kJoinAhead][kJoinHeads];
+#pragma unroll
+  for (int i = 0; i < kJoinAhead; ++i) {
+    const int k = group + i * GROUPS;
+#pragma unroll
+    for (int g = 0; g < kJoinHeads; ++g)
+      x[i][g] = k < parts && g < n ? a.ws_acc[(row(k) + g) * D + d] : 0.f;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < gn) {
+  if (warp < n) {
     float top = -CUDART_INF_F;
     for (int k = lane; k < parts; k += 32) {
       const float m = a.ws_m[row(k) + warp];
@@ -955,13 +980,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, i
     for (int k = lane; k < parts; k += 32) s_w[warp][k] *= inv;
   }
   __syncthreads();
-  const int d = threadIdx.x % D;
-  for (int g = threadIdx.x / D; g < gn; g += kJoinThreads / D) {
-    float y = s_w[g][0] * a.ws_acc[(row(0) + g) * D + d];
-#pragma unroll 8
-    for (int k = 1; k < parts; ++k)
-      y = fmaf(s_w[g][k], a.ws_acc[(2 * (int64_t)(c + k - 1) * a.hch + g) * D + d], y);
-    static_cast<uint16_t*>(a.out)[((int64_t)at.x * a.Hq + h * G + g0 + g) * D + d] =
+  float sum[kJoinHeads] = {};
+#pragma unroll
+  for (int i = 0; i < kJoinAhead; ++i) {
+    const int k = group + i * GROUPS;
+#pragma unroll
+    for (int g = 0; g < kJoinHeads; ++g)
+      if (k < parts && g < n) sum[g] = fmaf(s_w[g][k], x[i][g], sum[g]);
+  }
+#pragma unroll 4
+  for (int k = group + kJoinAhead * GROUPS; k < parts; k += GROUPS)
+#pragma unroll
+    for (int g = 0; g < kJoinHeads; ++g)
+      if (g < n) sum[g] = fmaf(s_w[g][k], a.ws_acc[(row(k) + g) * D + d], sum[g]);
+#pragma unroll
+  for (int g = 0; g < kJoinHeads; ++g) s_sum[group][g][d] = sum[g];
+  __syncthreads();
+  for (int g = group; g < n; g += GROUPS) {
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) y += s_sum[i][g][d];
+    static_cast<uint16_t*>(a.out)[((int64_t)at.b * a.Hq + h * G + g0 + first + g) * D + d] =
         a.dtype == PA_BFLOAT16 ? narrow<PA_BFLOAT16>(y) : narrow<PA_FLOAT16>(y);
   }
 }
@@ -1012,7 +1051,7 @@ Plan plan_of(int Hq, int H, int D, int max_seq_len) {
   p.tiles = ((int64_t)max_seq_len + tokens - 1) / tokens;
   auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
   const size_t rows = (size_t)2 * kMaxGrid * p.hch;
-  p.m_off = align(kMaxGrid * sizeof(int4) + sizeof(int64_t));
+  p.m_off = align(kMaxGrid * sizeof(Window));
   p.l_off = p.m_off + align(rows * sizeof(float));
   p.acc_off = p.l_off + align(rows * sizeof(float));
   p.total = p.acc_off + align(rows * D * sizeof(float));
@@ -1133,8 +1172,7 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.dtype = dtype;
   char* ws = static_cast<char*>(workspace);
-  a.info = reinterpret_cast<int4*>(ws);
-  a.total = reinterpret_cast<int64_t*>(ws + kMaxGrid * sizeof(int4));
+  a.info = reinterpret_cast<Window*>(ws);
   a.ws_m = reinterpret_cast<float*>(ws + p.m_off);
   a.ws_l = reinterpret_cast<float*>(ws + p.l_off);
   a.ws_acc = reinterpret_cast<float*>(ws + p.acc_off);
@@ -1148,7 +1186,7 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
                                   : launch_heads<64>(k, v, a, grid, device, stream);
   // an item of one tile is never cut
   if (e == cudaSuccess && p.tiles > 1 && grid > 1) {
-    const dim3 joins((unsigned)(grid - 1));
+    const dim3 joins((unsigned)(grid - 1), (unsigned)((p.hch + kJoinHeads - 1) / kJoinHeads));
     e = head_dim == 128
             ? launch_pdl(join_q8_kernel<128>, joins, kJoinThreads, 0, stream, a, grid)
             : launch_pdl(join_q8_kernel<64>, joins, kJoinThreads, 0, stream, a, grid);
