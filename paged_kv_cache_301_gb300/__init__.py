@@ -3,6 +3,8 @@
 Argument marshalling only: every computation runs in the library's CUDA
 kernels (or, for the block manager, its C++ host code).  Tensors are PyTorch
 tensors used as device buffers; the current CUDA stream is passed through.
+The calls of the 8-bit cache and the rotated writes are marshalled by a compiled
+module (_binding, csrc/pa_binding.cpp), the others by ctypes.
 """
 from __future__ import annotations
 
@@ -345,65 +347,17 @@ def alloc_cache_q8(num_blocks: int, num_kv_heads: int, block_size: int, head_dim
     return (*pools, *scales)
 
 
-def _on_current_device(where: str, *tensors) -> None:
-    """Every tensor (None aside) on the current CUDA device, where the launch goes."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{where}: every tensor must be on the current CUDA device")
+_native = None
 
 
-def _token_stride(t: torch.Tensor, where: str) -> int:
-    """Elements from token to token of [T, heads, D] with packed heads."""
-    T, H, D = t.shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (H > 1 and s1 != D):
-        raise ValueError(f"{where}: the heads of a token must be packed")
-    return s0 if T > 1 else 0
-
-
-def _int32(where: str, *tensors) -> None:
-    for t in tensors:
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
-            raise ValueError(f"{where}: index arrays are contiguous int32")
-
-
-def _check_q8(where, k_pool, v_pool, k_scale, v_scale):
-    if k_pool.dtype not in (E4M3, torch.uint8) or v_pool.dtype not in (E4M3, torch.uint8):
-        raise ValueError(f"{where}: 8-bit pools are float8_e4m3fn (or its bytes, uint8)")
-    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
-        raise ValueError(f"{where}: 8-bit pools are [NB, Hkv, bs, D], both alike")
-    if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or
-            k_scale.shape != k_pool.shape[:2] or v_scale.shape != k_pool.shape[:2]):
-        raise ValueError(f"{where}: scales are fp32 [num_blocks, num_kv_heads]")
-
-
-def _rope_args(where, q_out, q, key, value, cos_sin, block_tables, seq_lens, q_start, q_weight,
-               k_weight, positions):
-    """The checks both rotated writes share; (T, Hq, H, D, B, max_blocks, strides)."""
-    T, Hq, D = q.shape
-    H = key.shape[1]
-    B, MB = block_tables.shape
-    _on_current_device(where, q_out, q, key, value, cos_sin, block_tables, seq_lens, q_start,
-                       q_weight, k_weight, positions)
-    _int32(where, block_tables, seq_lens, q_start, positions)
-    if q_out.shape != q.shape or key.shape != (T, H, D) or value.shape != (T, H, D):
-        raise ValueError(f"{where}: q_out as q [T, Hq, D], key and value [T, Hkv, D]")
-    dt = q.dtype
-    if q_out.dtype != dt or key.dtype != dt or value.dtype != dt:
-        raise ValueError(f"{where}: q_out, q, key and value share one dtype")
-    for w in (q_weight, k_weight):
-        if w is not None and (w.shape != (D,) or w.dtype != dt):
-            raise ValueError(f"{where}: norm weights are [head_dim], of q's dtype")
-    if cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32):
-        raise ValueError(f"{where}: cos_sin is fp32 [max_position, rotary_dim]")
-    if (seq_lens.numel() != B or (q_start is not None and q_start.numel() != B + 1) or
-            (positions is not None and positions.numel() != T)):
-        raise ValueError(f"{where}: seq_lens [B], q_start [B + 1], positions [T]")
-    qs, ks, vs = _token_stride(q, where), _token_stride(key, where), _token_stride(value, where)
-    if ks != vs:
-        raise ValueError(f"{where}: key and value need the same token stride")
-    return T, Hq, H, D, B, MB, qs, ks
+def _bind():
+    """The compiled binding (built and loaded with libpagedattn.so)."""
+    global _native
+    if _native is None:
+        lib()
+        from . import _binding
+        _native = _binding
+    return _native
 
 
 def pa_rope_append(q_out: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -418,21 +372,10 @@ def pa_rope_append(q_out: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tens
     (see include/pagedattn.h, pa_rope_append).  q [T, Hq, D], key / value [T, Hkv, D]
     may be slices of one projection's output; q_start None: one token per sequence.
     cos_sin: rope_table(...), or None for no rotation."""
-    w = "pa_rope_append"
-    T, Hq, H, D, B, MB, qs, ks = _rope_args(w, q_out, q, key, value, cos_sin, block_tables,
-                                            seq_lens, q_start, q_weight, k_weight, positions)
-    NB, bs, Hp, Dp = k_pool.shape
-    _on_current_device(w, k_pool, v_pool, status)
-    if (v_pool.shape != k_pool.shape or Hp != H or Dp != D or k_pool.dtype != q.dtype or
-            v_pool.dtype != q.dtype):
-        raise ValueError(f"{w}: pools are [NB, bs, Hkv, D] of q's dtype")
-    P, R = cos_sin.shape if cos_sin is not None else (0, 0)
-    st = lib().pa_rope_append(
-        _ptr(q_out), _ptr(k_pool), _ptr(v_pool), q.data_ptr(), key.data_ptr(), value.data_ptr(),
-        _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin), P, R, int(interleaved),
-        _ptr(positions), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), B, T, qs, ks, Hq, H,
-        D, bs, MB, NB, _dtype(q), _ptr(status), _stream(stream))
-    _check(st, w)
+    st = (_native or _bind()).rope_append(
+        q_out, k_pool, v_pool, q, key, value, cos_sin, block_tables, seq_lens, q_start, q_weight,
+        k_weight, eps, interleaved, positions, status, stream)
+    _check(st, "pa_rope_append")
     return q_out
 
 
@@ -447,21 +390,10 @@ def pa_rope_append_q8(q_out: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.T
                       status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_rope_append into the 8-bit cache (see include/pagedattn.h): pools
     [NB, Hkv, bs, D] of e4m3 codes, scales [NB, Hkv] fp32 (alloc_cache_q8)."""
-    w = "pa_rope_append_q8"
-    T, Hq, H, D, B, MB, qs, ks = _rope_args(w, q_out, q, key, value, cos_sin, block_tables,
-                                            seq_lens, q_start, q_weight, k_weight, positions)
-    _check_q8(w, k_pool, v_pool, k_scale, v_scale)
-    NB, Hp, bs, Dp = k_pool.shape
-    _on_current_device(w, k_pool, v_pool, k_scale, v_scale, status)
-    if Hp != H or Dp != D:
-        raise ValueError(f"{w}: pools are [NB, Hkv, bs, D]")
-    P, R = cos_sin.shape if cos_sin is not None else (0, 0)
-    st = lib().pa_rope_append_q8(
-        _ptr(q_out), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), q.data_ptr(),
-        key.data_ptr(), value.data_ptr(), _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin), P,
-        R, int(interleaved), _ptr(positions), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start),
-        B, T, qs, ks, Hq, H, D, bs, MB, NB, _dtype(q), _ptr(status), _stream(stream))
-    _check(st, w)
+    st = (_native or _bind()).rope_append_q8(
+        q_out, k_pool, v_pool, k_scale, v_scale, q, key, value, cos_sin, block_tables, seq_lens,
+        q_start, q_weight, k_weight, eps, interleaved, positions, status, stream)
+    _check(st, "pa_rope_append_q8")
     return q_out
 
 
@@ -482,27 +414,12 @@ def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_poo
                  status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Decode attention over the 8-bit cache (see include/pagedattn.h, pa_decode_q8).
     max_seq_len and workspace default as in pa_decode."""
-    w = "pa_decode_q8"
-    B, Hq, D = q.shape
-    _check_q8(w, k_pool, v_pool, k_scale, v_scale)
-    NB, H, bs, Dp = k_pool.shape
-    MB = block_tables.shape[1]
-    _on_current_device(w, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens,
-                       workspace, status)
-    _int32(w, block_tables, seq_lens)
-    if (out.shape != q.shape or out.dtype != q.dtype or Dp != D or
-            block_tables.shape[0] != B or seq_lens.numel() != B):
-        raise ValueError(f"{w}: out as q [B, Hq, D], block_tables [B, MB], seq_lens [B]")
-    if max_seq_len is None:
-        max_seq_len = MB * bs
     if workspace is None:
-        workspace = workspace_for_q8(q, k_pool, max_seq_len)
-    st = lib().pa_decode_q8(
-        _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_tables), _ptr(seq_lens), B, Hq, H, D, bs, MB, NB, int(max_seq_len),
-        float(scale), _dtype(q), _ptr(workspace), workspace.numel(), _ptr(status),
-        _stream(stream))
-    _check(st, w)
+        most = block_tables.shape[1] * k_pool.shape[2] if max_seq_len is None else max_seq_len
+        workspace = workspace_for_q8(q, k_pool, most)
+    st = (_native or _bind()).decode_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                                        seq_lens, scale, max_seq_len, workspace, status, stream)
+    _check(st, "pa_decode_q8")
     return out
 
 
@@ -512,20 +429,9 @@ def pa_expand_blocks_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_pool8: tor
                         stream=None) -> None:
     """Blocks of the 8-bit cache to blocks of 16-bit pools [NB', bs, Hkv, D]
     (see include/pagedattn.h); block_pairs [n, 2] int32 (src, dst)."""
-    w = "pa_expand_blocks_q8"
-    _check_q8(w, k_pool8, v_pool8, k_scale, v_scale)
-    _on_current_device(w, k_pool, v_pool, k_pool8, v_pool8, k_scale, v_scale, block_pairs, status)
-    _int32(w, block_pairs)
-    NB8, H, bs, D = k_pool8.shape
-    if (k_pool.shape != v_pool.shape or k_pool.shape[1:] != (bs, H, D) or
-            k_pool.dtype != v_pool.dtype):
-        raise ValueError(f"{w}: 16-bit pools are [NB', bs, Hkv, D]")
-    n = block_pairs.shape[0] if block_pairs.numel() else 0
-    st = lib().pa_expand_blocks_q8(
-        _ptr(k_pool), _ptr(v_pool), _ptr(k_pool8), _ptr(v_pool8), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_pairs) if n else None, n, H, D, bs, NB8, k_pool.shape[0], _dtype(k_pool),
-        _ptr(status), _stream(stream))
-    _check(st, w)
+    st = (_native or _bind()).expand_blocks_q8(k_pool, v_pool, k_pool8, v_pool8, k_scale, v_scale,
+                                               block_pairs, status, stream)
+    _check(st, "pa_expand_blocks_q8")
 
 
 def pa_stream_read(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, stream=None) -> None:
