@@ -110,60 +110,78 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
                     narrow2<DT>(x[6], x[7]));
 }
 
-// Norm and rotation of the 8 elements [8 li, 8 li + 8) of a head row of D, shared
-// by the D/8 lanes of a group.  Called by whole warps (it shuffles) whose groups
-// may hold rows of different kinds: weight and angles are the group's own and
-// null where its row is not normed / not rotated; any_norm is the warp's.
-// angles: the position's row of cos_sin, R/2 cosines, then R/2 sines.
+// RMS norm of a head row of D, 8 elements to each of its group's D/8 lanes.  Called by
+// whole warps (it shuffles); `on`: the group's row is normed, by weight's 8 elements.
 template <int DT, int D>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], bool any_norm, const void* weight,
-                                            float eps, const float* angles, int R,
-                                            int interleaved, int li) {
-  constexpr int TG = D / 8;
-  if (any_norm) {
-    float ss = 0.f;
+__device__ __forceinline__ void norm(float (&x)[8], bool on, const uint4& weight, float eps) {
+  float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-    for (int o = TG / 2; o; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
-    if (weight) {
-      const float r = rsqrtf(ss * (1.f / D) + eps);
-      float w[8];
-      widen8<DT>(reinterpret_cast<const uint4*>(weight)[li], w);
+  for (int o = D / 16; o; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
+  if (on) {
+    const float r = rsqrtf(ss * (1.f / D) + eps);
+    float w[8];
+    widen8<DT>(weight, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-    }
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
   }
+}
+
+// A lane's part of a position's angles: cosines and sines of its 8 elements' pairs
+// (4 pairs when they are neighbours).
+struct Turn {
+  float4 c[2], s[2];
+};
+
+// angles: the position's row of cos_sin, R/2 cosines, then R/2 sines.
+__device__ __forceinline__ Turn load_turn(const float* angles, int R, int interleaved, int li) {
+  Turn t = {};
+  const float4* c = reinterpret_cast<const float4*>(angles);
+  const float4* s = reinterpret_cast<const float4*>(angles + R / 2);
   if (interleaved) {
-    if (angles && li * 8 < R) {
-      const float4 c = reinterpret_cast<const float4*>(angles)[li];
-      const float4 s = reinterpret_cast<const float4*>(angles + R / 2)[li];
-      const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+    if (li * 8 < R) {
+      t.c[0] = c[li];
+      t.s[0] = s[li];
+    }
+  } else if (li * 8 < R) {
+    const int at = (li < R / 16 ? li : li - R / 16) * 2;
+    t.c[0] = c[at];
+    t.c[1] = c[at + 1];
+    t.s[0] = s[at];
+    t.s[1] = s[at + 1];
+  }
+  return t;
+}
+
+// Rotation of a group's row; called by whole warps (it shuffles); `on`: the group's
+// row is rotated.
+__device__ __forceinline__ void rotate(float (&x)[8], bool on, const Turn& t, int R,
+                                       int interleaved, int li) {
+  const float c[8] = {t.c[0].x, t.c[0].y, t.c[0].z, t.c[0].w, t.c[1].x, t.c[1].y, t.c[1].z, t.c[1].w};
+  const float s[8] = {t.s[0].x, t.s[0].y, t.s[0].z, t.s[0].w, t.s[1].x, t.s[1].y, t.s[1].z, t.s[1].w};
+  on = on && li * 8 < R;
+  if (interleaved) {
+    if (on) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p = x[2 * i], q = x[2 * i + 1];
-        x[2 * i] = p * cc[i] - q * sn[i];
-        x[2 * i + 1] = q * cc[i] + p * sn[i];
+        x[2 * i] = p * c[i] - q * s[i];
+        x[2 * i + 1] = q * c[i] + p * s[i];
       }
     }
   } else if (R > 0) {
     const int half = R / 16;                     // lanes that hold half the rotated part
-    const bool first = li < half, second = !first && li < 2 * half;
-    const int partner = first ? li + half : (second ? li - half : li);
+    const bool first = li < half;
+    const int partner = li * 8 < R ? (first ? li + half : li - half) : li;
     const int base = (threadIdx.x & 31) - li;    // first lane of the group
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(kAll, x[i], base + partner);
-    if (angles && (first || second)) {
-      const int at = first ? li : partner;
-      const float4* cp = reinterpret_cast<const float4*>(angles) + at * 2;
-      const float4* sp = reinterpret_cast<const float4*>(angles + R / 2) + at * 2;
-      const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
-      const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-      const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    if (on) {
       const float sign = first ? -1.f : 1.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * cc[i] + sign * (y[i] * sn[i]);
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + sign * (y[i] * s[i]);
     }
   }
 }
@@ -182,12 +200,33 @@ __device__ __forceinline__ const float* angles_of(const RopeArgs& a, int t, int 
 
 // All rows of token t, by one CTA of NT threads: row r < Hq is query head r; with
 // KV16 the keys and values of the 16-bit cache follow.  Groups of D/8 lanes take
-// rows in turn, U at a time so that their loads overlap.
+// rows in turn, U at a time so that their loads overlap; the first ones, and the
+// norms' weights, are asked for before the token's place is looked up, and the
+// token's angles once for all of a thread's rows.
 template <int DT, int D, int NT, bool KV16>
 __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
   constexpr int TG = D / 8, NG = NT / TG, U = 3;
   const int lane = threadIdx.x & 31, li = threadIdx.x % TG, grp = threadIdx.x / TG;
   const int rows = KV16 ? a.Hq + 2 * a.H : a.Hq;
+  const uint4* q = reinterpret_cast<const uint4*>(a.q) + t * (a.q_stride / 8);
+  const uint4* key = reinterpret_cast<const uint4*>(a.key) + t * (a.kv_stride / 8);
+  const uint4* value = reinterpret_cast<const uint4*>(a.value) + t * (a.kv_stride / 8);
+  uint4 w[U];
+  auto load_rows = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * NG + grp;
+      w[u] = make_uint4(0, 0, 0, 0);
+      if (r < a.Hq) w[u] = q[r * TG + li];
+      else if (KV16 && r < a.Hq + a.H) w[u] = key[(r - a.Hq) * TG + li];
+      else if (KV16 && r < rows) w[u] = value[(r - a.Hq - a.H) * TG + li];
+    }
+  };
+  load_rows(0);
+  uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
+  if (a.q_weight) qw = reinterpret_cast<const uint4*>(a.q_weight)[li];
+  if (KV16 && a.k_weight) kw = reinterpret_cast<const uint4*>(a.k_weight)[li];
+
   const int b = a.q_start ? find_seq(a.q_start, a.B, t, lane) : t;
   bool bad;
   const Place at = place_of(a, b, t, &bad);
@@ -197,34 +236,27 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
     if ((bad || at.ok) && threadIdx.x == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
     return;
   }
+  Turn turn = {};
+  if (angles) turn = load_turn(angles, a.rotary, a.interleaved, li);
   int64_t slot = -1;
   if (KV16) {
     const int32_t blk = a.tables[(int64_t)b * a.max_blocks + at.pos / a.bs];
     if (blk >= 0 && blk < a.num_blocks) slot = (int64_t)blk * a.bs + at.pos % a.bs;
     else if (threadIdx.x == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
   }
-  const uint4* q = reinterpret_cast<const uint4*>(a.q) + t * (a.q_stride / 8);
-  const uint4* key = reinterpret_cast<const uint4*>(a.key) + t * (a.kv_stride / 8);
-  const uint4* value = reinterpret_cast<const uint4*>(a.value) + t * (a.kv_stride / 8);
-  const bool any_norm = a.q_weight || a.k_weight;
-  for (int r0 = 0; r0 < rows; r0 += NG * U) {
-    uint4 w[U];
+  const bool any_norm = a.q_weight || (KV16 && a.k_weight);
+  for (int r0 = 0;;) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 + u * NG + grp;
-      w[u] = make_uint4(0, 0, 0, 0);
-      if (r < a.Hq) w[u] = q[r * TG + li];
-      else if (KV16 && r < a.Hq + a.H) w[u] = key[(r - a.Hq) * TG + li];
-      else if (KV16 && r < rows) w[u] = value[(r - a.Hq - a.H) * TG + li];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * NG + grp;
+      if (r0 + u * NG >= rows) break;
       const bool is_q = r < a.Hq, is_k = KV16 && !is_q && r < a.Hq + a.H;
       float x[8];
       widen8<DT>(w[u], x);
-      norm_rotate<DT, D>(x, any_norm, is_q ? a.q_weight : (is_k ? a.k_weight : nullptr), a.eps,
-                         is_q || is_k ? angles : nullptr, a.rotary, a.interleaved, li);
+      if (any_norm)
+        norm<DT, D>(x, is_q ? a.q_weight != nullptr : is_k && a.k_weight != nullptr, is_q ? qw : kw,
+                    a.eps);
+      rotate(x, is_q || is_k, turn, a.rotary, a.interleaved, li);
       if (is_q) {
         reinterpret_cast<uint4*>(a.q_out)[((int64_t)t * a.Hq + r) * TG + li] = narrow8<DT>(x);
       } else if (is_k) {
@@ -234,6 +266,9 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
         reinterpret_cast<uint4*>(a.v_pool)[(slot * a.H + (r - a.Hq - a.H)) * TG + li] = w[u];
       }
     }
+    r0 += NG * U;
+    if (r0 >= rows) break;
+    load_rows(r0);
   }
 }
 
@@ -298,24 +333,30 @@ __device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int
   uint4 vw[RPT];
   bool live[RPT];
   float km = 0.f, vm = 0.f;
+  uint4 weight = make_uint4(0, 0, 0, 0), kw[RPT];
+  if (a.k_weight) weight = reinterpret_cast<const uint4*>(a.k_weight)[li];
 #pragma unroll
   for (int u = 0; u < RPT; ++u) {
     const int row = grp + u * NG, t = t0 + row - r0;
     live[u] = row >= r0 && row < r1;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    vw[u] = w;
-    const float* angles = nullptr;
+    kw[u] = vw[u] = make_uint4(0, 0, 0, 0);
     if (live[u]) {
-      angles = angles_of(a, t, j * BS + row, &live[u]);
-      if (!live[u] && li == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-    }
-    if (live[u]) {
-      w = reinterpret_cast<const uint4*>(a.key)[t * (a.kv_stride / 8) + h * TG + li];
+      kw[u] = reinterpret_cast<const uint4*>(a.key)[t * (a.kv_stride / 8) + h * TG + li];
       vw[u] = reinterpret_cast<const uint4*>(a.value)[t * (a.kv_stride / 8) + h * TG + li];
     }
-    widen8<DT>(w, kx[u]);
-    norm_rotate<DT, D>(kx[u], a.k_weight != nullptr, a.k_weight, a.eps, angles, a.rotary,
-                       a.interleaved, li);
+  }
+#pragma unroll
+  for (int u = 0; u < RPT; ++u) {
+    const int row = grp + u * NG, t = t0 + row - r0;
+    Turn turn = {};
+    if (live[u]) {
+      const float* angles = angles_of(a, t, j * BS + row, &live[u]);
+      if (angles) turn = load_turn(angles, a.rotary, a.interleaved, li);
+      if (!live[u] && li == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+    }
+    widen8<DT>(kw[u], kx[u]);
+    if (a.k_weight) norm<DT, D>(kx[u], true, weight, a.eps);
+    rotate(kx[u], true, turn, a.rotary, a.interleaved, li);
     if (live[u]) {
       float vx[8];
       widen8<DT>(vw[u], vx);
@@ -435,6 +476,8 @@ rope_step_q8_kernel(const RopeArgs a, int kv_ctas) {
   uint4 w = make_uint4(0, 0, 0, 0);
   if (in)
     w = reinterpret_cast<const uint4*>(is_v ? a.value : a.key)[b * (a.kv_stride / 8) + h * TG + li];
+  uint4 weight = make_uint4(0, 0, 0, 0);
+  if (a.k_weight) weight = reinterpret_cast<const uint4*>(a.k_weight)[li];
   bool bad = false;
   Place at = {0, 0, 0};
   if (in) at = place_of(a, b, b, &bad);
@@ -450,10 +493,12 @@ rope_step_q8_kernel(const RopeArgs a, int kv_ctas) {
   const int64_t tile = (int64_t)blk * a.H + h;
   float* scale = (is_v ? a.v_scale : a.k_scale) + tile;
   const float old = ok && row > 0 ? *scale : 0.f;
+  Turn turn = {};
+  if (angles && !is_v) turn = load_turn(angles, a.rotary, a.interleaved, li);
   float x[8];
   widen8<DT>(w, x);
-  norm_rotate<DT, D>(x, a.k_weight != nullptr, is_v ? nullptr : a.k_weight, a.eps,
-                     is_v ? nullptr : angles, a.rotary, a.interleaved, li);
+  if (a.k_weight) norm<DT, D>(x, !is_v, weight, a.eps);
+  rotate(x, !is_v, turn, a.rotary, a.interleaved, li);
   float m = mag8(x);
 #pragma unroll
   for (int o = TG / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
