@@ -16,6 +16,7 @@
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_q8.cuh"
+#include "pa_sm100.cuh"
 
 namespace pa {
 namespace {
@@ -198,14 +199,14 @@ __device__ __forceinline__ const float* angles_of(const RopeArgs& a, int t, int 
   return a.cos_sin + (int64_t)pos * a.rotary;
 }
 
-// All rows of token t, by one CTA of NT threads: row r < Hq is query head r; with
+// All rows of token t, by one CTA: row r < Hq is query head r; with
 // KV16 the keys and values of the 16-bit cache follow.  Groups of D/8 lanes take
 // rows in turn, U at a time so that their loads overlap; the first ones, and the
 // norms' weights, are asked for before the token's place is looked up, and the
 // token's angles once for all of a thread's rows.
-template <int DT, int D, int NT, bool KV16>
+template <int DT, int D, bool KV16>
 __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
-  constexpr int TG = D / 8, NG = NT / TG, U = 3;
+  constexpr int TG = D / 8, NG = kRowThreads / TG, U = 3;
   const int lane = threadIdx.x & 31, li = threadIdx.x % TG, grp = threadIdx.x / TG;
   const int rows = KV16 ? a.Hq + 2 * a.H : a.Hq;
   const uint4* q = reinterpret_cast<const uint4*>(a.q) + t * (a.q_stride / 8);
@@ -272,12 +273,187 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
   }
 }
 
+// ---------------------------------------------------------------- many tokens --
+// One CTA takes a run of tokens through a ring of shared-memory stages: bulk copies
+// bring a token's rows in (one contiguous copy each for q, key and value), the
+// threads norm and rotate them in place, bulk copies take them out (values without
+// passing through registers).  Reads of later tokens and writes of earlier ones are
+// in flight all the time, which the register kernel above cannot hold at the
+// occupancy its angles leave it.
+constexpr int kMaxStages = 4;
+constexpr int kPlaced = kRowThreads;           // tokens placed at once, one per thread
+constexpr int kStreamTokens = 8;               // tokens per SM from which on it is taken
+constexpr uint64_t kStreamLimitNs = 2000000000ull;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          sm100::smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(sm100::smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(sm100::smem_addr(src)), "r"(bytes)
+               : "memory");
+}
+
+// The place of one thread's token: a binary search for its sequence.
+__device__ __forceinline__ Place place_token(const RopeArgs& a, int t, bool* bad) {
+  int b = t;
+  if (a.q_start) {
+    int lo = 0, hi = a.B;                      // the boundaries at or before t: [lo, hi]
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      if (a.q_start[mid + 1] <= t) lo = mid + 1;
+      else hi = mid;
+    }
+    b = lo;
+  }
+  return place_of(a, b, t, bad);
+}
+
+// Tokens [total_q cta / ctas, total_q (cta + 1) / ctas).
+template <int DT, int D, bool KV16>
+__device__ __forceinline__ void stream_rows(const RopeArgs& a, int cta, int ctas, int stages,
+                                            uint8_t* ring) {
+  constexpr int TG = D / 8, NG = kRowThreads / TG;
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  __shared__ int64_t s_slot[kPlaced];          // pool row of the token (-1: none)
+  __shared__ int s_pos[kPlaced];               // row of cos_sin (-1: leave the token alone)
+  const int tid = threadIdx.x, li = tid % TG, grp = tid / TG;
+  const int t0 = (int)((int64_t)a.total_q * cta / ctas);
+  const int n = (int)((int64_t)a.total_q * (cta + 1) / ctas) - t0;
+  const uint32_t q_bytes = (uint32_t)(a.Hq * D * 2), kv_bytes = KV16 ? (uint32_t)(a.H * D * 2) : 0;
+  const uint32_t stage_bytes = q_bytes + 2 * kv_bytes;
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) sm100::mbar_init(&full[i], 1);
+    sm100::fence_mbar_init();
+  }
+  __syncthreads();
+  auto fetch = [&](int i) {                    // thread 0
+    uint8_t* to = ring + (uint32_t)(i % stages) * stage_bytes;
+    uint64_t* bar = &full[i % stages];
+    const int64_t t = t0 + i;
+    sm100::mbar_arrive_expect_tx(bar, stage_bytes);
+    bulk_load(to, static_cast<const uint16_t*>(a.q) + t * a.q_stride, q_bytes, bar);
+    if (KV16) {
+      bulk_load(to + q_bytes, static_cast<const uint16_t*>(a.key) + t * a.kv_stride, kv_bytes, bar);
+      bulk_load(to + q_bytes + kv_bytes, static_cast<const uint16_t*>(a.value) + t * a.kv_stride,
+                kv_bytes, bar);
+    }
+  };
+  if (tid == 0)
+    for (int i = 0; i < min(stages, n); ++i) fetch(i);
+  uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
+  if (a.q_weight) qw = reinterpret_cast<const uint4*>(a.q_weight)[li];
+  if (KV16 && a.k_weight) kw = reinterpret_cast<const uint4*>(a.k_weight)[li];
+  const bool any_norm = a.q_weight || (KV16 && a.k_weight);
+  const int turned = KV16 ? a.Hq + a.H : a.Hq;
+  Turn turn = {}, next = {};
+  auto turn_of = [&](int i) {
+    const int pos = s_pos[i % kPlaced];
+    if (a.rotary && pos >= 0)
+      next = load_turn(a.cos_sin + (int64_t)pos * a.rotary, a.rotary, a.interleaved, li);
+  };
+  bool late = false;
+  int fetched = min(stages, n);                // thread 0
+  for (int i = 0; i < n; ++i) {
+    if (i % kPlaced == 0) {                    // the next tokens' places
+      if (i > 0) __syncthreads();
+      const int t = t0 + i + tid;
+      int64_t slot = -1;
+      int pos = -1;
+      if (i + tid < n) {
+        bool bad;
+        const Place at = place_token(a, t, &bad);
+        bool ok = at.ok;
+        if (ok) angles_of(a, t, at.pos, &ok);
+        if (bad || (at.ok && !ok)) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+        if (ok) {
+          pos = a.rotary && a.positions ? a.positions[t] : at.pos;
+          if (KV16) {
+            const int32_t blk = a.tables[(int64_t)at.b * a.max_blocks + at.pos / a.bs];
+            if (blk >= 0 && blk < a.num_blocks) slot = (int64_t)blk * a.bs + at.pos % a.bs;
+            else report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+          }
+        }
+      }
+      s_slot[tid] = slot;
+      s_pos[tid] = pos;
+      __syncthreads();
+      turn_of(i);
+    }
+    turn = next;
+    if (i + 1 < n && (i + 1) % kPlaced != 0) turn_of(i + 1);
+    const bool live = s_pos[i % kPlaced] >= 0;
+    uint8_t* stage = ring + (uint32_t)(i % stages) * stage_bytes;
+    late = !sm100::mbar_try_wait(&full[i % stages], (i / stages) & 1) &&
+           !sm100::mbar_wait_drain(&full[i % stages], (i / stages) & 1, kStreamLimitNs);
+    if (live && !late) {
+      for (int r0 = 0; r0 < turned; r0 += NG) {
+        const int r = r0 + grp;
+        uint4* at = reinterpret_cast<uint4*>(stage) + r * TG + li;
+        const bool is_q = r < a.Hq, in = r < turned;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (in) w = *at;
+        float x[8];
+        widen8<DT>(w, x);
+        if (any_norm)
+          norm<DT, D>(x, is_q ? a.q_weight != nullptr : KV16 && a.k_weight != nullptr,
+                      is_q ? qw : kw, a.eps);
+        rotate(x, true, turn, a.rotary, a.interleaved, li);
+        if (in) *at = narrow8<DT>(x);
+      }
+    }
+    sm100::fence_async_smem();
+    if (__syncthreads_or(late)) {
+      late = true;
+      break;
+    }
+    if (tid == 0) {
+      if (live) {
+        bulk_store(static_cast<uint16_t*>(a.q_out) + (int64_t)(t0 + i) * a.Hq * D, stage, q_bytes);
+        const int64_t slot = s_slot[i % kPlaced];
+        if (KV16 && slot >= 0) {
+          bulk_store(static_cast<uint16_t*>(a.k_pool) + slot * a.H * D, stage + q_bytes, kv_bytes);
+          bulk_store(static_cast<uint16_t*>(a.v_pool) + slot * a.H * D, stage + q_bytes + kv_bytes,
+                     kv_bytes);
+        }
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      // the stage of the token before has been read out: the next one comes in
+      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      if (i > 0 && fetched < n) fetch(fetched++);
+    }
+  }
+  if (tid == 0) {
+    if (late) {                                // copies in flight land before the CTA ends
+      report(a.status_dev, PA_ERR_TIMEOUT);
+      for (int j = max(0, fetched - stages); j < fetched; ++j)
+        sm100::mbar_wait_drain(&full[j % stages], (j / stages) & 1, kStreamLimitNs);
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+}
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads)
 rope_append_kernel(const RopeArgs a) {
   allow_next_grid();
   wait_prior_grid();
-  token_rows<DT, D, kRowThreads, true>(a, (int)blockIdx.x);
+  token_rows<DT, D, true>(a, (int)blockIdx.x);
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kRowThreads, 4)
+rope_stream_kernel(const RopeArgs a, int stages) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  allow_next_grid();
+  wait_prior_grid();
+  stream_rows<DT, D, true>(a, (int)blockIdx.x, (int)gridDim.x, stages, ring);
 }
 
 // Bring older codes to a larger scale: 8 codes times `ratio`, rounded once more
@@ -302,66 +478,82 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
                     e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
-// The new rows of one block of one KV head, [r0, r1), tokens t0 .. of sequence b,
-// by a CTA of NT threads: group g holds rows g, g + NG, ...  All older rows are
-// below r0.  Both pools in one go.
-template <int DT, int D, int BS, int NT>
-__device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int h, int t0, int r0,
+// The new rows [r0, r1) of block j of sequence b, tokens t0 .., for the KV heads from
+// h0 on that the CTA's threads cover: a head has kHead threads, whose groups hold
+// rows g, g + NG, ...  All older rows are below r0.  Keys are normed and rotated
+// twice, for the largest magnitude and for the codes: the raw rows take a quarter
+// of the registers.
+template <int DT, int D, int BS>
+struct BlockShape {
+  static constexpr int TG = D / 8;
+  static constexpr int kHead = BS * TG < kRowThreads ? BS * TG : kRowThreads;
+  static constexpr int kHeads = kRowThreads / kHead;      // heads of a CTA
+  static constexpr int NG = kHead / TG, RPT = BS / NG;    // groups, rows of each
+};
+
+template <int DT, int D, int BS>
+__device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int h0, int t0, int r0,
                                             int r1) {
-  constexpr int TG = D / 8, NG = NT / TG, RPT = BS / NG, NW = NT / 32;
-  static_assert(RPT * NG == BS, "the groups cover a block's rows evenly");
-  __shared__ float s_mag[NW][2];
-  __shared__ int s_live;
+  using S = BlockShape<DT, D, BS>;
+  constexpr int TG = S::TG, NG = S::NG, RPT = S::RPT, NW = S::kHead / 32;
+  __shared__ float s_mag[kRowThreads / 32][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int li = threadIdx.x % TG, grp = threadIdx.x / TG;
+  const int mine = threadIdx.x / S::kHead, h = h0 + mine;
+  const int li = threadIdx.x % TG, grp = threadIdx.x % S::kHead / TG;
   const int32_t blk = a.tables[(int64_t)b * a.max_blocks + j];
   if (blk < 0 || blk >= a.num_blocks) {
     if (threadIdx.x == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
     return;
   }
+  const bool in = h < a.H;
   const int64_t tile = (int64_t)blk * a.H + h;
   uint2* kc = static_cast<uint2*>(a.k_pool) + tile * (BS * D / 8);
   uint2* vc = static_cast<uint2*>(a.v_pool) + tile * (BS * D / 8);
-  float k_old = 0.f, v_old = 0.f;
-  if (r0 > 0) {
-    k_old = a.k_scale[tile];
-    v_old = a.v_scale[tile];
-  }
-  __syncthreads();                    // the last block's s_mag and s_live are read
-  if (threadIdx.x == 0) s_live = 0;
-  float kx[RPT][8];
-  uint4 vw[RPT];
-  bool live[RPT];
-  float km = 0.f, vm = 0.f;
-  uint4 weight = make_uint4(0, 0, 0, 0), kw[RPT];
-  if (a.k_weight) weight = reinterpret_cast<const uint4*>(a.k_weight)[li];
+  uint4 weight = make_uint4(0, 0, 0, 0), kw[RPT], vw[RPT];
+  const float* angles[RPT];
+  bool live[RPT], any = false;
 #pragma unroll
   for (int u = 0; u < RPT; ++u) {
     const int row = grp + u * NG, t = t0 + row - r0;
-    live[u] = row >= r0 && row < r1;
+    live[u] = in && row >= r0 && row < r1;
     kw[u] = vw[u] = make_uint4(0, 0, 0, 0);
     if (live[u]) {
       kw[u] = reinterpret_cast<const uint4*>(a.key)[t * (a.kv_stride / 8) + h * TG + li];
       vw[u] = reinterpret_cast<const uint4*>(a.value)[t * (a.kv_stride / 8) + h * TG + li];
     }
   }
+  if (a.k_weight) weight = reinterpret_cast<const uint4*>(a.k_weight)[li];
+  float k_old = 0.f, v_old = 0.f;
+  if (in && r0 > 0) {
+    k_old = a.k_scale[tile];
+    v_old = a.v_scale[tile];
+  }
 #pragma unroll
   for (int u = 0; u < RPT; ++u) {
-    const int row = grp + u * NG, t = t0 + row - r0;
-    Turn turn = {};
+    const int row = grp + u * NG;
+    angles[u] = nullptr;
     if (live[u]) {
-      const float* angles = angles_of(a, t, j * BS + row, &live[u]);
-      if (angles) turn = load_turn(angles, a.rotary, a.interleaved, li);
+      angles[u] = angles_of(a, t0 + row - r0, j * BS + row, &live[u]);
       if (!live[u] && li == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
     }
-    widen8<DT>(kw[u], kx[u]);
-    if (a.k_weight) norm<DT, D>(kx[u], true, weight, a.eps);
-    rotate(kx[u], true, turn, a.rotary, a.interleaved, li);
+    any |= live[u];
+  }
+  auto new_key = [&](int u, float (&x)[8]) {   // whole warps
+    Turn turn = {};
+    if (angles[u]) turn = load_turn(angles[u], a.rotary, a.interleaved, li);
+    widen8<DT>(kw[u], x);
+    if (a.k_weight) norm<DT, D>(x, true, weight, a.eps);
+    rotate(x, true, turn, a.rotary, a.interleaved, li);
+  };
+  float km = 0.f, vm = 0.f;
+#pragma unroll
+  for (int u = 0; u < RPT; ++u) {
+    float x[8], y[8];
+    new_key(u, x);
+    widen8<DT>(vw[u], y);
     if (live[u]) {
-      float vx[8];
-      widen8<DT>(vw[u], vx);
-      km = fmaxf(km, mag8(kx[u]));
-      vm = fmaxf(vm, mag8(vx));
+      km = fmaxf(km, mag8(x));
+      vm = fmaxf(vm, mag8(y));
     }
   }
 #pragma unroll
@@ -369,61 +561,63 @@ __device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int
     km = fmaxf(km, __shfl_xor_sync(kAll, km, o));
     vm = fmaxf(vm, __shfl_xor_sync(kAll, vm, o));
   }
-  __syncthreads();                    // s_live is reset
+  __syncthreads();                    // the last block's s_mag is read
   if (lane == 0) {
     s_mag[warp][0] = km;
     s_mag[warp][1] = vm;
   }
-#pragma unroll
-  for (int u = 0; u < RPT; ++u)
-    if (live[u]) s_live = 1;
-  __syncthreads();
-  if (!s_live) return;
+  if (!__syncthreads_or(any)) return; // no row left to write: scales stay
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    km = fmaxf(km, s_mag[w][0]);
-    vm = fmaxf(vm, s_mag[w][1]);
+    km = fmaxf(km, s_mag[mine * NW + w][0]);
+    vm = fmaxf(vm, s_mag[mine * NW + w][1]);
   }
   const float ks = fmaxf(k_old, scale_for(km)), vs = fmaxf(v_old, scale_for(vm));
   const float k_inv = 1.f / ks, v_inv = 1.f / vs;
 #pragma unroll
   for (int u = 0; u < RPT; ++u) {
     const int row = grp + u * NG;
+    float x[8], y[8];
+    new_key(u, x);
     if (live[u]) {
-      float vx[8];
-      widen8<DT>(vw[u], vx);
-      kc[row * TG + li] = quantise8(kx[u], k_inv);
-      vc[row * TG + li] = quantise8(vx, v_inv);
-    } else if (row < r0) {
+      widen8<DT>(vw[u], y);
+      kc[row * TG + li] = quantise8(x, k_inv);
+      vc[row * TG + li] = quantise8(y, v_inv);
+    } else if (in && row < r0) {
       if (ks > k_old) rescale8(kc + row * TG + li, k_old * k_inv);
       if (vs > v_old) rescale8(vc + row * TG + li, v_old * v_inv);
     }
   }
-  if (threadIdx.x == 0) {
+  if (in && threadIdx.x % S::kHead == 0) {
     a.k_scale[tile] = ks;
     a.v_scale[tile] = vs;
   }
 }
 
-// Prompts and chunks.  CTAs [0, kv_ctas) hold a window of kWindow tokens and one
-// KV head each, and write the blocks whose first new token lies in the window;
-// the others hold one token's query rows.
-constexpr int kWindow = 8;
-
-template <int DT, int D, int BS, int NT>
-__global__ void __launch_bounds__(NT)
-rope_append_q8_kernel(const RopeArgs a, int kv_ctas) {
+// Prompts and chunks.  CTAs [0, kv_ctas) hold a window of tokens (32 at most) and the
+// KV heads their threads cover, and write the blocks whose first new token lies in
+// the window; the others hold query rows, of one token each or, with stages, a run.
+template <int DT, int D, int BS>
+__global__ void __launch_bounds__(kRowThreads, 3)
+rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int window, int stages) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  using S = BlockShape<DT, D, BS>;
   allow_next_grid();
   wait_prior_grid();
   if ((int)blockIdx.x >= kv_ctas) {
-    token_rows<DT, D, NT, false>(a, (int)blockIdx.x - kv_ctas);
+    const int cta = (int)blockIdx.x - kv_ctas;
+    if (stages)
+      stream_rows<DT, D, false>(a, cta, (int)gridDim.x - kv_ctas, stages, ring);
+    else
+      token_rows<DT, D, false>(a, cta);
     return;
   }
   const int lane = threadIdx.x & 31;
-  const int h = (int)blockIdx.x % a.H, w0 = (int)blockIdx.x / a.H * kWindow;
+  const int parts = (a.H + S::kHeads - 1) / S::kHeads;
+  const int h0 = (int)blockIdx.x % parts * S::kHeads, w0 = (int)blockIdx.x / parts * window;
   // each warp places the window's tokens, one per lane
   const int t = w0 + lane;
-  const bool in_window = lane < kWindow && t < a.total_q;
+  const bool in_window = lane < window && t < a.total_q;
   int b = find_seq(a.q_start, a.B, w0, lane);
   for (int base = b;; base += 32) {
     // the 32 boundaries after `base`: count those at or before each lane's token
@@ -439,9 +633,9 @@ rope_append_q8_kernel(const RopeArgs a, int kv_ctas) {
   Place at = {b, 0, 0};
   bool bad = false;
   if (in_window) at = place_of(a, b, t, &bad);
-  int begins = 0, row = 0, n_here = 0;
+  int begins = 0, n_here = 0;
   if (at.ok) {
-    row = at.pos % BS;
+    const int row = at.pos % BS;
     begins = row == 0 || t == a.q_start[b];
     n_here = min(a.q_start[b + 1] - t, BS - row);   // its sequence's rows in this block
   }
@@ -449,7 +643,7 @@ rope_append_q8_kernel(const RopeArgs a, int kv_ctas) {
     const int src = __ffs(todo) - 1;
     const int bb = __shfl_sync(kAll, at.b, src), pos = __shfl_sync(kAll, at.pos, src);
     const int n = __shfl_sync(kAll, n_here, src);
-    store_block<DT, D, BS, NT>(a, bb, pos / BS, h, w0 + src, pos % BS, pos % BS + n);
+    store_block<DT, D, BS>(a, bb, pos / BS, h0, w0 + src, pos % BS, pos % BS + n);
   }
 }
 
@@ -463,7 +657,7 @@ rope_step_q8_kernel(const RopeArgs a, int kv_ctas) {
   allow_next_grid();
   wait_prior_grid();
   if ((int)blockIdx.x >= kv_ctas) {
-    token_rows<DT, D, kRowThreads, false>(a, (int)blockIdx.x - kv_ctas);
+    token_rows<DT, D, false>(a, (int)blockIdx.x - kv_ctas);
     return;
   }
   const int li = threadIdx.x % TG;
@@ -558,6 +752,54 @@ pa_status check_rope_pointers(const RopeArgs& a, int head_dim) {
   return PA_OK;
 }
 
+// How tokens of `rows` head rows go through shared memory: stages of a CTA (0: the
+// register kernel), bytes of them, CTAs.
+struct Stream {
+  int stages, bytes, ctas;
+};
+
+pa_status plan_stream(int tokens, int rows, int head_dim, int most, Stream* s) {
+  *s = {0, 0, tokens};
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return PA_ERR_CUDA;
+  if (tokens < kStreamTokens * sms) return PA_OK;
+  // `most` CTAs of an SM where two stages of each fit its shared memory, else fewer
+  const int64_t token = (int64_t)rows * head_dim * 2;
+  for (int per_sm = most; per_sm; --per_sm) {
+    const int64_t room = (227 * 1024) / per_sm - 5 * 1024;
+    if (2 * token > room) continue;
+    s->stages = (int)(room / token < kMaxStages ? room / token : kMaxStages);
+    s->bytes = (int)(s->stages * token);
+    s->ctas = sms * per_sm;
+    break;
+  }
+  return PA_OK;
+}
+
+// Shared memory above 48 KB, static included, has to be asked for.
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes) {
+  if (bytes <= 44 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int DT, int D, int BS>
+cudaError_t launch_blocks(const RopeArgs& a, const Stream& s, cudaStream_t stream) {
+  // a window's blocks are written one after another: about as many tokens as a
+  // sequence has, a block's at most
+  int window = BS < 32 ? BS : 32;
+  while (window > 1 && (int64_t)window * a.B > a.total_q) window /= 2;
+  constexpr int heads = BlockShape<DT, D, BS>::kHeads;
+  const int64_t kv = ((int64_t)a.total_q + window - 1) / window * ((a.H + heads - 1) / heads);
+  if (kv + s.ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem(rope_append_q8_kernel<DT, D, BS>, s.bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(rope_append_q8_kernel<DT, D, BS>, dim3((unsigned)(kv + s.ctas)), kRowThreads,
+                    s.bytes, stream, a, (int)kv, window, s.stages);
+}
+
 template <int DT, int D>
 cudaError_t launch_q8(const RopeArgs& a, cudaStream_t stream) {
   constexpr int TG = D / 8;
@@ -568,27 +810,27 @@ cudaError_t launch_q8(const RopeArgs& a, cudaStream_t stream) {
     return launch_pdl(rope_step_q8_kernel<DT, D>, dim3((unsigned)(kv + a.total_q)), kRowThreads, 0,
                       stream, a, (int)kv);
   }
-  const int64_t kv = ((int64_t)a.total_q + kWindow - 1) / kWindow * a.H;
-  if (kv + a.total_q > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)(kv + a.total_q));
+  Stream s;
+  if (plan_stream(a.total_q, a.Hq, D, 3, &s) != PA_OK) return cudaErrorUnknown;
   switch (a.bs) {
-    case 8:
-      return launch_pdl(rope_append_q8_kernel<DT, D, 8, 8 * TG>, grid, 8 * TG, 0, stream, a,
-                        (int)kv);
-    case 16:
-      return launch_pdl(rope_append_q8_kernel<DT, D, 16, 16 * TG>, grid, 16 * TG, 0, stream, a,
-                        (int)kv);
-    case 32:
-      return launch_pdl(rope_append_q8_kernel<DT, D, 32, 256>, grid, 256, 0, stream, a, (int)kv);
-    default:
-      return launch_pdl(rope_append_q8_kernel<DT, D, 64, 256>, grid, 256, 0, stream, a, (int)kv);
+    case 8: return launch_blocks<DT, D, 8>(a, s, stream);
+    case 16: return launch_blocks<DT, D, 16>(a, s, stream);
+    case 32: return launch_blocks<DT, D, 32>(a, s, stream);
+    default: return launch_blocks<DT, D, 64>(a, s, stream);
   }
 }
 
 template <int DT, int D>
 cudaError_t launch_16(const RopeArgs& a, cudaStream_t stream) {
-  return launch_pdl(rope_append_kernel<DT, D>, dim3((unsigned)a.total_q), kRowThreads, 0, stream,
-                    a);
+  Stream s;
+  if (plan_stream(a.total_q, a.Hq + 2 * a.H, D, 4, &s) != PA_OK) return cudaErrorUnknown;
+  if (!s.stages)
+    return launch_pdl(rope_append_kernel<DT, D>, dim3((unsigned)a.total_q), kRowThreads, 0, stream,
+                      a);
+  const cudaError_t e = allow_smem(rope_stream_kernel<DT, D>, s.bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(rope_stream_kernel<DT, D>, dim3((unsigned)s.ctas), kRowThreads, s.bytes,
+                    stream, a, s.stages);
 }
 
 }  // namespace

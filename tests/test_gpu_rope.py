@@ -134,6 +134,12 @@ CASES = [
     (*MANY, 4, 2, 64, 8, "fp16", 64, dict(behind=9)),
     ([300], [300], 3, 1, 128, 16, "bf16", 128, dict(norm="q", interleaved=True)),
     ([70] + [2] * 66, [70] + [1] * 66, 4, 4, 64, 64, "fp16", 64, dict(norm="k")),
+    # enough tokens for the ring of shared-memory stages (8 per SM), with other shapes of it
+    ([1500, 3, 900, 1], [1400, 0, 900, 1], 4, 2, 128, 16, "bf16", 128, dict(norm="qk", packed=True)),
+    ([1500, 3, 900, 1], [1400, 2, 900, 1], 6, 3, 64, 8, "fp16", 32,
+     dict(interleaved=True, behind=5, positions=True)),
+    ([2500], [2400], 96, 1, 128, 64, "fp16", 64, dict(norm="q")),
+    ([2500], [2400], 1, 1, 64, 32, "bf16", 0, dict(norm="k")),
 ]
 
 
@@ -223,6 +229,34 @@ def test_in_place(pa, dt):
     pa.pa_rope_append(q2, kp, vp, q2, *args, **s.kw_args())
     torch.cuda.synchronize()
     assert torch.equal(q2, s.q_out)
+
+
+def test_many_tokens_in_place_and_past_a_bad_one(pa):
+    """The ring's writes over its own reads; a token outside the table and a bad block in
+    the middle of a run are left alone."""
+    s = Setup([2000, 700], [2000, 700], 8, 2, 128, 16, "bf16", 128, norm="qk")
+    pos = np.array([p[2] for p in s.places])
+    pos[1234] = s.cs.shape[0]
+    tables = s.tables.copy()
+    tables[1, 3] = -5
+    kw = s.kw_args() | dict(positions=i32(pos))
+    kp = torch.full((s.NB, s.bs, s.H, s.D), 9.0, dtype=s.dt, device="cuda")
+    vp = kp.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    before = f64(s.q)[1234]
+    q2 = s.q.clone()
+    pa.pa_rope_append(q2, kp, vp, q2, s.k, s.v, s.cs, i32(tables), i32(s.lens), status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 5
+    got = f64(q2)
+    assert np.array_equal(got[1234], before)
+    ref, err = s.reference(s.q, s.qw)
+    rows = np.array([t for t in range(s.T) if t != 1234])
+    s.close16(got[rows], ref[rows], err[rows])
+    v, stored = f64(s.v), f64(vp)
+    for t, b, p, block, row in s.places:
+        left = t == 1234 or (b == 1 and p // 16 == 3)
+        assert np.array_equal(stored[block, row], np.full_like(v[t], 9.0) if left else v[t])
 
 
 def test_step_form_and_general_form_agree(pa):
