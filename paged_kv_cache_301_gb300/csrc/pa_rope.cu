@@ -10,9 +10,9 @@
 //
 // Both only move memory: each element is read once and written once, so the
 // bound is bytes / HBM bandwidth for prompts and the chain of dependent loads
-// (length -> table -> slot) for decode steps.  A head row is shared by D/8
-// lanes that hold one 16-byte vector each: the norm's sum and the partner of a
-// half-split pair are then shuffles inside the group.
+// (length -> table -> slot) for decode steps.  A head row is shared by D/16 lanes;
+// each holds two 16-byte vectors, the two halves of its eight pairs, so that the
+// rotation stays inside a lane and only the norm's sum is shuffled.
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_q8.cuh"
@@ -105,84 +105,98 @@ __device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
   x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
 }
 
+// Two values rounded to nearest in one conversion, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (DT == PA_BFLOAT16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  const __half2 p = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
 template <int DT>
 __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
-  return make_uint4(narrow2<DT>(x[0], x[1]), narrow2<DT>(x[2], x[3]), narrow2<DT>(x[4], x[5]),
-                    narrow2<DT>(x[6], x[7]));
+  return make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
+                    pack2<DT>(x[6], x[7]));
 }
 
-// RMS norm of a head row of D, 8 elements to each of its group's D/8 lanes.  Called by
-// whole warps (it shuffles); `on`: the group's row is normed, by weight's 8 elements.
-template <int DT, int D>
-__device__ __forceinline__ void norm(float (&x)[8], bool on, const uint4& weight, float eps) {
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-  for (int o = D / 16; o; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
-  if (on) {
-    const float r = rsqrtf(ss * (1.f / D) + eps);
-    float w[8];
-    widen8<DT>(weight, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-  }
+// A lane's 16 elements of a head row: vectors (8 elements) v0 and v1 of it.  Rotated
+// lanes (li < R/16) hold pairs: with pairs (j, j + R/2) vectors li and li + R/16; with
+// neighbours, and behind the rotated part, two vectors side by side.
+struct Part {
+  int v0, v1;
+  bool turns;                  // the lane's elements are rotated
+};
+
+__device__ __forceinline__ Part part_of(int li, int R, int interleaved) {
+  const bool turns = li < R / 16;
+  if (turns && !interleaved) return {li, li + R / 16, true};
+  return {2 * li, 2 * li + 1, turns};
 }
 
-// A lane's part of a position's angles: cosines and sines of its 8 elements' pairs
-// (4 pairs when they are neighbours).
+// A position's cosines and sines of a lane's eight pairs.
 struct Turn {
-  float4 c[2], s[2];
+  float c[8], s[8];
 };
 
 // angles: the position's row of cos_sin, R/2 cosines, then R/2 sines.
-__device__ __forceinline__ Turn load_turn(const float* angles, int R, int interleaved, int li) {
-  Turn t = {};
-  const float4* c = reinterpret_cast<const float4*>(angles);
-  const float4* s = reinterpret_cast<const float4*>(angles + R / 2);
-  if (interleaved) {
-    if (li * 8 < R) {
-      t.c[0] = c[li];
-      t.s[0] = s[li];
-    }
-  } else if (li * 8 < R) {
-    const int at = (li < R / 16 ? li : li - R / 16) * 2;
-    t.c[0] = c[at];
-    t.c[1] = c[at + 1];
-    t.s[0] = s[at];
-    t.s[1] = s[at + 1];
-  }
+__device__ __forceinline__ Turn load_turn(const float* angles, int R, int li) {
+  const float4* c = reinterpret_cast<const float4*>(angles + 8 * li);
+  const float4* s = reinterpret_cast<const float4*>(angles + R / 2 + 8 * li);
+  const float4 c0 = c[0], c1 = c[1], s0 = s[0], s1 = s[1];
+  Turn t;
+  t.c[0] = c0.x; t.c[1] = c0.y; t.c[2] = c0.z; t.c[3] = c0.w;
+  t.c[4] = c1.x; t.c[5] = c1.y; t.c[6] = c1.z; t.c[7] = c1.w;
+  t.s[0] = s0.x; t.s[1] = s0.y; t.s[2] = s0.z; t.s[3] = s0.w;
+  t.s[4] = s1.x; t.s[5] = s1.y; t.s[6] = s1.z; t.s[7] = s1.w;
   return t;
 }
 
-// Rotation of a group's row; called by whole warps (it shuffles); `on`: the group's
-// row is rotated.
-__device__ __forceinline__ void rotate(float (&x)[8], bool on, const Turn& t, int R,
-                                       int interleaved, int li) {
-  const float c[8] = {t.c[0].x, t.c[0].y, t.c[0].z, t.c[0].w, t.c[1].x, t.c[1].y, t.c[1].z, t.c[1].w};
-  const float s[8] = {t.s[0].x, t.s[0].y, t.s[0].z, t.s[0].w, t.s[1].x, t.s[1].y, t.s[1].z, t.s[1].w};
-  on = on && li * 8 < R;
+__device__ __forceinline__ uint4 pick(bool first, uint4 x, uint4 y) {
+  return make_uint4(first ? x.x : y.x, first ? x.y : y.y, first ? x.z : y.z, first ? x.w : y.w);
+}
+
+// RMS norm of a head row over its D/16 lanes.  Called by whole warps (it shuffles);
+// `on`: the group's row is normed, by w0 and w1, the weight's vectors v0 and v1.
+template <int DT, int D>
+__device__ __forceinline__ void norm(float (&a)[8], float (&b)[8], bool on, uint4 w0,
+                                     uint4 w1, float eps) {
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+#pragma unroll
+  for (int o = D / 32; o; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
+  if (on) {
+    const float r = rsqrtf(ss * (1.f / D) + eps);
+    float w[8];
+    widen8<DT>(w0, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = a[i] * r * w[i];
+    widen8<DT>(w1, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = b[i] * r * w[i];
+  }
+}
+
+__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Turn& t,
+                                       int interleaved) {
   if (interleaved) {
-    if (on) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = x[2 * i], q = x[2 * i + 1];
-        x[2 * i] = p * c[i] - q * s[i];
-        x[2 * i + 1] = q * c[i] + p * s[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float p = a[2 * i], q = a[2 * i + 1], u = b[2 * i], v = b[2 * i + 1];
+      a[2 * i] = p * t.c[i] - q * t.s[i];
+      a[2 * i + 1] = q * t.c[i] + p * t.s[i];
+      b[2 * i] = u * t.c[i + 4] - v * t.s[i + 4];
+      b[2 * i + 1] = v * t.c[i + 4] + u * t.s[i + 4];
     }
-  } else if (R > 0) {
-    const int half = R / 16;                     // lanes that hold half the rotated part
-    const bool first = li < half;
-    const int partner = li * 8 < R ? (first ? li + half : li - half) : li;
-    const int base = (threadIdx.x & 31) - li;    // first lane of the group
-    float y[8];
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(kAll, x[i], base + partner);
-    if (on) {
-      const float sign = first ? -1.f : 1.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + sign * (y[i] * s[i]);
+    for (int i = 0; i < 8; ++i) {
+      const float p = a[i], q = b[i];
+      a[i] = p * t.c[i] - q * t.s[i];
+      b[i] = q * t.c[i] + p * t.s[i];
     }
   }
 }
@@ -200,33 +214,42 @@ __device__ __forceinline__ const float* angles_of(const RopeArgs& a, int t, int 
 }
 
 // All rows of token t, by one CTA: row r < Hq is query head r; with
-// KV16 the keys and values of the 16-bit cache follow.  Groups of D/8 lanes take
+// KV16 the keys and values of the 16-bit cache follow.  Groups of D/16 lanes take
 // rows in turn, U at a time so that their loads overlap; the first ones, and the
 // norms' weights, are asked for before the token's place is looked up, and the
 // token's angles once for all of a thread's rows.
 template <int DT, int D, bool KV16>
 __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
-  constexpr int TG = D / 8, NG = kRowThreads / TG, U = 3;
+  constexpr int TG = D / 16, NG = kRowThreads / TG, U = 2, RV = D / 8;
   const int lane = threadIdx.x & 31, li = threadIdx.x % TG, grp = threadIdx.x / TG;
+  const Part part = part_of(li, a.rotary, a.interleaved);
   const int rows = KV16 ? a.Hq + 2 * a.H : a.Hq;
   const uint4* q = reinterpret_cast<const uint4*>(a.q) + t * (a.q_stride / 8);
   const uint4* key = reinterpret_cast<const uint4*>(a.key) + t * (a.kv_stride / 8);
   const uint4* value = reinterpret_cast<const uint4*>(a.value) + t * (a.kv_stride / 8);
-  uint4 w[U];
+  uint4 w[U][2];
   auto load_rows = [&](int r0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 + u * NG + grp;
-      w[u] = make_uint4(0, 0, 0, 0);
-      if (r < a.Hq) w[u] = q[r * TG + li];
-      else if (KV16 && r < a.Hq + a.H) w[u] = key[(r - a.Hq) * TG + li];
-      else if (KV16 && r < rows) w[u] = value[(r - a.Hq - a.H) * TG + li];
+      const uint4* row = nullptr;
+      if (r < a.Hq) row = q + r * RV;
+      else if (KV16 && r < a.Hq + a.H) row = key + (r - a.Hq) * RV;
+      else if (KV16 && r < rows) row = value + (r - a.Hq - a.H) * RV;
+      w[u][0] = row ? row[part.v0] : make_uint4(0, 0, 0, 0);
+      w[u][1] = row ? row[part.v1] : make_uint4(0, 0, 0, 0);
     }
   };
   load_rows(0);
-  uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
-  if (a.q_weight) qw = reinterpret_cast<const uint4*>(a.q_weight)[li];
-  if (KV16 && a.k_weight) kw = reinterpret_cast<const uint4*>(a.k_weight)[li];
+  uint4 qw[2] = {}, kw[2] = {};
+  if (a.q_weight) {
+    qw[0] = reinterpret_cast<const uint4*>(a.q_weight)[part.v0];
+    qw[1] = reinterpret_cast<const uint4*>(a.q_weight)[part.v1];
+  }
+  if (KV16 && a.k_weight) {
+    kw[0] = reinterpret_cast<const uint4*>(a.k_weight)[part.v0];
+    kw[1] = reinterpret_cast<const uint4*>(a.k_weight)[part.v1];
+  }
 
   const int b = a.q_start ? find_seq(a.q_start, a.B, t, lane) : t;
   bool bad;
@@ -238,7 +261,7 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
     return;
   }
   Turn turn = {};
-  if (angles) turn = load_turn(angles, a.rotary, a.interleaved, li);
+  if (part.turns) turn = load_turn(angles, a.rotary, li);
   int64_t slot = -1;
   if (KV16) {
     const int32_t blk = a.tables[(int64_t)b * a.max_blocks + at.pos / a.bs];
@@ -252,19 +275,24 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
       const int r = r0 + u * NG + grp;
       if (r0 + u * NG >= rows) break;
       const bool is_q = r < a.Hq, is_k = KV16 && !is_q && r < a.Hq + a.H;
-      float x[8];
-      widen8<DT>(w[u], x);
+      float x[8], y[8];
+      widen8<DT>(w[u][0], x);
+      widen8<DT>(w[u][1], y);
       if (any_norm)
-        norm<DT, D>(x, is_q ? a.q_weight != nullptr : is_k && a.k_weight != nullptr, is_q ? qw : kw,
-                    a.eps);
-      rotate(x, is_q || is_k, turn, a.rotary, a.interleaved, li);
-      if (is_q) {
-        reinterpret_cast<uint4*>(a.q_out)[((int64_t)t * a.Hq + r) * TG + li] = narrow8<DT>(x);
-      } else if (is_k) {
-        if (slot >= 0)
-          reinterpret_cast<uint4*>(a.k_pool)[(slot * a.H + (r - a.Hq)) * TG + li] = narrow8<DT>(x);
-      } else if (KV16 && r < rows && slot >= 0) {
-        reinterpret_cast<uint4*>(a.v_pool)[(slot * a.H + (r - a.Hq - a.H)) * TG + li] = w[u];
+        norm<DT, D>(x, y, is_q ? a.q_weight != nullptr : is_k && a.k_weight != nullptr,
+                    pick(is_q, qw[0], kw[0]), pick(is_q, qw[1], kw[1]), a.eps);
+      if (part.turns) rotate(x, y, turn, a.interleaved);
+      uint4* to = nullptr;
+      if (is_q) to = reinterpret_cast<uint4*>(a.q_out) + ((int64_t)t * a.Hq + r) * RV;
+      else if (is_k && slot >= 0)
+        to = reinterpret_cast<uint4*>(a.k_pool) + (slot * a.H + (r - a.Hq)) * RV;
+      if (to) {
+        to[part.v0] = narrow8<DT>(x);
+        to[part.v1] = narrow8<DT>(y);
+      } else if (KV16 && !is_k && r < rows && slot >= 0) {
+        to = reinterpret_cast<uint4*>(a.v_pool) + (slot * a.H + (r - a.Hq - a.H)) * RV;
+        to[part.v0] = w[u][0];
+        to[part.v1] = w[u][1];
       }
     }
     r0 += NG * U;
@@ -275,14 +303,17 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
 
 // ---------------------------------------------------------------- many tokens --
 // One CTA takes a run of tokens through a ring of shared-memory stages: bulk copies
-// bring a token's rows in (one contiguous copy each for q, key and value), the
-// threads norm and rotate them in place, bulk copies take them out (values without
-// passing through registers).  Reads of later tokens and writes of earlier ones are
-// in flight all the time, which the register kernel above cannot hold at the
-// occupancy its angles leave it.
+// bring a few tokens' rows and angles in (one contiguous copy each for q, key, value
+// and the row of cos_sin), seven warps norm and rotate them in place, bulk copies take
+// them out (values without passing through registers).  The eighth warp issues all the
+// copies, so that no computing warp waits for one to be read out.  Reads of later
+// tokens and writes of earlier ones are in flight all the time, which the register
+// kernel above cannot hold at the occupancy that a row's registers leave it.
 constexpr int kMaxStages = 4;
-constexpr int kPlaced = kRowThreads;           // tokens placed at once, one per thread
+constexpr int kComputeWarps = kRowThreads / 32 - 1;
+constexpr int kRun = kRowThreads;              // tokens of a CTA at most: one thread places one
 constexpr int kStreamTokens = 8;               // tokens per SM from which on it is taken
+constexpr int kMaxTogether = 8;                // tokens of a stage at most
 constexpr uint64_t kStreamLimitNs = 2000000000ull;
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
@@ -315,132 +346,179 @@ __device__ __forceinline__ Place place_token(const RopeArgs& a, int t, bool* bad
   return place_of(a, b, t, bad);
 }
 
-// Tokens [total_q cta / ctas, total_q (cta + 1) / ctas).
+// Tokens [total_q cta / ctas, total_q (cta + 1) / ctas), kRun at most, `together` of
+// them to a stage.
 template <int DT, int D, bool KV16>
 __device__ __forceinline__ void stream_rows(const RopeArgs& a, int cta, int ctas, int stages,
-                                            uint8_t* ring) {
-  constexpr int TG = D / 8, NG = kRowThreads / TG;
-  __shared__ __align__(8) uint64_t full[kMaxStages];
-  __shared__ int64_t s_slot[kPlaced];          // pool row of the token (-1: none)
-  __shared__ int s_pos[kPlaced];               // row of cos_sin (-1: leave the token alone)
-  const int tid = threadIdx.x, li = tid % TG, grp = tid / TG;
+                                            int together, uint8_t* ring) {
+  constexpr int TG = D / 16, NG = kComputeWarps * 32 / TG, RV = D / 8;
+  __shared__ __align__(8) uint64_t full[kMaxStages], done[kMaxStages];
+  __shared__ int64_t s_slot[kRun];             // pool row of the token (-1: none)
+  __shared__ int s_pos[kRun];                  // row of cos_sin (-1: leave the token alone)
+  __shared__ int s_abort;
+  volatile int* abort_flag = &s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int li = tid % TG, grp = tid / TG;
+  const bool copies = tid == kComputeWarps * 32;       // the thread that issues them
+  const Part part = part_of(li, a.rotary, a.interleaved);
   const int t0 = (int)((int64_t)a.total_q * cta / ctas);
   const int n = (int)((int64_t)a.total_q * (cta + 1) / ctas) - t0;
+  const int steps = (n + together - 1) / together;
   const uint32_t q_bytes = (uint32_t)(a.Hq * D * 2), kv_bytes = KV16 ? (uint32_t)(a.H * D * 2) : 0;
-  const uint32_t stage_bytes = q_bytes + 2 * kv_bytes;
-  if (tid == 0) {
-    for (int i = 0; i < stages; ++i) sm100::mbar_init(&full[i], 1);
+  const uint32_t row_bytes = q_bytes + 2 * kv_bytes, angle_bytes = (uint32_t)(a.rotary * 4);
+  const uint32_t token_bytes = row_bytes + angle_bytes;
+  if (copies) {
+    for (int i = 0; i < stages; ++i) {
+      sm100::mbar_init(&full[i], 2);           // rows, angles
+      sm100::mbar_init(&done[i], kComputeWarps);
+    }
+    s_abort = 0;
     sm100::fence_mbar_init();
   }
   __syncthreads();
-  auto fetch = [&](int i) {                    // thread 0
-    uint8_t* to = ring + (uint32_t)(i % stages) * stage_bytes;
-    uint64_t* bar = &full[i % stages];
-    const int64_t t = t0 + i;
-    sm100::mbar_arrive_expect_tx(bar, stage_bytes);
-    bulk_load(to, static_cast<const uint16_t*>(a.q) + t * a.q_stride, q_bytes, bar);
-    if (KV16) {
-      bulk_load(to + q_bytes, static_cast<const uint16_t*>(a.key) + t * a.kv_stride, kv_bytes, bar);
-      bulk_load(to + q_bytes + kv_bytes, static_cast<const uint16_t*>(a.value) + t * a.kv_stride,
-                kv_bytes, bar);
-    }
+  auto stage_of = [&](int step) {
+    return ring + (uint32_t)(step % stages) * ((uint32_t)together * token_bytes);
   };
-  if (tid == 0)
-    for (int i = 0; i < min(stages, n); ++i) fetch(i);
-  uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
-  if (a.q_weight) qw = reinterpret_cast<const uint4*>(a.q_weight)[li];
-  if (KV16 && a.k_weight) kw = reinterpret_cast<const uint4*>(a.k_weight)[li];
-  const bool any_norm = a.q_weight || (KV16 && a.k_weight);
-  const int turned = KV16 ? a.Hq + a.H : a.Hq;
-  Turn turn = {}, next = {};
-  auto turn_of = [&](int i) {
-    const int pos = s_pos[i % kPlaced];
-    if (a.rotary && pos >= 0)
-      next = load_turn(a.cos_sin + (int64_t)pos * a.rotary, a.rotary, a.interleaved, li);
-  };
-  bool late = false;
-  int fetched = min(stages, n);                // thread 0
-  for (int i = 0; i < n; ++i) {
-    if (i % kPlaced == 0) {                    // the next tokens' places
-      if (i > 0) __syncthreads();
-      const int t = t0 + i + tid;
-      int64_t slot = -1;
-      int pos = -1;
-      if (i + tid < n) {
-        bool bad;
-        const Place at = place_token(a, t, &bad);
-        bool ok = at.ok;
-        if (ok) angles_of(a, t, at.pos, &ok);
-        if (bad || (at.ok && !ok)) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-        if (ok) {
-          pos = a.rotary && a.positions ? a.positions[t] : at.pos;
-          if (KV16) {
-            const int32_t blk = a.tables[(int64_t)at.b * a.max_blocks + at.pos / a.bs];
-            if (blk >= 0 && blk < a.num_blocks) slot = (int64_t)blk * a.bs + at.pos % a.bs;
-            else report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-          }
-        }
-      }
-      s_slot[tid] = slot;
-      s_pos[tid] = pos;
-      __syncthreads();
-      turn_of(i);
-    }
-    turn = next;
-    if (i + 1 < n && (i + 1) % kPlaced != 0) turn_of(i + 1);
-    const bool live = s_pos[i % kPlaced] >= 0;
-    uint8_t* stage = ring + (uint32_t)(i % stages) * stage_bytes;
-    late = !sm100::mbar_try_wait(&full[i % stages], (i / stages) & 1) &&
-           !sm100::mbar_wait_drain(&full[i % stages], (i / stages) & 1, kStreamLimitNs);
-    if (live && !late) {
-      for (int r0 = 0; r0 < turned; r0 += NG) {
-        const int r = r0 + grp;
-        uint4* at = reinterpret_cast<uint4*>(stage) + r * TG + li;
-        const bool is_q = r < a.Hq, in = r < turned;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (in) w = *at;
-        float x[8];
-        widen8<DT>(w, x);
-        if (any_norm)
-          norm<DT, D>(x, is_q ? a.q_weight != nullptr : KV16 && a.k_weight != nullptr,
-                      is_q ? qw : kw, a.eps);
-        rotate(x, true, turn, a.rotary, a.interleaved, li);
-        if (in) *at = narrow8<DT>(x);
+  auto fetch_rows = [&](int step) {
+    uint8_t* to = stage_of(step);
+    uint64_t* bar = &full[step % stages];
+    const int first = step * together, many = min(together, n - first);
+    sm100::mbar_arrive_expect_tx(bar, many * row_bytes);
+    for (int i = 0; i < many; ++i, to += token_bytes) {
+      const int64_t t = t0 + first + i;
+      bulk_load(to, static_cast<const uint16_t*>(a.q) + t * a.q_stride, q_bytes, bar);
+      if (KV16) {
+        bulk_load(to + q_bytes, static_cast<const uint16_t*>(a.key) + t * a.kv_stride, kv_bytes,
+                  bar);
+        bulk_load(to + q_bytes + kv_bytes, static_cast<const uint16_t*>(a.value) + t * a.kv_stride,
+                  kv_bytes, bar);
       }
     }
-    sm100::fence_async_smem();
-    if (__syncthreads_or(late)) {
-      late = true;
-      break;
+  };
+  auto fetch_angles = [&](int step) {
+    uint8_t* to = stage_of(step) + row_bytes;
+    uint64_t* bar = &full[step % stages];
+    const int first = step * together, many = min(together, n - first);
+    int live = 0;
+    for (int i = 0; i < many; ++i) live += s_pos[first + i] >= 0 ? 1 : 0;
+    sm100::mbar_arrive_expect_tx(bar, live * angle_bytes);
+    if (a.rotary == 0) return;
+    for (int i = 0; i < many; ++i) {
+      const int pos = s_pos[first + i];
+      if (pos >= 0)
+        bulk_load(to + i * token_bytes, a.cos_sin + (int64_t)pos * a.rotary, angle_bytes, bar);
     }
-    if (tid == 0) {
-      if (live) {
-        bulk_store(static_cast<uint16_t*>(a.q_out) + (int64_t)(t0 + i) * a.Hq * D, stage, q_bytes);
-        const int64_t slot = s_slot[i % kPlaced];
+  };
+  int fetched = min(stages, steps);
+  if (copies)
+    for (int i = 0; i < fetched; ++i) fetch_rows(i);
+  uint4 qw[2] = {}, kw[2] = {};
+  if (a.q_weight) {
+    qw[0] = reinterpret_cast<const uint4*>(a.q_weight)[part.v0];
+    qw[1] = reinterpret_cast<const uint4*>(a.q_weight)[part.v1];
+  }
+  if (KV16 && a.k_weight) {
+    kw[0] = reinterpret_cast<const uint4*>(a.k_weight)[part.v0];
+    kw[1] = reinterpret_cast<const uint4*>(a.k_weight)[part.v1];
+  }
+  if (tid < n) {                               // every thread places a token of the run
+    bool bad;
+    const int t = t0 + tid;
+    const Place at = place_token(a, t, &bad);
+    bool ok = at.ok;
+    if (ok) angles_of(a, t, at.pos, &ok);
+    if (bad || (at.ok && !ok)) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+    int64_t slot = -1;
+    if (KV16 && ok) {
+      const int32_t blk = a.tables[(int64_t)at.b * a.max_blocks + at.pos / a.bs];
+      if (blk >= 0 && blk < a.num_blocks) slot = (int64_t)blk * a.bs + at.pos % a.bs;
+      else report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+    }
+    s_slot[tid] = slot;
+    s_pos[tid] = !ok ? -1 : (a.rotary && a.positions ? a.positions[t] : at.pos);
+  }
+  __syncthreads();
+
+  if (warp == kComputeWarps) {
+    if (!copies) return;
+    for (int i = 0; i < fetched; ++i) fetch_angles(i);
+    bool ok = true;
+    for (int step = 0; step < steps; ++step) {
+      ok = sm100::mbar_wait(&done[step % stages], (step / stages) & 1, abort_flag, kStreamLimitNs);
+      if (!ok) break;
+      const uint8_t* token = stage_of(step);
+      const int first = step * together, many = min(together, n - first);
+      for (int i = 0; i < many; ++i, token += token_bytes) {
+        if (s_pos[first + i] < 0) continue;
+        bulk_store(static_cast<uint16_t*>(a.q_out) + (int64_t)(t0 + first + i) * a.Hq * D, token,
+                   q_bytes);
+        const int64_t slot = s_slot[first + i];
         if (KV16 && slot >= 0) {
-          bulk_store(static_cast<uint16_t*>(a.k_pool) + slot * a.H * D, stage + q_bytes, kv_bytes);
-          bulk_store(static_cast<uint16_t*>(a.v_pool) + slot * a.H * D, stage + q_bytes + kv_bytes,
+          bulk_store(static_cast<uint16_t*>(a.k_pool) + slot * a.H * D, token + q_bytes, kv_bytes);
+          bulk_store(static_cast<uint16_t*>(a.v_pool) + slot * a.H * D, token + q_bytes + kv_bytes,
                      kv_bytes);
         }
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      // the stage of the token before has been read out: the next one comes in
-      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      if (i > 0 && fetched < n) fetch(fetched++);
+      if (step > 0 && fetched < steps) {
+        // the stage of the step before has been read out: the next one comes in
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        fetch_rows(fetched);
+        fetch_angles(fetched++);
+      }
     }
-  }
-  if (tid == 0) {
-    if (late) {                                // copies in flight land before the CTA ends
+    if (!ok) {                                 // copies in flight land before the CTA ends
+      *abort_flag = 1;
       report(a.status_dev, PA_ERR_TIMEOUT);
       for (int j = max(0, fetched - stages); j < fetched; ++j)
         sm100::mbar_wait_drain(&full[j % stages], (j / stages) & 1, kStreamLimitNs);
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    return;
+  }
+
+  const bool any_norm = a.q_weight || (KV16 && a.k_weight);
+  const int turned = KV16 ? a.Hq + a.H : a.Hq;
+  for (int step = 0; step < steps; ++step) {
+    const int first = step * together, many = min(together, n - first);
+    if (!__all_sync(kAll, sm100::mbar_wait(&full[step % stages], (step / stages) & 1, abort_flag,
+                                           kStreamLimitNs))) {
+      *abort_flag = 1;
+      break;
+    }
+    uint8_t* stage = stage_of(step);
+    // (token, row) pairs in turn; whole warps stay in the loop for the shuffles
+    int i = 0, r = grp;
+    for (int k = 0; k < many * turned; k += NG, r += NG) {
+      while (r >= turned && i < many) {
+        r -= turned;
+        ++i;
+      }
+      const bool live = i < many && s_pos[first + min(i, many - 1)] >= 0;
+      const bool is_q = r < a.Hq;
+      uint8_t* token = stage + (uint32_t)i * token_bytes;
+      uint4* row = reinterpret_cast<uint4*>(token) + r * RV;
+      float x[8], y[8];
+      widen8<DT>(live ? row[part.v0] : make_uint4(0, 0, 0, 0), x);
+      widen8<DT>(live ? row[part.v1] : make_uint4(0, 0, 0, 0), y);
+      if (any_norm)
+        norm<DT, D>(x, y, is_q ? a.q_weight != nullptr : KV16 && a.k_weight != nullptr,
+                    pick(is_q, qw[0], kw[0]), pick(is_q, qw[1], kw[1]), a.eps);
+      if (!live) continue;
+      if (part.turns)
+        rotate(x, y, load_turn(reinterpret_cast<const float*>(token + row_bytes), a.rotary, li),
+               a.interleaved);
+      row[part.v0] = narrow8<DT>(x);
+      row[part.v1] = narrow8<DT>(y);
+    }
+    sm100::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&done[step % stages]);
   }
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 3)
 rope_append_kernel(const RopeArgs a) {
   allow_next_grid();
   wait_prior_grid();
@@ -449,11 +527,11 @@ rope_append_kernel(const RopeArgs a) {
 
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads, 4)
-rope_stream_kernel(const RopeArgs a, int stages) {
+rope_stream_kernel(const RopeArgs a, int stages, int together) {
   extern __shared__ __align__(128) uint8_t ring[];
   allow_next_grid();
   wait_prior_grid();
-  stream_rows<DT, D, true>(a, (int)blockIdx.x, (int)gridDim.x, stages, ring);
+  stream_rows<DT, D, true>(a, (int)blockIdx.x, (int)gridDim.x, stages, together, ring);
 }
 
 // Bring older codes to a larger scale: 8 codes times `ratio`, rounded once more
@@ -483,9 +561,9 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
 // rows g, g + NG, ...  All older rows are below r0.  Keys are normed and rotated
 // twice, for the largest magnitude and for the codes: the raw rows take a quarter
 // of the registers.
-template <int DT, int D, int BS>
+template <int D, int BS>
 struct BlockShape {
-  static constexpr int TG = D / 8;
+  static constexpr int TG = D / 16;
   static constexpr int kHead = BS * TG < kRowThreads ? BS * TG : kRowThreads;
   static constexpr int kHeads = kRowThreads / kHead;      // heads of a CTA
   static constexpr int NG = kHead / TG, RPT = BS / NG;    // groups, rows of each
@@ -494,12 +572,13 @@ struct BlockShape {
 template <int DT, int D, int BS>
 __device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int h0, int t0, int r0,
                                             int r1) {
-  using S = BlockShape<DT, D, BS>;
-  constexpr int TG = S::TG, NG = S::NG, RPT = S::RPT, NW = S::kHead / 32;
+  using S = BlockShape<D, BS>;
+  constexpr int TG = S::TG, NG = S::NG, RPT = S::RPT, NW = S::kHead / 32, RV = D / 8;
   __shared__ float s_mag[kRowThreads / 32][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int mine = threadIdx.x / S::kHead, h = h0 + mine;
   const int li = threadIdx.x % TG, grp = threadIdx.x % S::kHead / TG;
+  const Part part = part_of(li, a.rotary, a.interleaved);
   const int32_t blk = a.tables[(int64_t)b * a.max_blocks + j];
   if (blk < 0 || blk >= a.num_blocks) {
     if (threadIdx.x == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
@@ -507,22 +586,29 @@ __device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int
   }
   const bool in = h < a.H;
   const int64_t tile = (int64_t)blk * a.H + h;
-  uint2* kc = static_cast<uint2*>(a.k_pool) + tile * (BS * D / 8);
-  uint2* vc = static_cast<uint2*>(a.v_pool) + tile * (BS * D / 8);
-  uint4 weight = make_uint4(0, 0, 0, 0), kw[RPT], vw[RPT];
+  uint2* kc = static_cast<uint2*>(a.k_pool) + tile * (BS * RV);
+  uint2* vc = static_cast<uint2*>(a.v_pool) + tile * (BS * RV);
+  uint4 wt[2] = {}, kw[RPT][2], vw[RPT][2];
   const float* angles[RPT];
   bool live[RPT], any = false;
 #pragma unroll
   for (int u = 0; u < RPT; ++u) {
     const int row = grp + u * NG, t = t0 + row - r0;
     live[u] = in && row >= r0 && row < r1;
-    kw[u] = vw[u] = make_uint4(0, 0, 0, 0);
+    kw[u][0] = kw[u][1] = vw[u][0] = vw[u][1] = make_uint4(0, 0, 0, 0);
     if (live[u]) {
-      kw[u] = reinterpret_cast<const uint4*>(a.key)[t * (a.kv_stride / 8) + h * TG + li];
-      vw[u] = reinterpret_cast<const uint4*>(a.value)[t * (a.kv_stride / 8) + h * TG + li];
+      const uint4* k = reinterpret_cast<const uint4*>(a.key) + t * (a.kv_stride / 8) + h * RV;
+      const uint4* v = reinterpret_cast<const uint4*>(a.value) + t * (a.kv_stride / 8) + h * RV;
+      kw[u][0] = k[part.v0];
+      kw[u][1] = k[part.v1];
+      vw[u][0] = v[part.v0];
+      vw[u][1] = v[part.v1];
     }
   }
-  if (a.k_weight) weight = reinterpret_cast<const uint4*>(a.k_weight)[li];
+  if (a.k_weight) {
+    wt[0] = reinterpret_cast<const uint4*>(a.k_weight)[part.v0];
+    wt[1] = reinterpret_cast<const uint4*>(a.k_weight)[part.v1];
+  }
   float k_old = 0.f, v_old = 0.f;
   if (in && r0 > 0) {
     k_old = a.k_scale[tile];
@@ -538,22 +624,24 @@ __device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int
     }
     any |= live[u];
   }
-  auto new_key = [&](int u, float (&x)[8]) {   // whole warps
-    Turn turn = {};
-    if (angles[u]) turn = load_turn(angles[u], a.rotary, a.interleaved, li);
-    widen8<DT>(kw[u], x);
-    if (a.k_weight) norm<DT, D>(x, true, weight, a.eps);
-    rotate(x, true, turn, a.rotary, a.interleaved, li);
+  auto new_key = [&](int u, float (&x)[8], float (&y)[8]) {   // whole warps
+    widen8<DT>(kw[u][0], x);
+    widen8<DT>(kw[u][1], y);
+    if (a.k_weight) norm<DT, D>(x, y, true, wt[0], wt[1], a.eps);
+    if (part.turns && angles[u]) {
+      rotate(x, y, load_turn(angles[u], a.rotary, li), a.interleaved);
+    }
   };
   float km = 0.f, vm = 0.f;
 #pragma unroll
   for (int u = 0; u < RPT; ++u) {
     float x[8], y[8];
-    new_key(u, x);
-    widen8<DT>(vw[u], y);
+    new_key(u, x, y);
     if (live[u]) {
-      km = fmaxf(km, mag8(x));
-      vm = fmaxf(vm, mag8(y));
+      km = fmaxf(km, fmaxf(mag8(x), mag8(y)));
+      widen8<DT>(vw[u][0], x);
+      widen8<DT>(vw[u][1], y);
+      vm = fmaxf(vm, fmaxf(mag8(x), mag8(y)));
     }
   }
 #pragma unroll
@@ -578,14 +666,23 @@ __device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int
   for (int u = 0; u < RPT; ++u) {
     const int row = grp + u * NG;
     float x[8], y[8];
-    new_key(u, x);
+    new_key(u, x, y);
     if (live[u]) {
-      widen8<DT>(vw[u], y);
-      kc[row * TG + li] = quantise8(x, k_inv);
-      vc[row * TG + li] = quantise8(y, v_inv);
+      kc[row * RV + part.v0] = quantise8(x, k_inv);
+      kc[row * RV + part.v1] = quantise8(y, k_inv);
+      widen8<DT>(vw[u][0], x);
+      widen8<DT>(vw[u][1], y);
+      vc[row * RV + part.v0] = quantise8(x, v_inv);
+      vc[row * RV + part.v1] = quantise8(y, v_inv);
     } else if (in && row < r0) {
-      if (ks > k_old) rescale8(kc + row * TG + li, k_old * k_inv);
-      if (vs > v_old) rescale8(vc + row * TG + li, v_old * v_inv);
+      if (ks > k_old) {
+        rescale8(kc + row * RV + part.v0, k_old * k_inv);
+        rescale8(kc + row * RV + part.v1, k_old * k_inv);
+      }
+      if (vs > v_old) {
+        rescale8(vc + row * RV + part.v0, v_old * v_inv);
+        rescale8(vc + row * RV + part.v1, v_old * v_inv);
+      }
     }
   }
   if (in && threadIdx.x % S::kHead == 0) {
@@ -599,15 +696,15 @@ __device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int
 // the window; the others hold query rows, of one token each or, with stages, a run.
 template <int DT, int D, int BS>
 __global__ void __launch_bounds__(kRowThreads, 3)
-rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int window, int stages) {
+rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int window, int stages, int together) {
   extern __shared__ __align__(128) uint8_t ring[];
-  using S = BlockShape<DT, D, BS>;
+  using S = BlockShape<D, BS>;
   allow_next_grid();
   wait_prior_grid();
   if ((int)blockIdx.x >= kv_ctas) {
     const int cta = (int)blockIdx.x - kv_ctas;
     if (stages)
-      stream_rows<DT, D, false>(a, cta, (int)gridDim.x - kv_ctas, stages, ring);
+      stream_rows<DT, D, false>(a, cta, (int)gridDim.x - kv_ctas, stages, together, ring);
     else
       token_rows<DT, D, false>(a, cta);
     return;
@@ -648,12 +745,12 @@ rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int window, int stages) {
 }
 
 // A decode step: one new token per sequence.  CTAs [0, kv_ctas): each group of
-// D/8 lanes takes the K or the V row of one (sequence, KV head); the others hold
+// D/16 lanes takes the K or the V row of one (sequence, KV head); the others hold
 // one token's query rows.
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads)
 rope_step_q8_kernel(const RopeArgs a, int kv_ctas) {
-  constexpr int TG = D / 8, NG = kRowThreads / TG;
+  constexpr int TG = D / 16, NG = kRowThreads / TG, RV = D / 8;
   allow_next_grid();
   wait_prior_grid();
   if ((int)blockIdx.x >= kv_ctas) {
@@ -661,17 +758,24 @@ rope_step_q8_kernel(const RopeArgs a, int kv_ctas) {
     return;
   }
   const int li = threadIdx.x % TG;
+  const Part part = part_of(li, a.rotary, a.interleaved);
   const int64_t item = (int64_t)blockIdx.x * NG + threadIdx.x / TG;
   const bool is_v = item & 1;
   const int h = (int)((item >> 1) % a.H);
   const int64_t b64 = (item >> 1) / a.H;
   const bool in = b64 < a.B;
   const int b = in ? (int)b64 : 0;
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (in)
-    w = reinterpret_cast<const uint4*>(is_v ? a.value : a.key)[b * (a.kv_stride / 8) + h * TG + li];
-  uint4 weight = make_uint4(0, 0, 0, 0);
-  if (a.k_weight) weight = reinterpret_cast<const uint4*>(a.k_weight)[li];
+  uint4 w[2] = {}, wt[2] = {};
+  if (in) {
+    const uint4* from =
+        reinterpret_cast<const uint4*>(is_v ? a.value : a.key) + b * (a.kv_stride / 8) + h * RV;
+    w[0] = from[part.v0];
+    w[1] = from[part.v1];
+  }
+  if (a.k_weight) {
+    wt[0] = reinterpret_cast<const uint4*>(a.k_weight)[part.v0];
+    wt[1] = reinterpret_cast<const uint4*>(a.k_weight)[part.v1];
+  }
   bool bad = false;
   Place at = {0, 0, 0};
   if (in) at = place_of(a, b, b, &bad);
@@ -688,20 +792,26 @@ rope_step_q8_kernel(const RopeArgs a, int kv_ctas) {
   float* scale = (is_v ? a.v_scale : a.k_scale) + tile;
   const float old = ok && row > 0 ? *scale : 0.f;
   Turn turn = {};
-  if (angles && !is_v) turn = load_turn(angles, a.rotary, a.interleaved, li);
-  float x[8];
-  widen8<DT>(w, x);
-  if (a.k_weight) norm<DT, D>(x, !is_v, weight, a.eps);
-  rotate(x, !is_v, turn, a.rotary, a.interleaved, li);
-  float m = mag8(x);
+  const bool turns = part.turns && angles && !is_v;
+  if (turns) turn = load_turn(angles, a.rotary, li);
+  float x[8], y[8];
+  widen8<DT>(w[0], x);
+  widen8<DT>(w[1], y);
+  if (a.k_weight) norm<DT, D>(x, y, !is_v, wt[0], wt[1], a.eps);
+  if (turns) rotate(x, y, turn, a.interleaved);
+  float m = fmaxf(mag8(x), mag8(y));
 #pragma unroll
   for (int o = TG / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
   const float s = fmaxf(old, scale_for(m)), inv = 1.f / s;
   if (!ok) return;
-  uint2* codes = static_cast<uint2*>(is_v ? a.v_pool : a.k_pool) + tile * a.bs * TG;
-  codes[row * TG + li] = quantise8(x, inv);
+  uint2* codes = static_cast<uint2*>(is_v ? a.v_pool : a.k_pool) + tile * a.bs * RV;
+  codes[row * RV + part.v0] = quantise8(x, inv);
+  codes[row * RV + part.v1] = quantise8(y, inv);
   if (s > old) {
-    for (int r = 0; r < row; ++r) rescale8(codes + r * TG + li, old * inv);
+    for (int r = 0; r < row; ++r) {
+      rescale8(codes + r * RV + part.v0, old * inv);
+      rescale8(codes + r * RV + part.v1, old * inv);
+    }
     if (li == 0) *scale = s;
   }
 }
@@ -753,26 +863,29 @@ pa_status check_rope_pointers(const RopeArgs& a, int head_dim) {
 }
 
 // How tokens of `rows` head rows go through shared memory: stages of a CTA (0: the
-// register kernel), bytes of them, CTAs.
+// register kernel), tokens of a stage, bytes of all stages, CTAs.
 struct Stream {
-  int stages, bytes, ctas;
+  int stages, together, bytes, ctas;
 };
 
-pa_status plan_stream(int tokens, int rows, int head_dim, int most, Stream* s) {
-  *s = {0, 0, tokens};
+pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int most, Stream* s) {
+  *s = {0, 1, 0, tokens};
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return PA_ERR_CUDA;
   if (tokens < kStreamTokens * sms) return PA_OK;
   // `most` CTAs of an SM where two stages of each fit its shared memory, else fewer
-  const int64_t token = (int64_t)rows * head_dim * 2;
+  const int64_t token = (int64_t)rows * head_dim * 2 + rotary * 4;
   for (int per_sm = most; per_sm; --per_sm) {
     const int64_t room = (227 * 1024) / per_sm - 5 * 1024;
     if (2 * token > room) continue;
-    s->stages = (int)(room / token < kMaxStages ? room / token : kMaxStages);
-    s->bytes = (int)(s->stages * token);
-    s->ctas = sms * per_sm;
+    while (s->together < kMaxTogether && 3 * 2 * s->together * token <= room) s->together *= 2;
+    const int64_t stage = s->together * token;
+    s->stages = (int)(room / stage < kMaxStages ? room / stage : kMaxStages);
+    s->bytes = (int)(s->stages * stage);
+    const int runs = (tokens - 1) / (kRun - 1) + 1;        // of fewer than kRun tokens
+    s->ctas = sms * per_sm > runs ? sms * per_sm : runs;
     break;
   }
   return PA_OK;
@@ -791,27 +904,26 @@ cudaError_t launch_blocks(const RopeArgs& a, const Stream& s, cudaStream_t strea
   // sequence has, a block's at most
   int window = BS < 32 ? BS : 32;
   while (window > 1 && (int64_t)window * a.B > a.total_q) window /= 2;
-  constexpr int heads = BlockShape<DT, D, BS>::kHeads;
+  constexpr int heads = BlockShape<D, BS>::kHeads;
   const int64_t kv = ((int64_t)a.total_q + window - 1) / window * ((a.H + heads - 1) / heads);
   if (kv + s.ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem(rope_append_q8_kernel<DT, D, BS>, s.bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(rope_append_q8_kernel<DT, D, BS>, dim3((unsigned)(kv + s.ctas)), kRowThreads,
-                    s.bytes, stream, a, (int)kv, window, s.stages);
+                    s.bytes, stream, a, (int)kv, window, s.stages, s.together);
 }
 
 template <int DT, int D>
 cudaError_t launch_q8(const RopeArgs& a, cudaStream_t stream) {
-  constexpr int TG = D / 8;
   if (!a.q_start) {
-    const int64_t groups = (int64_t)a.B * a.H * 2, per = kRowThreads / TG;
+    const int64_t groups = (int64_t)a.B * a.H * 2, per = kRowThreads / (D / 16);
     const int64_t kv = (groups + per - 1) / per;
     if (kv + a.total_q > 0x7FFFFFFF) return cudaErrorInvalidValue;
     return launch_pdl(rope_step_q8_kernel<DT, D>, dim3((unsigned)(kv + a.total_q)), kRowThreads, 0,
                       stream, a, (int)kv);
   }
   Stream s;
-  if (plan_stream(a.total_q, a.Hq, D, 3, &s) != PA_OK) return cudaErrorUnknown;
+  if (plan_stream(a.total_q, a.Hq, D, a.rotary, 3, &s) != PA_OK) return cudaErrorUnknown;
   switch (a.bs) {
     case 8: return launch_blocks<DT, D, 8>(a, s, stream);
     case 16: return launch_blocks<DT, D, 16>(a, s, stream);
@@ -823,14 +935,14 @@ cudaError_t launch_q8(const RopeArgs& a, cudaStream_t stream) {
 template <int DT, int D>
 cudaError_t launch_16(const RopeArgs& a, cudaStream_t stream) {
   Stream s;
-  if (plan_stream(a.total_q, a.Hq + 2 * a.H, D, 4, &s) != PA_OK) return cudaErrorUnknown;
+  if (plan_stream(a.total_q, a.Hq + 2 * a.H, D, a.rotary, 4, &s) != PA_OK) return cudaErrorUnknown;
   if (!s.stages)
     return launch_pdl(rope_append_kernel<DT, D>, dim3((unsigned)a.total_q), kRowThreads, 0, stream,
                       a);
   const cudaError_t e = allow_smem(rope_stream_kernel<DT, D>, s.bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(rope_stream_kernel<DT, D>, dim3((unsigned)s.ctas), kRowThreads, s.bytes,
-                    stream, a, s.stages);
+                    stream, a, s.stages, s.together);
 }
 
 }  // namespace
