@@ -104,6 +104,8 @@ struct Tail {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], red_bar[2];
   uint64_t sum_bar, drain;
   float qscale[2][GP];
+  uint32_t q[2][GP][D / 2];      // q as it is, of a segment and the one behind it
+  float inv[4][GP];              // per warp: 1 / the weights' sums of a finished segment
   float red[2][4][GP + 1];       // per warp: heads' maxima, the largest V scale
   struct alignas(8) {            // per warp: heads' running maxima, then 2^(before - now)
     float now[2 * GP];
@@ -177,7 +179,8 @@ template <>
 __device__ __forceinline__ void load_cols<16>(uint32_t t, float* v) {
   uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
         "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
@@ -192,7 +195,8 @@ template <>
 __device__ __forceinline__ void load_cols<24>(uint32_t t, float* v) {
   uint32_t r[24];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%24];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%25];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
@@ -209,7 +213,8 @@ template <>
 __device__ __forceinline__ void load_cols<32>(uint32_t t, float* v) {
   uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
@@ -228,9 +233,11 @@ template <>
 __device__ __forceinline__ void load_cols<48>(uint32_t t, float* v) {
   uint32_t r[48];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%48];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, [%49];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, [%49];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
         "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
@@ -557,41 +564,47 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------------- q digits --
+    // Once per segment and a loop over heads: the code is cold, so it is kept short.
     constexpr int W = D / 64;                   // 32-bit words of a lane and head
-    uint32_t now[GP][W], ahead[GP][W];          // this segment's q, and the next one's
-    auto load_q = [&](const Walk<TOKENS>& w, uint32_t (&x)[GP][W]) {
+    auto fetch_q = [&](const Walk<TOKENS>& w, int buf) {   // asynchronous, a segment ahead
       const int g0 = w.chunk * a.hch, gn = w.left > 0 ? min(a.hch, G - g0) : 0;
       const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) +
                           ((int64_t)w.b * a.Hq + w.h * G + g0) * (D / 2) + lane * W;
-#pragma unroll
-      for (int g = 0; g < GP; ++g)
-#pragma unroll
-        for (int e = 0; e < W; ++e) x[g][e] = g < gn ? q[g * (D / 2) + e] : 0u;
+#pragma unroll 1
+      for (int g = 0; g < gn; ++g)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                         smem_addr(&tail->q[buf][g][lane * W])),
+                     "l"(q + g * (D / 2)), "n"(4 * W)
+                     : "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int seg = 0;
-    load_q(walk, now);
+    fetch_q(walk, 0);
     while (walk.left > 0) {
       const int slot = seg & 1;
+      const int gn = min(a.hch, G - walk.chunk * a.hch);
       const int skip = min(walk.nt - walk.j, walk.left) - 1;   // to the segment's last tile
       walk.j += skip;
       walk.left -= skip;
       walk.next(a);
-      load_q(walk, ahead);
+      fetch_q(walk, slot ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
       if (!__all_sync(kAll, mbar_wait(&tail->q_empty[slot], ((seg >> 1) & 1) ^ 1, abort_flag,
                                       kLimitNs))) {
         ok = false;
         break;
       }
       uint8_t* op = smem + S::kQOff + slot * S::kOperand;
-#pragma unroll
-      for (int g = 0; g < GP; ++g) {
+#pragma unroll 1
+      for (int g = 0; g < gn; ++g) {
         float2 x[W];
         float m = 0.f;
         bool bad = false;
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-          x[e] = a.dtype == PA_BFLOAT16 ? widen2<PA_BFLOAT16>(now[g][e])
-                                        : widen2<PA_FLOAT16>(now[g][e]);
+          const uint32_t w = tail->q[slot][g][lane * W + e];
+          x[e] = a.dtype == PA_BFLOAT16 ? widen2<PA_BFLOAT16>(w) : widen2<PA_FLOAT16>(w);
           m = fmaxf(m, fmaxf(finite_mag(x[e].x), finite_mag(x[e].y)));
           bad |= !(fabsf(x[e].x) < CUDART_INF_F) || !(fabsf(x[e].y) < CUDART_INF_F);
         }
@@ -615,17 +628,14 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->q_full[slot]);
       ++seg;
-#pragma unroll
-      for (int g = 0; g < GP; ++g)
-#pragma unroll
-        for (int e = 0; e < W; ++e) now[g][e] = ahead[g][e];
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     // lengths out of range are reported; empty sequences get zero rows
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       const int L = a.lens[b];
       if ((L < 0 || L > a.max_seq_len) && lane == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
       if (L <= 0 || a.max_seq_len == 0) {
-        uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (int64_t)b * a.Hq * D);
+        uint4* row = static_cast<uint4*>(a.out) + (int64_t)b * a.Hq * (D / 8);
         for (int i = lane; i < a.Hq * (D / 8); i += 32) row[i] = make_uint4(0, 0, 0, 0);
       }
     }
@@ -663,7 +673,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     float x[TPR][GP];                           // scores of the tile ahead
     float l[GP], acc[GP], unit = 0.f;           // unit: of the tile behind
     float m_lane = -CUDART_INF_F;               // head `lane`: the running maximum
-    int t = 0, seg = 0;                         // tile; segment of tile t
+    int seg = 0;                                // segment of tile t
 
     // scores of tile u (n tokens left, segment sg) and their maxima, posted for all warps
     auto score_tile = [&](int u, int n, int sg, bool first, float ks, float vs) -> bool {
@@ -674,7 +684,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       float s[cols_for(S::kUsed)];
       load_cols<cols_for(S::kUsed)>(tmem + lanes + slot * N, s);
       // heads in pairs (two-wide fp32 arithmetic); a last odd one is paired with itself
-      const uint64_t c16 = f2_pack(1.f / 16.f, 1.f / 16.f), c256 = f2_pack(1.f / 256.f, 1.f / 256.f);
+      const uint64_t c16 = f2_pack(1.f / 16.f, 1.f / 16.f);
+      const uint64_t c256 = f2_pack(1.f / 256.f, 1.f / 256.f);
       const uint64_t ks2 = f2_pack(ks, ks);
 #pragma unroll
       for (int g = 0; g < GP; g += 2) {
@@ -712,7 +723,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       tc_fence_after();
       float o[cols_for(3 * GP)];
       load_cols<cols_for(3 * GP)>(tmem + lanes + (2 + slot) * N + par * 3 * GP, o);
-      const uint64_t c16 = f2_pack(1.f / 16.f, 1.f / 16.f), c256 = f2_pack(1.f / 256.f, 1.f / 256.f);
+      const uint64_t c16 = f2_pack(1.f / 16.f, 1.f / 16.f);
+      const uint64_t c256 = f2_pack(1.f / 256.f, 1.f / 256.f);
       const uint64_t unit2 = f2_pack(unit, unit);
 #pragma unroll
       for (int g = 0; g < GP; g += 2) {
@@ -742,27 +754,33 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
         if (lane == 0) mbar_arrive(&tail->sum_bar);
         if (!wait_all(&tail->sum_bar, D == 64 ? sg & 1 : 0)) return false;
       }
+      // once per segment: short code, a head to a lane where that is possible
       const int g0 = chunk * a.hch, gn = min(a.hch, G - g0);
+      const int64_t part = (2 * (int64_t)blockIdx.x + (sg > 0)) * a.hch;
+      if (lane < gn) {
+        const float* lr = &tail->lred[sg & 1][0][lane];
+        const float sum = (lr[0] + lr[GP]) + (lr[2 * GP] + lr[3 * GP]);
+        tail->inv[wq][lane] = 1.f / sum;
+        if (!whole && wq == 0) {
+          a.ws_m[part + lane] = tail->mred[sg & 1][lane];
+          a.ws_l[part + lane] = sum;
+        }
+      }
+      __syncwarp();
       if (r < D) {
-        const int64_t row0 = (int64_t)b * a.Hq + h * G + g0;
-        const int64_t part = (2 * (int64_t)blockIdx.x + (sg > 0)) * a.hch;
+        uint16_t* to = static_cast<uint16_t*>(a.out) + ((int64_t)b * a.Hq + h * G + g0) * D + r;
+        float* ws = a.ws_acc + part * D + r;
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
-          if (g >= gn) continue;
-          const float* lr = &tail->lred[sg & 1][0][g];
-          const float sum = (lr[0] + lr[GP]) + (lr[2 * GP] + lr[3 * GP]);
-          const float o = acc[g] + (D == 64 ? tail->half[g * 64 + (r & 63)] : 0.f);
-          if (whole) {
-            const float y = __fdividef(o, sum);
-            static_cast<uint16_t*>(a.out)[(row0 + g) * D + r] =
-                a.dtype == PA_BFLOAT16 ? narrow<PA_BFLOAT16>(y) : narrow<PA_FLOAT16>(y);
-          } else {
-            a.ws_acc[(part + g) * D + r] = o;
-            if (r == 0) {
-              a.ws_m[part + g] = tail->mred[sg & 1][g];
-              a.ws_l[part + g] = sum;
-            }
+          if (g < gn) {
+            const float o = acc[g] + (D == 64 ? tail->half[g * 64 + (r & 63)] : 0.f);
+            const float y = o * tail->inv[wq][g];
+            if (whole) *to = (uint16_t)(a.dtype == PA_BFLOAT16 ? pack2<PA_BFLOAT16>(y, y)
+                                                                 : pack2<PA_FLOAT16>(y, y));
+            else *ws = o;
           }
+          to += D;
+          ws += D;
         }
       }
 #pragma unroll
@@ -770,118 +788,121 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       return true;
     };
 
-    Walk<TOKENS> cur = walk;                    // tile t; walk runs ahead
-    float vs_cur = 0.f, ks_next, vs_next;
+    // One pass more than tiles at both ends (t = -1: only scores; t = tiles: only sums),
+    // so that each step stands once in the code: a second copy would be run cold.
+    Walk<TOKENS> cur = walk;                    // tile t; walk stands at tile t + 1
+    cur.left = 0;
+    float vs_cur = 0.f, ks_next, vs_next;       // scales of tile t; of tile t + 1
+    scales_of(walk, ks_next, vs_next);
     bool first = true, first_of_item = walk.j == 0;
-    int fin_b = 0, fin_h = 0, fin_chunk = 0;                // the segment that tile t - 1 finished
+    int fin_b = 0, fin_h = 0, fin_chunk = 0;    // the segment that tile t - 1 finished
     bool fin = false, fin_whole = false;
 #pragma unroll
     for (int g = 0; g < GP; ++g) l[g] = acc[g] = 0.f;
-    if (cur.left > 0) {
-      float ks;
-      scales_of(cur, ks, vs_cur);
-      walk.next(a);
-      scales_of(walk, ks_next, vs_next);
-      ok = score_tile(0, cur.L - cur.j * TOKENS, 0, true, ks, vs_cur);
-    }
-    while (ok && cur.left > 0) {
-      const int slot = t & 1;
-      const int n = cur.L - cur.j * TOKENS;     // tokens left from this tile on
-      const bool ends = cur.j + 1 == cur.nt || cur.left == 1;
+    for (int t = -1; in; ++t) {
+      const int slot = t & 1, seg_t = seg;
+      const bool have = cur.left > 0;
+      const bool ends = have && (cur.j + 1 == cur.nt || cur.left == 1);
       const Walk<TOKENS> ahead = walk;          // tile t + 1
-      float ks2 = 0.f, vs2 = 0.f;
+      float ks2 = 0.f, vs2 = 0.f, vmax = 0.f;
       if (ahead.left > 0) {
         walk.next(a);
         scales_of(walk, ks2, vs2);              // tile t + 2
       }
-      if (first) {
-        m_lane = -CUDART_INF_F;
+      if (have) {
+        const int n = cur.L - cur.j * TOKENS;     // tokens left from this tile on
+        if (first) {
+          m_lane = -CUDART_INF_F;
 #pragma unroll
-        for (int g = 0; g < GP; ++g) l[g] = 0.f;
-      }
-      if (!wait_all(&tail->red_bar[slot], (t >> 1) & 1)) { ok = false; break; }
-      float vmax = 0.f;
-      {
-        const float* red = &tail->red[slot][0][min(lane, GP)];
-        const float top = fmaxf(fmaxf(red[0], red[GP + 1]), fmaxf(red[2 * GP + 2], red[3 * GP + 3]));
-        vmax = __shfl_sync(kAll, top, GP);
-        if (lane < GP) {
-          const float now = fmaxf(m_lane, top);
-          tail->top[wq][slot].now[lane] = now;
-          tail->top[wq][slot].now[GP + lane] = ex2_approx(m_lane - now);
-          m_lane = now;
+          for (int g = 0; g < GP; ++g) l[g] = 0.f;
         }
+        if (!wait_all(&tail->red_bar[slot], (t >> 1) & 1)) { ok = false; break; }
+        {
+          const float* red = &tail->red[slot][0][min(lane, GP)];
+          const float top =
+              fmaxf(fmaxf(red[0], red[GP + 1]), fmaxf(red[2 * GP + 2], red[3 * GP + 3]));
+          vmax = __shfl_sync(kAll, top, GP);
+          if (lane < GP) {
+            const float now = fmaxf(m_lane, top);
+            tail->top[wq][slot].now[lane] = now;
+            tail->top[wq][slot].now[GP + lane] = ex2_approx(m_lane - now);
+            m_lane = now;
+          }
+          __syncwarp();
+        }
+        // weights, in units of the tile's largest V scale and 256 at most
+        const float to = vmax > 0.f ? vs_cur * (256.f / vmax) : 0.f;
+        const float* top = tail->top[wq][slot].now;
+        const uint64_t to2 = f2_pack(to, to);
+#pragma unroll
+        for (int g = 0; g < GP; g += 2) {
+          const int g1 = g + 1 < GP ? g + 1 : g;
+          const uint64_t m2 = f2_pack(top[g], top[g1]);
+          uint64_t sum = f2_mul(f2_pack(l[g], l[g1]), f2_pack(top[GP + g], top[GP + g1]));
+#pragma unroll
+          for (int v = 0; v < TPR; ++v) {
+            float p0, p1;                         // 0 behind the end
+            f2_unpack(f2_sub(f2_pack(x[v][g], x[v][g1]), m2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            const uint64_t p2 = f2_pack(p0, p1);
+            sum = f2_add(sum, p2);
+            float w0, w1;
+            f2_unpack(f2_mul(p2, to2), w0, w1);
+            uint32_t d[3];
+            digits2(__floats2half2_rn(w0, w1), d);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const int row = (v * 3 + i) * GP + g;
+              put[row & 7][slot * S::kOperand + row * 128] = (uint8_t)d[i];
+              if (g1 > g)
+                put[(row + 1) & 7][slot * S::kOperand + (row + 1) * 128] = (uint8_t)(d[i] >> 8);
+            }
+          }
+          float l0, l1;
+          f2_unpack(sum, l0, l1);
+          l[g] = l0;
+          if (g1 > g) l[g1] = l1;
+        }
+        // tokens behind the end: zero their V, so that 0 times garbage stays 0
+        if (n < TOKENS) {
+          const int u = 2 * t + 1;
+          if (!wait_all(&tail->full[u % R], (u / R) & 1)) { ok = false; break; }
+          uint8_t* vt = smem + (u % R) * kStageBytes;
+#pragma unroll
+          for (int v = 0; v < TPR; ++v)
+            if (r * TPR + v >= n) {
+#pragma unroll
+              for (int c = 0; c < D; c += 16)
+                *reinterpret_cast<uint4*>(vt + swizzled(r, v * D + c)) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        fence_async_smem();
+        tc_fence_before();
         __syncwarp();
-      }
-      // weights, in units of the tile's largest V scale and 256 at most
-      const float to = vmax > 0.f ? vs_cur * (256.f / vmax) : 0.f;
-      const float* top = tail->top[wq][slot].now;
-      const uint64_t to2 = f2_pack(to, to);
+        if (lane == 0) mbar_arrive(&tail->p_full[slot]);
+        if (ends) {                               // what finish() needs of tile t's segment
 #pragma unroll
-      for (int g = 0; g < GP; g += 2) {
-        const int g1 = g + 1 < GP ? g + 1 : g;
-        const uint64_t m2 = f2_pack(top[g], top[g1]);
-        uint64_t sum = f2_mul(f2_pack(l[g], l[g1]), f2_pack(top[GP + g], top[GP + g1]));
+          for (int g = 0; g < GP; ++g) {
+            float sum = l[g];
 #pragma unroll
-        for (int v = 0; v < TPR; ++v) {
-          float p0, p1;                         // 0 behind the end
-          f2_unpack(f2_sub(f2_pack(x[v][g], x[v][g1]), m2), p0, p1);
-          p0 = ex2_approx(p0);
-          p1 = ex2_approx(p1);
-          const uint64_t p2 = f2_pack(p0, p1);
-          sum = f2_add(sum, p2);
-          float w0, w1;
-          f2_unpack(f2_mul(p2, to2), w0, w1);
-          uint32_t d[3];
-          digits2(__floats2half2_rn(w0, w1), d);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const int row = (v * 3 + i) * GP + g;
-            put[row & 7][slot * S::kOperand + row * 128] = (uint8_t)d[i];
-            if (g1 > g)
-              put[(row + 1) & 7][slot * S::kOperand + (row + 1) * 128] = (uint8_t)(d[i] >> 8);
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+            if (lane == g) tail->lred[seg & 1][wq][g] = sum;
           }
+          if (wq == 0 && lane < GP) tail->mred[seg & 1][lane] = m_lane;
+          if (lane == 0) mbar_arrive(&tail->q_empty[seg & 1]);
+          ++seg;
         }
-        float l0, l1;
-        f2_unpack(sum, l0, l1);
-        l[g] = l0;
-        if (g1 > g) l[g1] = l1;
-      }
-      // tokens behind the end: zero their V, so that 0 times garbage stays 0
-      if (n < TOKENS) {
-        const int u = 2 * t + 1;
-        if (!wait_all(&tail->full[u % R], (u / R) & 1)) { ok = false; break; }
-        uint8_t* vt = smem + (u % R) * kStageBytes;
-#pragma unroll
-        for (int v = 0; v < TPR; ++v)
-          if (r * TPR + v >= n) {
-#pragma unroll
-            for (int c = 0; c < D; c += 16)
-              *reinterpret_cast<uint4*>(vt + swizzled(r, v * D + c)) = make_uint4(0, 0, 0, 0);
-          }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->p_full[slot]);
-      const int seg_t = seg;
-      if (ends) {                               // what finish() needs of tile t's segment
-#pragma unroll
-        for (int g = 0; g < GP; ++g) {
-          float sum = l[g];
-#pragma unroll
-          for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-          if (lane == g) tail->lred[seg & 1][wq][g] = sum;
-        }
-        if (wq == 0 && lane < GP) tail->mred[seg & 1][lane] = m_lane;
-        if (lane == 0) mbar_arrive(&tail->q_empty[seg & 1]);
-        ++seg;
       }
       // what finish() reads is written again only behind the red_bar that score_tile posts
       if (t > 0 && !add_tile(t - 1)) { ok = false; break; }
-      if (fin && !finish(seg_t - 1, fin_b, fin_h, fin_chunk, fin_whole, false)) { ok = false; break; }
-      if (ahead.left > 0 &&
-          !score_tile(t + 1, ahead.L - ahead.j * TOKENS, seg, ends, ks_next, vs_next)) {
+      if (fin && !finish(seg_t - 1, fin_b, fin_h, fin_chunk, fin_whole, !have)) {
+        ok = false;
+        break;
+      }
+      if (ahead.left <= 0 && !have) break;
+      if (ahead.left > 0 && !score_tile(t + 1, ahead.L - ahead.j * TOKENS, seg, t < 0 || ends,
+                                        ks_next, vs_next)) {
         ok = false;
         break;
       }
@@ -894,14 +915,12 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
         fin_whole = first_of_item && cur.j + 1 == cur.nt;
         first_of_item = true;                   // the next segment begins at tile 0
       }
-      first = ends;
+      first = t < 0 || ends;
       cur = ahead;
       vs_cur = vs_next;
       ks_next = ks2;
       vs_next = vs2;
-      ++t;
     }
-    if (ok && fin) ok = add_tile(t - 1) && finish(seg - 1, fin_b, fin_h, fin_chunk, fin_whole, true);
     if (!ok) {
       *abort_flag = 1;
       if (lane == 0) report(a.status_dev, PA_ERR_TIMEOUT);
@@ -1044,7 +1063,7 @@ struct Plan {
 
 Plan plan_of(int Hq, int H, int D, int max_seq_len) {
   Plan p;
-  const int G = Hq / H, most = D == 128 ? 16 : 8;
+  const int G = Hq / H, most = 8;
   p.chunks = (G + most - 1) / most;
   p.hch = (G + p.chunks - 1) / p.chunks;
   const int tokens = kTileRows * 128 / D;
@@ -1085,8 +1104,7 @@ cudaError_t launch_heads(const CUtensorMap& k, const CUtensorMap& v, const Q8Arg
   if (a.hch <= 2) return launch_decode<D, 2>(k, v, a, grid, device, stream);
   if (a.hch <= 4) return launch_decode<D, 4>(k, v, a, grid, device, stream);
   if (a.hch <= 5) return launch_decode<D, 5>(k, v, a, grid, device, stream);
-  if (D == 64 || a.hch <= 8) return launch_decode<D, 8>(k, v, a, grid, device, stream);
-  return launch_decode<128, 16>(k, v, a, grid, device, stream);
+  return launch_decode<D, 8>(k, v, a, grid, device, stream);
 }
 
 }  // namespace

@@ -5,8 +5,8 @@
 // One byte is read and two are written per element, so the bound is 3 bytes per
 // element at HBM bandwidth.  The two layouts differ in order: codes are
 // [head][row][dim], the 16-bit block is [row][head][dim].  Threads run in the
-// order of the 16-bit block, so the stores of a warp are contiguous and its
-// loads are whole 64- or 128-byte rows.
+// order of the 16-bit block, eight codes each, so that a warp's stores are one
+// contiguous 512 bytes and its loads are whole 64- or 128-byte rows.
 #include "pa_common.cuh"
 #include "pa_q8.cuh"
 
@@ -14,17 +14,17 @@ namespace pa {
 namespace {
 
 constexpr int kExpandThreads = 256;
-constexpr int kExpandVecs = 2;      // 16-code vectors per thread and pool
+constexpr int kExpandVecs = 4;      // 8-code vectors per thread and pool
 
 struct ExpandArgs {
   uint4* k_out;
   uint4* v_out;
-  const uint4* k8;
-  const uint4* v8;
+  const uint2* k8;
+  const uint2* v8;
   const float* k_scale;
   const float* v_scale;
   const int32_t* pairs;
-  int H, bs, vecs, chunks;          // vecs: 16-code vectors of a block and pool
+  int H, bs, vecs, chunks;          // vecs: 8-code vectors of a block and pool
   int src_blocks, dst_blocks;
   int32_t* status_dev;
 };
@@ -37,12 +37,12 @@ __device__ __forceinline__ uint32_t expand2(uint32_t codes, float scale) {
   // past the type's largest value (the code above a magnitude near it): saturate; NaN stays
   a = a > most ? most : (a < -most ? -most : a);
   b = b > most ? most : (b < -most ? -most : b);
-  return narrow2<DT>(a, b);
+  return pack2<DT>(a, b);
 }
 
 template <int DT, int D>
 __global__ void __launch_bounds__(kExpandThreads) expand_q8_kernel(const ExpandArgs a) {
-  constexpr int RV = D / 16;        // vectors of a head's row
+  constexpr int RV = D / 8;         // vectors of a head's row
   allow_next_grid();
   wait_prior_grid();
   const int pair = (int)blockIdx.x / a.chunks, chunk = (int)blockIdx.x - pair * a.chunks;
@@ -51,9 +51,9 @@ __global__ void __launch_bounds__(kExpandThreads) expand_q8_kernel(const ExpandA
     if (threadIdx.x == 0 && chunk == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
     return;
   }
-  const int64_t from = (int64_t)src * a.vecs, to = (int64_t)dst * a.vecs * 2;
+  const int64_t from = (int64_t)src * a.vecs, to = (int64_t)dst * a.vecs;
   const int i0 = chunk * (kExpandThreads * kExpandVecs) + (int)threadIdx.x;
-  uint4 w[kExpandVecs][2];
+  uint2 w[kExpandVecs][2];
   float s[kExpandVecs][2];
 #pragma unroll
   for (int u = 0; u < kExpandVecs; ++u) {
@@ -73,13 +73,11 @@ __global__ void __launch_bounds__(kExpandThreads) expand_q8_kernel(const ExpandA
     if (i < a.vecs) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        uint4* out = (p ? a.v_out : a.k_out) + to + 2 * (int64_t)i;
-        const uint4 c = w[u][p];
+        const uint2 c = w[u][p];
         const float f = s[u][p];
-        out[0] = make_uint4(expand2<DT>(c.x, f), expand2<DT>(c.x >> 16, f), expand2<DT>(c.y, f),
-                            expand2<DT>(c.y >> 16, f));
-        out[1] = make_uint4(expand2<DT>(c.z, f), expand2<DT>(c.z >> 16, f), expand2<DT>(c.w, f),
-                            expand2<DT>(c.w >> 16, f));
+        (p ? a.v_out : a.k_out)[to + i] =
+            make_uint4(expand2<DT>(c.x, f), expand2<DT>(c.x >> 16, f), expand2<DT>(c.y, f),
+                       expand2<DT>(c.y >> 16, f));
       }
     }
   }
@@ -110,13 +108,13 @@ extern "C" pa_status pa_expand_blocks_q8(void* k_pool, void* v_pool, const void*
   if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_pool8) || !aligned16(v_pool8) ||
       ((uintptr_t)k_scale & 3u) || ((uintptr_t)v_scale & 3u))
     return PA_ERR_INVALID_ARG;
-  const int64_t vecs = (int64_t)block_size * num_kv_heads * head_dim / 16;
-  if (vecs > (1 << 24)) return PA_ERR_INVALID_ARG;
+  const int64_t vecs = (int64_t)block_size * num_kv_heads * head_dim / 8;
+  if (vecs > (1 << 25)) return PA_ERR_INVALID_ARG;
   const int per = kExpandThreads * kExpandVecs;
   const int64_t chunks = (vecs + per - 1) / per;
   if (chunks * num_pairs > 0x7FFFFFFF) return PA_ERR_INVALID_ARG;
-  const ExpandArgs a = {(uint4*)k_pool, (uint4*)v_pool, (const uint4*)k_pool8,
-                        (const uint4*)v_pool8, k_scale, v_scale, block_pairs, num_kv_heads,
+  const ExpandArgs a = {(uint4*)k_pool, (uint4*)v_pool, (const uint2*)k_pool8,
+                        (const uint2*)v_pool8, k_scale, v_scale, block_pairs, num_kv_heads,
                         block_size, (int)vecs, (int)chunks, src_num_blocks, dst_num_blocks,
                         status_dev};
   const dim3 grid((unsigned)(chunks * num_pairs));

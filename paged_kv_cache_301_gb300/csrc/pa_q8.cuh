@@ -49,4 +49,15 @@ __device__ __forceinline__ float2 e4m3_widen2(uint32_t w) {
   return __half22float2(__half2(h));
 }
 
+// Two fp32 values rounded to nearest in one conversion, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (DT == PA_BFLOAT16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  const __half2 p = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
 }  // namespace pa

@@ -105,17 +105,6 @@ __device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
   x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
 }
 
-// Two values rounded to nearest in one conversion, the first in the low half.
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if (DT == PA_BFLOAT16) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&p);
-  }
-  const __half2 p = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
 template <int DT>
 __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
   return make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
@@ -309,7 +298,7 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
 // copies, so that no computing warp waits for one to be read out.  Reads of later
 // tokens and writes of earlier ones are in flight all the time, which the register
 // kernel above cannot hold at the occupancy that a row's registers leave it.
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 3;                  // a fourth costs 10%: 222 KB of an SM's 228 for four CTAs
 constexpr int kComputeWarps = kRowThreads / 32 - 1;
 constexpr int kRun = kRowThreads;              // tokens of a CTA at most: one thread places one
 constexpr int kStreamTokens = 8;               // tokens per SM from which on it is taken
