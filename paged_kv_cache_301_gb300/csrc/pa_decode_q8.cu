@@ -596,7 +596,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
         break;
       }
       uint8_t* op = smem + S::kQOff + slot * S::kOperand;
-#pragma unroll 1
+#pragma unroll 4
       for (int g = 0; g < gn; ++g) {
         float2 x[W];
         float m = 0.f;
@@ -942,10 +942,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
 // takes a head's maximum and weights, the other threads are elements of a head, the
 // parts dealt out to kJoinThreads / D groups of them.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinHeads = 2;
 constexpr int kJoinAhead = 4;                  // parts of a group asked for at once
 
-template <int D>
+template <int D, int kJoinHeads>
 __global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, int grid) {
   constexpr int GROUPS = kJoinThreads / D;
   __shared__ float s_w[kJoinHeads][kMaxGrid];
@@ -1202,12 +1201,14 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   if (work / grid >= (1ll << 31)) return PA_ERR_INVALID_ARG;
   cudaError_t e = head_dim == 128 ? launch_heads<128>(k, v, a, grid, device, stream)
                                   : launch_heads<64>(k, v, a, grid, device, stream);
-  // an item of one tile is never cut
+  // an item of one tile is never cut; two heads to a joining CTA, four of wider groups
+  // (all joining CTAs are then resident at once)
   if (e == cudaSuccess && p.tiles > 1 && grid > 1) {
-    const dim3 joins((unsigned)(grid - 1), (unsigned)((p.hch + kJoinHeads - 1) / kJoinHeads));
-    e = head_dim == 128
-            ? launch_pdl(join_q8_kernel<128>, joins, kJoinThreads, 0, stream, a, grid)
-            : launch_pdl(join_q8_kernel<64>, joins, kJoinThreads, 0, stream, a, grid);
+    const int heads = p.hch <= 4 ? 2 : 4;
+    const dim3 joins((unsigned)(grid - 1), (unsigned)((p.hch + heads - 1) / heads));
+    auto join = head_dim == 128 ? (heads == 2 ? join_q8_kernel<128, 2> : join_q8_kernel<128, 4>)
+                                : (heads == 2 ? join_q8_kernel<64, 2> : join_q8_kernel<64, 4>);
+    e = launch_pdl(join, joins, kJoinThreads, 0, stream, a, grid);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
