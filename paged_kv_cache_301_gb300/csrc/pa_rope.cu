@@ -147,30 +147,48 @@ __device__ __forceinline__ uint4 pick(bool first, uint4 x, uint4 y) {
   return make_uint4(first ? x.x : y.x, first ? x.y : y.y, first ? x.z : y.z, first ? x.w : y.w);
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // RMS norm of a head row over its D/16 lanes.  Called by whole warps (it shuffles);
 // `on`: the group's row is normed, by w0 and w1, the weight's vectors v0 and v1.
+// Two-wide fp32 arithmetic: these kernels issue nearly as much as they move.
 template <int DT, int D>
 __device__ __forceinline__ void norm(float (&a)[8], float (&b)[8], bool on, uint4 w0,
                                      uint4 w1, float eps) {
-  float ss = 0.f;
+  using namespace sm100;
+  uint64_t sum = 0;                            // two zeros
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t p = f2_pack(a[i], a[i + 1]), q = f2_pack(b[i], b[i + 1]);
+    sum = f2_fma(p, p, f2_fma(q, q, sum));
+  }
+  float s0, s1;
+  f2_unpack(sum, s0, s1);
+  float ss = s0 + s1;
 #pragma unroll
   for (int o = D / 32; o; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
   if (on) {
     const float r = rsqrtf(ss * (1.f / D) + eps);
+    const uint64_t r2 = f2_pack(r, r);
     float w[8];
     widen8<DT>(w0, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = a[i] * r * w[i];
+    for (int i = 0; i < 8; i += 2)
+      f2_unpack(mul2(mul2(f2_pack(a[i], a[i + 1]), r2), f2_pack(w[i], w[i + 1])), a[i], a[i + 1]);
     widen8<DT>(w1, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = b[i] * r * w[i];
+    for (int i = 0; i < 8; i += 2)
+      f2_unpack(mul2(mul2(f2_pack(b[i], b[i + 1]), r2), f2_pack(w[i], w[i + 1])), b[i], b[i + 1]);
   }
 }
 
 __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Turn& t,
                                        int interleaved) {
+  using namespace sm100;
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -182,10 +200,11 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Turn&
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = a[i], q = b[i];
-      a[i] = p * t.c[i] - q * t.s[i];
-      b[i] = q * t.c[i] + p * t.s[i];
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t p = f2_pack(a[i], a[i + 1]), q = f2_pack(b[i], b[i + 1]);
+      const uint64_t c = f2_pack(t.c[i], t.c[i + 1]), s = f2_pack(t.s[i], t.s[i + 1]);
+      f2_unpack(f2_sub(mul2(p, c), mul2(q, s)), a[i], a[i + 1]);
+      f2_unpack(f2_fma(q, c, mul2(p, s)), b[i], b[i + 1]);
     }
   }
 }
@@ -533,23 +552,53 @@ __device__ __forceinline__ void rescale8(uint2* p, float ratio) {
                   e4m3x4(c.x * ratio, c.y * ratio, d.x * ratio, d.y * ratio));
 }
 
-__device__ __forceinline__ float mag8(const float (&x)[8]) {
+// The largest finite magnitude of 16 elements.  A NaN is never the largest; an
+// infinity, which would be, sends the lane through them again.
+__device__ __forceinline__ float mag16(const float (&a)[8], const float (&b)[8]) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_mag(x[i]));
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(a[i]), fabsf(b[i])));
+  if (__float_as_uint(m) == 0x7F800000u) {
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(finite_mag(a[i]), finite_mag(b[i])));
+  }
   return m;
 }
 
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
-  return make_uint2(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                    e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+// The same of 16 stored elements: their magnitudes order as their bits do, two at a
+// time; from the infinity's bits on they are not finite.
+template <int DT>
+__device__ __forceinline__ float mag16(const uint4& a, const uint4& b) {
+  constexpr uint32_t inf = DT == PA_BFLOAT16 ? 0x7F80u : 0x7C00u;
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  if (m >= inf) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+      if (lo < inf) m = max(m, lo);
+      if (hi < inf) m = max(m, hi);
+    }
+  }
+  return widen2<DT>(m).x;
 }
 
-// The new rows [r0, r1) of block j of sequence b, tokens t0 .., for the KV heads from
-// h0 on that the CTA's threads cover: a head has kHead threads, whose groups hold
-// rows g, g + NG, ...  All older rows are below r0.  Keys are normed and rotated
-// twice, for the largest magnitude and for the codes: the raw rows take a quarter
-// of the registers.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
+  const uint64_t i2 = sm100::f2_pack(inv, inv);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    sm100::f2_unpack(mul2(sm100::f2_pack(x[i], x[i + 1]), i2), y[i], y[i + 1]);
+  return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+}
+
+// How a CTA covers a block's rows: a head has kHead threads, whose groups hold rows
+// g, g + NG, ...
 template <int D, int BS>
 struct BlockShape {
   static constexpr int TG = D / 16;
@@ -558,136 +607,180 @@ struct BlockShape {
   static constexpr int NG = kHead / TG, RPT = BS / NG;    // groups, rows of each
 };
 
+// A block with new rows: [r0, r0 + n), tokens t ..; older rows are below r0.
+struct NewRows {
+  int t, pos, n, blk;          // first token, its position, rows, physical block
+};
+
+// Keys and values of tokens [t0, t0 + n) (kRowThreads at most) to the 8-bit cache: the
+// blocks whose first new token is among them, for `parts` groups of KV heads from
+// `part` on.  A block and a group of heads is one item: its largest magnitudes are
+// taken over the CTA, then its codes are made.  The next item's rows are asked for
+// before an item is worked on.
 template <int DT, int D, int BS>
-__device__ __forceinline__ void store_block(const RopeArgs& a, int b, int j, int h0, int t0, int r0,
-                                            int r1) {
+__device__ __forceinline__ void store_run(const RopeArgs& a, int t0, int n, int part, int parts) {
   using S = BlockShape<D, BS>;
   constexpr int TG = S::TG, NG = S::NG, RPT = S::RPT, NW = S::kHead / 32, RV = D / 8;
-  __shared__ float s_mag[kRowThreads / 32][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int mine = threadIdx.x / S::kHead, h = h0 + mine;
-  const int li = threadIdx.x % TG, grp = threadIdx.x % S::kHead / TG;
-  const Part part = part_of(li, a.rotary, a.interleaved);
-  const int32_t blk = a.tables[(int64_t)b * a.max_blocks + j];
-  if (blk < 0 || blk >= a.num_blocks) {
-    if (threadIdx.x == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-    return;
-  }
-  const bool in = h < a.H;
-  const int64_t tile = (int64_t)blk * a.H + h;
-  uint2* kc = static_cast<uint2*>(a.k_pool) + tile * (BS * RV);
-  uint2* vc = static_cast<uint2*>(a.v_pool) + tile * (BS * RV);
-  uint4 wt[2] = {}, kw[RPT][2], vw[RPT][2];
-  const float* angles[RPT];
-  bool live[RPT], any = false;
-#pragma unroll
-  for (int u = 0; u < RPT; ++u) {
-    const int row = grp + u * NG, t = t0 + row - r0;
-    live[u] = in && row >= r0 && row < r1;
-    kw[u][0] = kw[u][1] = vw[u][0] = vw[u][1] = make_uint4(0, 0, 0, 0);
-    if (live[u]) {
-      const uint4* k = reinterpret_cast<const uint4*>(a.key) + t * (a.kv_stride / 8) + h * RV;
-      const uint4* v = reinterpret_cast<const uint4*>(a.value) + t * (a.kv_stride / 8) + h * RV;
-      kw[u][0] = k[part.v0];
-      kw[u][1] = k[part.v1];
-      vw[u][0] = v[part.v0];
-      vw[u][1] = v[part.v1];
+  constexpr int WARPS = kRowThreads / 32;
+  __shared__ NewRows s_list[kRowThreads];
+  __shared__ int s_count[WARPS];
+  __shared__ float s_mag[2][WARPS][2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int mine = tid / S::kHead, li = tid % TG, grp = tid % S::kHead / TG;
+  const Part el = part_of(li, a.rotary, a.interleaved);
+
+  // every thread places a token; those that begin a block's new rows make the list
+  NewRows first = {t0 + tid, 0, 0, -1};
+  bool begins = false;
+  if (tid < n) {
+    bool bad;
+    const Place at = place_token(a, first.t, &bad);
+    if (at.ok) {
+      const int row = at.pos % BS;
+      begins = row == 0 || first.t == a.q_start[at.b];
+      if (begins) {
+        first.pos = at.pos;
+        first.n = min(a.q_start[at.b + 1] - first.t, BS - row);
+        first.blk = a.tables[(int64_t)at.b * a.max_blocks + at.pos / BS];
+        if (first.blk < 0 || first.blk >= a.num_blocks) {
+          if (part == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+          begins = false;
+        }
+      }
     }
   }
+  const uint32_t ballot = __ballot_sync(kAll, begins);
+  if (lane == 0) s_count[warp] = __popc(ballot);
+  __syncthreads();
+  int before = 0, blocks = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    before += w < warp ? s_count[w] : 0;
+    blocks += s_count[w];
+  }
+  if (begins) s_list[before + __popc(ballot & ((1u << lane) - 1))] = first;
+  __syncthreads();
+
+  uint4 wt[2] = {};
   if (a.k_weight) {
-    wt[0] = reinterpret_cast<const uint4*>(a.k_weight)[part.v0];
-    wt[1] = reinterpret_cast<const uint4*>(a.k_weight)[part.v1];
+    wt[0] = reinterpret_cast<const uint4*>(a.k_weight)[el.v0];
+    wt[1] = reinterpret_cast<const uint4*>(a.k_weight)[el.v1];
   }
-  float k_old = 0.f, v_old = 0.f;
-  if (in && r0 > 0) {
-    k_old = a.k_scale[tile];
-    v_old = a.v_scale[tile];
-  }
+  const int items = blocks * parts;
+  uint4 kn[RPT][2], vn[RPT][2];                // the next item's rows
+  auto ask = [&](int item) {
+    const NewRows at = s_list[item / parts];
+    const int h = (part + item % parts) * S::kHeads + mine, r0 = at.pos % BS;
 #pragma unroll
-  for (int u = 0; u < RPT; ++u) {
-    const int row = grp + u * NG;
-    angles[u] = nullptr;
-    if (live[u]) {
-      angles[u] = angles_of(a, t0 + row - r0, j * BS + row, &live[u]);
-      if (!live[u] && li == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-    }
-    any |= live[u];
-  }
-  auto new_key = [&](int u, float (&x)[8], float (&y)[8]) {   // whole warps
-    widen8<DT>(kw[u][0], x);
-    widen8<DT>(kw[u][1], y);
-    if (a.k_weight) norm<DT, D>(x, y, true, wt[0], wt[1], a.eps);
-    if (part.turns && angles[u]) {
-      rotate(x, y, load_turn(angles[u], a.rotary, li), a.interleaved);
+    for (int u = 0; u < RPT; ++u) {
+      const int row = grp + u * NG;
+      kn[u][0] = kn[u][1] = vn[u][0] = vn[u][1] = make_uint4(0, 0, 0, 0);
+      if (h < a.H && row >= r0 && row < r0 + at.n) {
+        const int64_t from = (at.t + row - r0) * (a.kv_stride / 8) + h * RV;
+        const uint4* k = reinterpret_cast<const uint4*>(a.key) + from;
+        const uint4* v = reinterpret_cast<const uint4*>(a.value) + from;
+        kn[u][0] = k[el.v0];
+        kn[u][1] = k[el.v1];
+        vn[u][0] = v[el.v0];
+        vn[u][1] = v[el.v1];
+      }
     }
   };
-  float km = 0.f, vm = 0.f;
-#pragma unroll
-  for (int u = 0; u < RPT; ++u) {
-    float x[8], y[8];
-    new_key(u, x, y);
-    if (live[u]) {
-      km = fmaxf(km, fmaxf(mag8(x), mag8(y)));
-      widen8<DT>(vw[u][0], x);
-      widen8<DT>(vw[u][1], y);
-      vm = fmaxf(vm, fmaxf(mag8(x), mag8(y)));
+  if (items > 0) ask(0);
+  for (int item = 0; item < items; ++item) {
+    const NewRows at = s_list[item / parts];
+    const int h = (part + item % parts) * S::kHeads + mine, r0 = at.pos % BS;
+    const bool in = h < a.H;
+    const int64_t tile = (int64_t)at.blk * a.H + h;
+    uint2* kc = static_cast<uint2*>(a.k_pool) + tile * (BS * RV);
+    uint2* vc = static_cast<uint2*>(a.v_pool) + tile * (BS * RV);
+    float k_old = 0.f, v_old = 0.f;
+    if (in && r0 > 0) {
+      k_old = a.k_scale[tile];
+      v_old = a.v_scale[tile];
     }
-  }
+    float kx[RPT][8], ky[RPT][8];
+    uint4 vw[RPT][2];
+    bool live[RPT], any = false;
+    float km = 0.f, vm = 0.f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    km = fmaxf(km, __shfl_xor_sync(kAll, km, o));
-    vm = fmaxf(vm, __shfl_xor_sync(kAll, vm, o));
-  }
-  __syncthreads();                    // the last block's s_mag is read
-  if (lane == 0) {
-    s_mag[warp][0] = km;
-    s_mag[warp][1] = vm;
-  }
-  if (!__syncthreads_or(any)) return; // no row left to write: scales stay
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    km = fmaxf(km, s_mag[mine * NW + w][0]);
-    vm = fmaxf(vm, s_mag[mine * NW + w][1]);
-  }
-  const float ks = fmaxf(k_old, scale_for(km)), vs = fmaxf(v_old, scale_for(vm));
-  const float k_inv = 1.f / ks, v_inv = 1.f / vs;
-#pragma unroll
-  for (int u = 0; u < RPT; ++u) {
-    const int row = grp + u * NG;
-    float x[8], y[8];
-    new_key(u, x, y);
-    if (live[u]) {
-      kc[row * RV + part.v0] = quantise8(x, k_inv);
-      kc[row * RV + part.v1] = quantise8(y, k_inv);
-      widen8<DT>(vw[u][0], x);
-      widen8<DT>(vw[u][1], y);
-      vc[row * RV + part.v0] = quantise8(x, v_inv);
-      vc[row * RV + part.v1] = quantise8(y, v_inv);
-    } else if (in && row < r0) {
-      if (ks > k_old) {
-        rescale8(kc + row * RV + part.v0, k_old * k_inv);
-        rescale8(kc + row * RV + part.v1, k_old * k_inv);
+    for (int u = 0; u < RPT; ++u) {
+      const int row = grp + u * NG;
+      vw[u][0] = vn[u][0];
+      vw[u][1] = vn[u][1];
+      widen8<DT>(kn[u][0], kx[u]);
+      widen8<DT>(kn[u][1], ky[u]);
+      live[u] = in && row >= r0 && row < r0 + at.n;
+      const float* angles = nullptr;
+      if (live[u]) {
+        angles = angles_of(a, at.t + row - r0, at.pos - r0 + row, &live[u]);
+        if (!live[u] && li == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
       }
-      if (vs > v_old) {
-        rescale8(vc + row * RV + part.v0, v_old * v_inv);
-        rescale8(vc + row * RV + part.v1, v_old * v_inv);
+      any |= live[u];
+      if (a.k_weight) norm<DT, D>(kx[u], ky[u], true, wt[0], wt[1], a.eps);
+      if (el.turns && angles)
+        rotate(kx[u], ky[u], load_turn(angles, a.rotary, li), a.interleaved);
+      if (live[u]) {
+        km = fmaxf(km, mag16(kx[u], ky[u]));
+        vm = fmaxf(vm, mag16<DT>(vw[u][0], vw[u][1]));
       }
     }
-  }
-  if (in && threadIdx.x % S::kHead == 0) {
-    a.k_scale[tile] = ks;
-    a.v_scale[tile] = vs;
+    if (item + 1 < items) ask(item + 1);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      km = fmaxf(km, __shfl_xor_sync(kAll, km, o));
+      vm = fmaxf(vm, __shfl_xor_sync(kAll, vm, o));
+    }
+    // two sets of maxima: the set of the item before last has been read by all
+    float (*mag)[2] = s_mag[item & 1];
+    if (lane == 0) {
+      mag[warp][0] = km;
+      mag[warp][1] = vm;
+    }
+    if (!__syncthreads_or(any)) continue;      // no row left to write: scales stay
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      km = fmaxf(km, mag[mine * NW + w][0]);
+      vm = fmaxf(vm, mag[mine * NW + w][1]);
+    }
+    const float ks = fmaxf(k_old, scale_for(km)), vs = fmaxf(v_old, scale_for(vm));
+    const float k_inv = 1.f / ks, v_inv = 1.f / vs;
+#pragma unroll
+    for (int u = 0; u < RPT; ++u) {
+      const int row = grp + u * NG;
+      if (live[u]) {
+        float x[8], y[8];
+        kc[row * RV + el.v0] = quantise8(kx[u], k_inv);
+        kc[row * RV + el.v1] = quantise8(ky[u], k_inv);
+        widen8<DT>(vw[u][0], x);
+        widen8<DT>(vw[u][1], y);
+        vc[row * RV + el.v0] = quantise8(x, v_inv);
+        vc[row * RV + el.v1] = quantise8(y, v_inv);
+      } else if (in && row < r0) {
+        if (ks > k_old) {
+          rescale8(kc + row * RV + el.v0, k_old * k_inv);
+          rescale8(kc + row * RV + el.v1, k_old * k_inv);
+        }
+        if (vs > v_old) {
+          rescale8(vc + row * RV + el.v0, v_old * v_inv);
+          rescale8(vc + row * RV + el.v1, v_old * v_inv);
+        }
+      }
+    }
+    if (in && tid % S::kHead == 0) {
+      a.k_scale[tile] = ks;
+      a.v_scale[tile] = vs;
+    }
   }
 }
 
-// Prompts and chunks.  CTAs [0, kv_ctas) hold a window of tokens (32 at most) and the
-// KV heads their threads cover, and write the blocks whose first new token lies in
-// the window; the others hold query rows, of one token each or, with stages, a run.
+// Prompts and chunks.  CTAs [0, kv_ctas) write keys and values: with `run` = 0 a share
+// of all tokens and every KV head each, else `run` tokens and one group of KV heads.
+// The others hold query rows, of one token each or, with stages, a run of tokens.
 template <int DT, int D, int BS>
-__global__ void __launch_bounds__(kRowThreads, 3)
-rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int window, int stages, int together) {
+__global__ void __launch_bounds__(kRowThreads, 2)
+rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int run, int stages, int together) {
   extern __shared__ __align__(128) uint8_t ring[];
-  using S = BlockShape<D, BS>;
   allow_next_grid();
   wait_prior_grid();
   if ((int)blockIdx.x >= kv_ctas) {
@@ -698,38 +791,14 @@ rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int window, int stages, int
       token_rows<DT, D, false>(a, cta);
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const int parts = (a.H + S::kHeads - 1) / S::kHeads;
-  const int h0 = (int)blockIdx.x % parts * S::kHeads, w0 = (int)blockIdx.x / parts * window;
-  // each warp places the window's tokens, one per lane
-  const int t = w0 + lane;
-  const bool in_window = lane < window && t < a.total_q;
-  int b = find_seq(a.q_start, a.B, w0, lane);
-  for (int base = b;; base += 32) {
-    // the 32 boundaries after `base`: count those at or before each lane's token
-    const int j = base + 1 + lane;
-    const int bound = j <= a.B ? a.q_start[j] : 0x7FFFFFFF;
-    int passed = 0;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) passed += __shfl_sync(kAll, bound, k) <= t ? 1 : 0;
-    const bool more = in_window && passed == 32;
-    if (b == base) b += passed;
-    if (!__any_sync(kAll, more)) break;
-  }
-  Place at = {b, 0, 0};
-  bool bad = false;
-  if (in_window) at = place_of(a, b, t, &bad);
-  int begins = 0, n_here = 0;
-  if (at.ok) {
-    const int row = at.pos % BS;
-    begins = row == 0 || t == a.q_start[b];
-    n_here = min(a.q_start[b + 1] - t, BS - row);   // its sequence's rows in this block
-  }
-  for (uint32_t todo = __ballot_sync(kAll, begins); todo; todo &= todo - 1) {
-    const int src = __ffs(todo) - 1;
-    const int bb = __shfl_sync(kAll, at.b, src), pos = __shfl_sync(kAll, at.pos, src);
-    const int n = __shfl_sync(kAll, n_here, src);
-    store_block<DT, D, BS>(a, bb, pos / BS, h0, w0 + src, pos % BS, pos % BS + n);
+  constexpr int heads = BlockShape<D, BS>::kHeads;
+  const int parts = (a.H + heads - 1) / heads, c = (int)blockIdx.x;
+  if (run) {
+    const int t0 = c / parts * run;
+    store_run<DT, D, BS>(a, t0, min(run, a.total_q - t0), c % parts, 1);
+  } else {
+    const int t0 = (int)((int64_t)a.total_q * c / kv_ctas);
+    store_run<DT, D, BS>(a, t0, (int)((int64_t)a.total_q * (c + 1) / kv_ctas) - t0, 0, parts);
   }
 }
 
@@ -788,7 +857,7 @@ rope_step_q8_kernel(const RopeArgs a, int kv_ctas) {
   widen8<DT>(w[1], y);
   if (a.k_weight) norm<DT, D>(x, y, !is_v, wt[0], wt[1], a.eps);
   if (turns) rotate(x, y, turn, a.interleaved);
-  float m = fmaxf(mag8(x), mag8(y));
+  float m = mag16(x, y);
 #pragma unroll
   for (int o = TG / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
   const float s = fmaxf(old, scale_for(m)), inv = 1.f / s;
@@ -857,24 +926,27 @@ struct Stream {
   int stages, together, bytes, ctas;
 };
 
-pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int most, Stream* s) {
+// `resident` CTAs of an SM at most, `most` of them for this.
+pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int resident, int most,
+                      Stream* s) {
   *s = {0, 1, 0, tokens};
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return PA_ERR_CUDA;
   if (tokens < kStreamTokens * sms) return PA_OK;
-  // `most` CTAs of an SM where two stages of each fit its shared memory, else fewer
+  // where two stages of each fit the SM's shared memory, else fewer
   const int64_t token = (int64_t)rows * head_dim * 2 + rotary * 4;
-  for (int per_sm = most; per_sm; --per_sm) {
-    const int64_t room = (227 * 1024) / per_sm - 5 * 1024;
+  for (int per_sm = resident; per_sm; --per_sm) {
+    const int64_t room = (227 * 1024) / per_sm - 9 * 1024;
     if (2 * token > room) continue;
     while (s->together < kMaxTogether && 3 * 2 * s->together * token <= room) s->together *= 2;
     const int64_t stage = s->together * token;
     s->stages = (int)(room / stage < kMaxStages ? room / stage : kMaxStages);
     s->bytes = (int)(s->stages * stage);
     const int runs = (tokens - 1) / (kRun - 1) + 1;        // of fewer than kRun tokens
-    s->ctas = sms * per_sm > runs ? sms * per_sm : runs;
+    const int ctas = sms * (per_sm < most ? per_sm : most);
+    s->ctas = ctas > runs ? ctas : runs;
     break;
   }
   return PA_OK;
@@ -889,17 +961,22 @@ cudaError_t allow_smem(K* kernel, int bytes) {
 
 template <int DT, int D, int BS>
 cudaError_t launch_blocks(const RopeArgs& a, const Stream& s, cudaStream_t stream) {
-  // a window's blocks are written one after another: about as many tokens as a
-  // sequence has, a block's at most
-  int window = BS < 32 ? BS : 32;
-  while (window > 1 && (int64_t)window * a.B > a.total_q) window /= 2;
-  constexpr int heads = BlockShape<D, BS>::kHeads;
-  const int64_t kv = ((int64_t)a.total_q + window - 1) / window * ((a.H + heads - 1) / heads);
+  // few tokens: short runs, whose blocks are written one after another, of about as many
+  // tokens as a sequence has; many: as many CTAs as for the queries share them (93 us for
+  // 18,432 tokens; 100 with one CTA of each kind on an SM at a time)
+  int run = 0;
+  int64_t kv = s.ctas;
+  if (s.stages == 0) {
+    constexpr int heads = BlockShape<D, BS>::kHeads;
+    run = BS < 32 ? BS : 32;
+    while (run > 1 && (int64_t)run * a.B > a.total_q) run /= 2;
+    kv = ((int64_t)a.total_q + run - 1) / run * ((a.H + heads - 1) / heads);
+  }
   if (kv + s.ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem(rope_append_q8_kernel<DT, D, BS>, s.bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(rope_append_q8_kernel<DT, D, BS>, dim3((unsigned)(kv + s.ctas)), kRowThreads,
-                    s.bytes, stream, a, (int)kv, window, s.stages, s.together);
+                    s.bytes, stream, a, (int)kv, run, s.stages, s.together);
 }
 
 template <int DT, int D>
@@ -912,7 +989,7 @@ cudaError_t launch_q8(const RopeArgs& a, cudaStream_t stream) {
                       stream, a, (int)kv);
   }
   Stream s;
-  if (plan_stream(a.total_q, a.Hq, D, a.rotary, 3, &s) != PA_OK) return cudaErrorUnknown;
+  if (plan_stream(a.total_q, a.Hq, D, a.rotary, 2, 2, &s) != PA_OK) return cudaErrorUnknown;
   switch (a.bs) {
     case 8: return launch_blocks<DT, D, 8>(a, s, stream);
     case 16: return launch_blocks<DT, D, 16>(a, s, stream);
@@ -924,7 +1001,7 @@ cudaError_t launch_q8(const RopeArgs& a, cudaStream_t stream) {
 template <int DT, int D>
 cudaError_t launch_16(const RopeArgs& a, cudaStream_t stream) {
   Stream s;
-  if (plan_stream(a.total_q, a.Hq + 2 * a.H, D, a.rotary, 4, &s) != PA_OK) return cudaErrorUnknown;
+  if (plan_stream(a.total_q, a.Hq + 2 * a.H, D, a.rotary, 4, 4, &s) != PA_OK) return cudaErrorUnknown;
   if (!s.stages)
     return launch_pdl(rope_append_kernel<DT, D>, dim3((unsigned)a.total_q), kRowThreads, 0, stream,
                       a);
