@@ -113,8 +113,8 @@ struct Tail {
   float lred[2][4][GP];          // of a finished segment, per warp: weights' sums
   float mred[2][GP];             // ... and the maxima
   float half[D == 64 ? GP * 64 : 1];   // the other parity's sums (head_dim 64)
-  int sums[kThreads];
-  int start[5];                  // window's first sequence, item, tile; its length; all tiles
+  int sums[kThreads / 32];
+  int start[4];                  // window's first sequence, item, tile; its length
   uint32_t tmem;
   int abort_flag;
 };
@@ -380,37 +380,31 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   int mine = 0;
   for (int b = b0; b < b1; ++b) mine += (clamp_len(a, b) + TOKENS - 1) / TOKENS;
-  tail->sums[tid] = mine;
+  int before = mine;                           // the tiles of earlier threads' sequences
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(kAll, before, o);
+    if (lane >= o) before += up;
+  }
+  if (lane == 31) tail->sums[warp] = before;
+  before -= mine;
   if (tid < 4) tail->start[tid] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) {                            // exclusive scan, seven entries a lane
-    constexpr int E = kThreads / 32;
-    int v[E], sum = 0;
+  int all = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      v[i] = sum;
-      sum += tail->sums[lane * E + i];
-    }
-    int scan = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(kAll, scan, o);
-      if (lane >= o) scan += up;
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) tail->sums[lane * E + i] = scan - sum + v[i];
-    if (lane == 31) tail->start[4] = scan;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    before += w < warp ? tail->sums[w] : 0;
+    all += tail->sums[w];
   }
-  __syncthreads();
-  const int64_t work = (int64_t)tail->start[4] * items;
+  const int64_t work = (int64_t)all * items;
   const int64_t ctas = work < (int64_t)gridDim.x ? work : (int64_t)gridDim.x;
   const bool in = (int64_t)blockIdx.x < ctas;
   const int64_t w0 = in ? work * blockIdx.x / ctas : 0;
   const int64_t w1 = in ? work * (blockIdx.x + 1) / ctas : 0;
   if (in) {
-    const int t = (int)(w0 / items), before = tail->sums[tid];
+    const int t = (int)(w0 / items);
     if (before <= t && t < before + mine) {
       int b = b0, sum = before, nt = 0, len = 0;
       for (;; ++b) {
@@ -436,7 +430,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   walk.L = tail->start[3];
   walk.nt = (walk.L + TOKENS - 1) / TOKENS;
   if (tid == 0)
-    a.info[blockIdx.x] = {walk.b, tail->start[1], walk.j, walk.nt, walk.left, 0, work};
+    a.info[blockIdx.x] = Window{walk.b, tail->start[1], walk.j, walk.nt, walk.left, 0, work};
   const uint32_t tmem = tail->tmem;
   const uint32_t ring = smem_addr(smem), qb = smem_addr(smem + S::kQOff),
                  pb = smem_addr(smem + S::kPOff);
@@ -935,8 +929,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   }
 }
 
-// Joins the partials of items that window boundaries cut: CTA (c, y) looks at the
-// boundary where window c + 1 begins, and joins kJoinHeads heads of its item if that
+// Joins the partials of items that window boundaries cut: CTA c looks at the boundary
+// where window c + 1 begins, and joins its item, of kJoinHeads heads at most, if that
 // boundary is the item's first.  Its time is the chain of loads (window, then all
 // partials), so the partials are asked for before the weights are known: a warp
 // takes a head's maximum and weights, the other threads are elements of a head, the
@@ -945,7 +939,7 @@ constexpr int kJoinThreads = 512;
 constexpr int kJoinAhead = 4;                  // parts of a group asked for at once
 
 template <int D, int kJoinHeads>
-__global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads, 2) join_q8_kernel(const Q8Args a, int grid) {
   constexpr int GROUPS = kJoinThreads / D;
   __shared__ float s_w[kJoinHeads][kMaxGrid];
   __shared__ float s_sum[GROUPS][kJoinHeads][D];
@@ -963,11 +957,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, i
   const int last = (int)min((end * windows - 1) / at.total, windows - 1);
   const int parts = last - c + 2;
   const int h = at.item / a.chunks, G = a.Hq / a.H, g0 = (at.item - h * a.chunks) * a.hch;
-  const int first = (int)blockIdx.y * kJoinHeads;
-  const int n = min(min(a.hch, G - g0) - first, kJoinHeads);
-  if (n <= 0) return;
+  const int n = min(a.hch, G - g0);
   const int64_t head = 2 * (int64_t)(c - 1) + (same ? 0 : 1);
-  auto row = [&](int k) { return (k == 0 ? head : 2 * (int64_t)(c + k - 1)) * a.hch + first; };
+  auto row = [&](int k) { return (k == 0 ? head : 2 * (int64_t)(c + k - 1)) * a.hch; };
   const int d = threadIdx.x % D, group = threadIdx.x / D;
   float x[kJoinAhead][kJoinHeads];
 #pragma unroll
@@ -1018,7 +1010,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_q8_kernel(const Q8Args a, i
     float y = 0.f;
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) y += s_sum[i][g][d];
-    static_cast<uint16_t*>(a.out)[((int64_t)at.b * a.Hq + h * G + g0 + first + g) * D + d] =
+    static_cast<uint16_t*>(a.out)[((int64_t)at.b * a.Hq + h * G + g0 + g) * D + d] =
         a.dtype == PA_BFLOAT16 ? narrow<PA_BFLOAT16>(y) : narrow<PA_FLOAT16>(y);
   }
 }
@@ -1104,6 +1096,14 @@ cudaError_t launch_heads(const CUtensorMap& k, const CUtensorMap& v, const Q8Arg
   if (a.hch <= 4) return launch_decode<D, 4>(k, v, a, grid, device, stream);
   if (a.hch <= 5) return launch_decode<D, 5>(k, v, a, grid, device, stream);
   return launch_decode<D, 8>(k, v, a, grid, device, stream);
+}
+
+// One CTA to a boundary and all of an item's heads: every CTA is resident at once.
+template <int D>
+cudaError_t launch_join(const Q8Args& a, int grid, cudaStream_t stream) {
+  auto join = a.hch <= 2 ? join_q8_kernel<D, 2>
+                         : (a.hch <= 4 ? join_q8_kernel<D, 4> : join_q8_kernel<D, 8>);
+  return launch_pdl(join, dim3((unsigned)(grid - 1)), kJoinThreads, 0, stream, a, grid);
 }
 
 }  // namespace
@@ -1201,14 +1201,8 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   if (work / grid >= (1ll << 31)) return PA_ERR_INVALID_ARG;
   cudaError_t e = head_dim == 128 ? launch_heads<128>(k, v, a, grid, device, stream)
                                   : launch_heads<64>(k, v, a, grid, device, stream);
-  // an item of one tile is never cut; two heads to a joining CTA, four of wider groups
-  // (all joining CTAs are then resident at once)
-  if (e == cudaSuccess && p.tiles > 1 && grid > 1) {
-    const int heads = p.hch <= 4 ? 2 : 4;
-    const dim3 joins((unsigned)(grid - 1), (unsigned)((p.hch + heads - 1) / heads));
-    auto join = head_dim == 128 ? (heads == 2 ? join_q8_kernel<128, 2> : join_q8_kernel<128, 4>)
-                                : (heads == 2 ? join_q8_kernel<64, 2> : join_q8_kernel<64, 4>);
-    e = launch_pdl(join, joins, kJoinThreads, 0, stream, a, grid);
-  }
+  // an item of one tile is never cut
+  if (e == cudaSuccess && p.tiles > 1 && grid > 1)
+    e = head_dim == 128 ? launch_join<128>(a, grid, stream) : launch_join<64>(a, grid, stream);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
