@@ -25,8 +25,8 @@
 // the quarter where token parity and column set agree is used.
 //
 // Work: the tiles of all (sequence, KV head, head chunk) items in a row, cut into
-// equal windows, one per CTA (two CTAs per SM).  An item that a window boundary
-// cuts leaves partial (m, l, acc) in the workspace; the combine kernel joins
+// windows of equal cost, one per CTA (two CTAs per SM); an item costs its tiles and
+// something for its beginning and end.  An item that a window boundary cuts leaves partial (m, l, acc) in the workspace; the combine kernel joins
 // them: M = max m, out = sum acc 2^(m - M) / sum l 2^(m - M).
 //
 // Roles (224 threads): warp 0 block ids and TMA; warp 1 TMEM and MMA issue; warp 2
@@ -56,12 +56,11 @@ constexpr int kMaxGrid = 320;                  // CTAs at most (two per SM)
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
-// Where a CTA's window begins: sequence, item of it, tile; tiles of that item and in
-// the window; tiles of all items.
+// Where a CTA's window begins: sequence, item of it, tile; tiles in the window; where
+// that item's final tile begins; the cost of all items (both in units of cost).
 struct alignas(16) Window {
-  int b, item, j, nt;
-  int tiles, pad;
-  int64_t total;
+  int b, item, j, tiles;
+  int64_t final, total;
 };
 
 struct Q8Args {
@@ -98,6 +97,14 @@ struct Shape {
   static constexpr int kTailOff = kPOff + 2 * kOperand;
 };
 
+// An item's cost is 4 for a tile and this for its beginning and end (sums over the
+// rows, a new q, the output; measured: 0.2-0.5 us with four heads, 1.1 us with eight, of
+// 1.25 us a tile).
+template <int D, int GP>
+constexpr int item_cost() {
+  return GP * (128 / D) <= 2 ? 0 : (GP * (128 / D) <= 4 ? 1 : (GP * (128 / D) <= 5 ? 2 : 4));
+}
+
 template <int D, int GP>
 struct Tail {
   uint64_t full[6], empty[6];
@@ -112,9 +119,10 @@ struct Tail {
   } top[4][2];
   float lred[2][4][GP];          // of a finished segment, per warp: weights' sums
   float mred[2][GP];             // ... and the maxima
-  float half[D == 64 ? GP * 64 : 1];   // the other parity's sums (head_dim 64)
-  int sums[kThreads / 32];
+  float half[2][D == 64 ? GP * 64 : 1];   // head_dim 64: the other parity's sums, by segment
+  int2 sums[kThreads / 32];      // per warp: tiles, sequences that have any
   int start[4];                  // window's first sequence, item, tile; its length
+  int64_t lin[2], final;         // its first tile and the next window's, of all; see Window
   uint32_t tmem;
   int abort_flag;
 };
@@ -375,50 +383,104 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   fence_async_smem();
   wait_prior_grid();
 
-  // this CTA's window of the tiles of all items
+  // this CTA's window: tiles and sequences that have any, up to each thread's first
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (clamp_len(a, b) + TOKENS - 1) / TOKENS;
-  int before = mine;                           // the tiles of earlier threads' sequences
+  int tiles = 0, seqs = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int nt = (clamp_len(a, b) + TOKENS - 1) / TOKENS;
+    tiles += nt;
+    seqs += nt > 0;
+  }
+  int tiles_to = tiles, seqs_to = seqs;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(kAll, before, o);
-    if (lane >= o) before += up;
+    const int t = __shfl_up_sync(kAll, tiles_to, o), n = __shfl_up_sync(kAll, seqs_to, o);
+    if (lane >= o) {
+      tiles_to += t;
+      seqs_to += n;
+    }
   }
-  if (lane == 31) tail->sums[warp] = before;
-  before -= mine;
-  if (tid < 4) tail->start[tid] = 0;
+  if (lane == 31) tail->sums[warp] = make_int2(tiles_to, seqs_to);
+  tiles_to -= tiles;
+  seqs_to -= seqs;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int all = 0;
+  int all_tiles = 0, all_seqs = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    before += w < warp ? tail->sums[w] : 0;
-    all += tail->sums[w];
+    const int2 sum = tail->sums[w];
+    tiles_to += w < warp ? sum.x : 0;
+    seqs_to += w < warp ? sum.y : 0;
+    all_tiles += sum.x;
+    all_seqs += sum.y;
   }
-  const int64_t work = (int64_t)all * items;
+  const int64_t work = (int64_t)all_tiles * items;
   const int64_t ctas = work < (int64_t)gridDim.x ? work : (int64_t)gridDim.x;
   const bool in = (int64_t)blockIdx.x < ctas;
-  const int64_t w0 = in ? work * blockIdx.x / ctas : 0;
-  const int64_t w1 = in ? work * (blockIdx.x + 1) / ctas : 0;
+  // every window holds a tile: the cost of an item's ends counts only where windows are
+  // longer than it
+  int ends_cost = item_cost<D, GP>();
+  int64_t total = (4 * (int64_t)all_tiles + ends_cost * all_seqs) * items;
+  if (total < ctas * 2 * (4 + ends_cost)) {
+    ends_cost = 0;
+    total = 4 * work;
+  }
   if (in) {
-    const int t = (int)(w0 / items);
-    if (before <= t && t < before + mine) {
-      int b = b0, sum = before, nt = 0, len = 0;
+    const int before = 4 * tiles_to + ends_cost * seqs_to;      // of one item of each
+    const int mine = 4 * tiles + ends_cost * seqs;
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+      // 64-bit division takes half a microsecond; most batches fit 32 bits
+      const bool narrow = total < (1 << 22);
+      const int64_t w = narrow ? (int64_t)((uint32_t)total * (blockIdx.x + end) / (uint32_t)ctas)
+                               : total * (blockIdx.x + end) / ctas;
+      const int t = narrow ? (int)((uint32_t)w / (uint32_t)items) : (int)(w / items);
+      if (w == total) {
+        if (tid == 0) tail->lin[end] = work;
+        continue;
+      }
+      if (t < before || t >= before + mine) continue;
+      int b = b0, cost = before, tile = tiles_to, nt = 0, len = 0;
       for (;; ++b) {
         len = clamp_len(a, b);
         nt = (len + TOKENS - 1) / TOKENS;
-        if (t < sum + nt || b + 1 >= b1) break;
-        sum += nt;
+        const int c = nt ? 4 * nt + ends_cost : 0;
+        if (t < cost + c || b + 1 >= b1) break;
+        cost += c;
+        tile += nt;
       }
-      const int at = (int)(w0 - (int64_t)sum * items);
-      tail->start[0] = b;
-      tail->start[1] = at / nt;
-      tail->start[2] = at - at / nt * nt;
-      tail->start[3] = len;
+      // tile 0 of an item begins at 0, tile j at 4 j + ends_cost: the first one from w on
+      const int c = 4 * nt + ends_cost;
+      const int at = (int)(w - (int64_t)cost * items);
+      int item = at / c;
+      const int r = at - item * c;
+      int j = r == 0 ? 0 : max(1, (r - ends_cost + 3) >> 2);
+      tail->lin[end] = (int64_t)tile * items + (int64_t)item * nt + j;
+      if (end == 0) {
+        int64_t base = (int64_t)cost * items + (int64_t)item * c;
+        if (j >= nt) {                          // the next item, maybe of a later sequence
+          j = 0;
+          base += c;
+          if (++item == items) {
+            item = 0;
+            do {
+              len = ++b < a.B ? clamp_len(a, b) : 0;
+              nt = (len + TOKENS - 1) / TOKENS;
+            } while (nt == 0 && b < a.B);
+          }
+        }
+        tail->start[0] = b;
+        tail->start[1] = item;
+        tail->start[2] = j;
+        tail->start[3] = len;
+        tail->final = base + (nt > 1 ? 4 * (nt - 1) + ends_cost : 0);
+      }
     }
+  } else if (tid < 4) {
+    tail->start[tid] = 0;
+    tail->lin[tid & 1] = 0;
   }
   __syncthreads();
   Walk<TOKENS> walk;
@@ -426,11 +488,11 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   walk.h = tail->start[1] / a.chunks;
   walk.chunk = tail->start[1] - walk.h * a.chunks;
   walk.j = tail->start[2];
-  walk.left = (int)(w1 - w0);
+  walk.left = (int)(tail->lin[1] - tail->lin[0]);
   walk.L = tail->start[3];
   walk.nt = (walk.L + TOKENS - 1) / TOKENS;
   if (tid == 0)
-    a.info[blockIdx.x] = Window{walk.b, tail->start[1], walk.j, walk.nt, walk.left, 0, work};
+    a.info[blockIdx.x] = Window{walk.b, tail->start[1], walk.j, walk.left, tail->final, total};
   const uint32_t tmem = tail->tmem;
   const uint32_t ring = smem_addr(smem), qb = smem_addr(smem + S::kQOff),
                  pb = smem_addr(smem + S::kPOff);
@@ -740,9 +802,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     auto finish = [&](int sg, int b, int h, int chunk, bool whole, bool alone) -> bool {
       if (D == 64 && par == 1) {
 #pragma unroll
-        for (int g = 0; g < GP; ++g) tail->half[g * 64 + r - 64] = acc[g];
+        for (int g = 0; g < GP; ++g) tail->half[sg & 1][g * 64 + r - 64] = acc[g];
       }
-      // a tile behind the segment has its red_bar between lred's writes and here
+      // a tile behind the segment has its red_bar between lred's writes and here; half's
+      // two sets: the set of the segment before last has been read by all, at its sum_bar
       if (D == 64 || alone) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&tail->sum_bar);
@@ -767,7 +830,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
           if (g < gn) {
-            const float o = acc[g] + (D == 64 ? tail->half[g * 64 + (r & 63)] : 0.f);
+            const float o = acc[g] + (D == 64 ? tail->half[sg & 1][g * 64 + (r & 63)] : 0.f);
             const float y = o * tail->inv[wq][g];
             if (whole) *to = (uint16_t)(a.dtype == PA_BFLOAT16 ? pack2<PA_BFLOAT16>(y, y)
                                                                  : pack2<PA_FLOAT16>(y, y));
@@ -952,9 +1015,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_q8_kernel(const Q8Args a
   if (same && before.j > 0) return;            // an earlier boundary cuts this item
   // the parts: the segment of window c - 1 that ends there, then the first segments of
   // windows c .. last, last holding the item's final tile
-  const int64_t windows = at.total < grid ? at.total : grid;
-  const int64_t end = at.total * c / windows - at.j + at.nt;
-  const int last = (int)min((end * windows - 1) / at.total, windows - 1);
+  const int64_t windows = at.total / 4 < grid ? at.total / 4 : grid;   // fewer: of a tile each
+  const int last = (int)min(((at.final + 1) * windows - 1) / at.total, windows - 1);
   const int parts = last - c + 2;
   const int h = at.item / a.chunks, G = a.Hq / a.H, g0 = (at.item - h * a.chunks) * a.hch;
   const int n = min(a.hch, G - g0);
@@ -1153,10 +1215,10 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   const Plan p = plan_of(num_q_heads, num_kv_heads, head_dim, max_seq_len);
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.total)
     return PA_ERR_WORKSPACE;
-  // 32-bit tile counts, rows and grid
+  // 32-bit costs of tiles, rows and grid
   const int block_rows = block_size * head_dim / 128;
   const long long rows = (long long)num_blocks * num_kv_heads * block_rows;
-  if (rows >= (1ll << 31) || (long long)num_seqs * p.tiles >= (1ll << 31) ||
+  if (rows >= (1ll << 31) || (long long)num_seqs * p.tiles >= (1ll << 28) ||
       (long long)num_kv_heads * p.chunks >= (1ll << 20) ||
       p.tiles * num_kv_heads * p.chunks >= (1ll << 31))
     return PA_ERR_INVALID_ARG;

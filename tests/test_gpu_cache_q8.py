@@ -172,6 +172,17 @@ def test_decode_many_tiles_per_window(pa, D, G, bs):
             assert not bad.any(), (b, h, int(bad.sum()))
 
 
+@pytest.mark.parametrize("G", [1, 8])
+def test_decode_d64_segments_of_one_tile(pa, G):
+    """head_dim 64: segments of one tile follow one another to the end of every window, and
+    each hands the sums of odd tokens to the threads of even ones."""
+    lens = [1 + (61 * i) % 256 for i in range(500)]
+    b = Batch(lens, G, 3, 64, 16, "bf16", seed=G)
+    outs = [b.run(pa) for _ in range(6)]
+    b.check(outs[0], rows=range(0, 500, 3))
+    assert all(torch.equal(o.view(torch.int16), outs[0].view(torch.int16)) for o in outs)
+
+
 def test_decode_any_positive_scale(pa):
     b = Batch([300, 77], 4, 2, 128, 16, "bf16", seed=5, po2=False)
     b.check(b.run(pa))
