@@ -427,7 +427,26 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     ends_cost = 0;
     total = 4 * work;
   }
-  if (in) {
+  if (in && ctas == work) {                     // a tile each: the shortest way, latency counts
+    const int w = (int)blockIdx.x, t = w / items;
+    if (tiles_to <= t && t < tiles_to + tiles) {
+      int b = b0, tile = tiles_to, len = 0, nt = 0;
+      for (;; ++b) {
+        len = clamp_len(a, b);
+        nt = (len + TOKENS - 1) / TOKENS;
+        if (t < tile + nt) break;
+        tile += nt;
+      }
+      const int at = w - tile * items, item = at / nt;
+      tail->start[0] = b;
+      tail->start[1] = item;
+      tail->start[2] = at - item * nt;
+      tail->start[3] = len;
+      tail->lin[0] = w;
+      tail->lin[1] = w + 1;
+      tail->final = 4 * (int64_t)(tile * items + item * nt + nt - 1);
+    }
+  } else if (in) {
     const int before = 4 * tiles_to + ends_cost * seqs_to;      // of one item of each
     const int mine = 4 * tiles + ends_cost * seqs;
 #pragma unroll 1
