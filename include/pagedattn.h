@@ -448,7 +448,7 @@ pa_status pa_rope_append(void* q_out, void* k_pool, void* v_pool, const void* q,
  * block_size, head_dim] (one head's rows of a block are contiguous), k_scale /
  * v_scale [num_blocks, num_kv_heads] fp32; a stored value is code * scale.  The
  * writer's scales are powers of two: s(a) is the smallest 2^e, e >= -64, with
- * a <= 448 * 2^e.  Readers take any positive finite scale.  Copy-on-write and
+ * a <= 448 * 2^e.  Readers take any finite scale of 2^-100 or more.  Copy-on-write and
  * swaps of such blocks are pa_copy_blocks_multi / pa_swap_blocks (they move
  * bytes; the scale rows are one more pool when num_kv_heads is a multiple of 4).
  *

@@ -67,6 +67,7 @@ struct Args {
     for (int i = 0; i < count; ++i) {
       need(!(dense >> i & 1) || seen[i]->is_contiguous(), "tensors must be contiguous");
       need(seen[i]->is_cuda(), "every tensor must be on the current CUDA device");
+      for (const int64_t n : seen[i]->sizes()) need(n <= 0x7FFFFFFF, "a size does not fit 32 bits");
     }
     const int device = c10::cuda::current_device();
     for (int i = 0; i < count; ++i)
@@ -101,7 +102,9 @@ T* ptr_as(const Tensor* t) { return static_cast<T*>(ptr(t)); }
 int64_t token_stride(const Args& a, const Tensor& t) {
   a.need(t.stride(2) == 1 && (t.size(1) == 1 || t.stride(1) == t.size(2)),
          "the heads of a token must be packed");
-  return t.size(0) > 1 ? t.stride(0) : 0;
+  if (t.size(0) <= 1) return 0;
+  a.need(t.stride(0) > 0, "tokens that share one row (a stride of 0) are no token rows");
+  return t.stride(0);
 }
 
 void check_q8(const Args& a, const Tensor& k, const Tensor& v, const Tensor& ks, const Tensor& vs) {
@@ -137,6 +140,7 @@ long rope(Args a, bool q8) {
   const Tensor* kw = a.packed(i++, true);
   const double eps = a.number(i++);
   const int interleaved = PyObject_IsTrue(a.v[i++]);
+  if (interleaved < 0) throw Bad("");
   const Tensor* pos = a.index(i++, true);
   const Tensor* status = a.status(i++);
   a.need(q.dim() == 3 && k.dim() == 3 && v.dim() == 3 && tables.dim() == 2,

@@ -80,11 +80,11 @@ __device__ __forceinline__ Place place_of(const RopeArgs& a, int b, int t, bool*
   if (a.q_start) {
     s = a.q_start[b];
     const int e = a.q_start[b + 1];
-    n = e - s;
-    if (t < s || t >= e || e > a.total_q) {
+    if (s < 0 || t < s || t >= e || e > a.total_q) {
       *bad = true;
       return p;
     }
+    n = e - s;
   } else if (L == 0) {
     return p;                        // an empty sequence of a decode step
   }
@@ -317,7 +317,7 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
 // copies, so that no computing warp waits for one to be read out.  Reads of later
 // tokens and writes of earlier ones are in flight all the time, which the register
 // kernel above cannot hold at the occupancy that a row's registers leave it.
-constexpr int kMaxStages = 3;                  // a fourth costs 10%: 222 KB of an SM's 228 for four CTAs
+constexpr int kMaxStages = 3;                  // a fourth costs 10%
 constexpr int kComputeWarps = kRowThreads / 32 - 1;
 constexpr int kRun = kRowThreads;              // tokens of a CTA at most: one thread places one
 constexpr int kStreamTokens = 8;               // tokens per SM from which on it is taken
@@ -952,10 +952,11 @@ pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int reside
   return PA_OK;
 }
 
-// Shared memory above 48 KB, static included, has to be asked for.
+// Shared memory above 48 KB, static included (under 9 KB in each kernel), has to be
+// asked for.
 template <typename K>
 cudaError_t allow_smem(K* kernel, int bytes) {
-  if (bytes <= 44 * 1024) return cudaSuccess;
+  if (bytes <= 39 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 

@@ -140,6 +140,10 @@ CASES = [
      dict(interleaved=True, behind=5, positions=True)),
     ([2500], [2400], 96, 1, 128, 64, "fp16", 64, dict(norm="q")),
     ([2500], [2400], 1, 1, 64, 32, "bf16", 0, dict(norm="k")),
+    # a ring whose stages take just under 48 KB
+    ([2500], [2400], 14, 2, 64, 16, "bf16", 16, dict(norm="qk")),
+    ([1 + (7 * i) % 40 for i in range(1300)], [min(1 + (7 * i) % 40, 1 + i % 2) for i in range(1300)],
+     2, 2, 128, 16, "bf16", 128, dict(norm="k")),
 ]
 
 
@@ -310,6 +314,26 @@ def test_zeros_have_the_smallest_scale(pa):
     blk = int(s.tables[0, 0])
     assert (sc[1][blk] == 2.0 ** -64).all()
     assert not (codes[1][blk, :, :3] & 0x7F).any() and (codes[1][blk, :, 3:] == 7).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("many", [False, True])
+def test_bad_row_ranges_are_reported_and_skipped(pa, q8, many):
+    """q_start that is negative, falls, or ends past the rows: none of it is followed."""
+    n = 1500 if many else 40
+    s = Setup([n, 30, 30], [n, 20, 20], 2, 2, 64, 16, "bf16", 64)
+    pools = [torch.zeros(s.NB, 2, 16, 64, dtype=torch.uint8, device="cuda") if q8 else
+             torch.zeros(s.NB, 16, 2, 64, dtype=s.dt, device="cuda") for _ in "kv"]
+    rest = [torch.ones(s.NB, 2, device="cuda") for _ in "kv"] if q8 else []
+    f = pa.pa_rope_append_q8 if q8 else pa.pa_rope_append
+    for start in ([-(1 << 31), n, n + 20, n + 40], [0, n, n - 1, n + 40], [0, n, n + 20, n + 41],
+                  [0, n, n + 20, (1 << 31) - 1], [5, n, n + 20, n + 40]):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kw = s.kw_args() | dict(q_start=i32(start))
+        f(s.q_out, *pools, *rest, s.q, s.k, s.v, s.cs, i32(s.tables), i32(s.lens), status=status,
+          **kw)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 5, start
 
 
 @pytest.mark.parametrize("q8", [False, True])

@@ -123,6 +123,12 @@ def test_binding_refuses_what_the_library_cannot_see(lib):
     with pytest.raises(ValueError, match="device"):                # CPU tensors
         pa.pa_rope_append(q, torch.zeros(6, 16, 2, 64), torch.zeros(6, 16, 2, 64), q, k, k, None,
                           t, n)
+    pools = torch.zeros(6, 16, 2, 64), torch.zeros(6, 16, 2, 64)
+    for qkv in ((q[:1].expand(2, 4, 64), k, k), (q, *[k[:1].expand(2, 2, 64)] * 2)):
+        with pytest.raises(ValueError, match="stride of 0"):       # one row for all tokens
+            pa.pa_rope_append(q, *pools, *qkv, None, t, n)
+    with pytest.raises(ValueError, match="packed"):
+        pa.pa_rope_append(q, *pools, q[:, :1].expand(2, 4, 64), k, k, None, t, n)
     with pytest.raises(ValueError, match="device"):
         pa.pa_decode_q8(q, q, pool8, pool8, sc, sc, t, n, 0.1)
     with pytest.raises(ValueError, match="8-bit pools"):
