@@ -31,13 +31,15 @@ struct ExpandArgs {
 
 template <int DT>
 __device__ __forceinline__ uint32_t expand2(uint32_t codes, float scale) {
-  const float most = DT == PA_FLOAT16 ? 65504.f : 3.3895313892515355e38f;
   const float2 c = e4m3_widen2(codes);
-  float a = c.x * scale, b = c.y * scale;
+  const float a = c.x * scale, b = c.y * scale;
   // past the type's largest value (the code above a magnitude near it): saturate; NaN stays
-  a = a > most ? most : (a < -most ? -most : a);
-  b = b > most ? most : (b < -most ? -most : b);
-  return pack2<DT>(a, b);
+  uint32_t d;
+  if (DT == PA_FLOAT16)
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
 }
 
 template <int DT, int D>
