@@ -333,6 +333,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// 16 bytes to shared memory, behind the thread's back.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_addr(dst)), "l"(src)
+               : "memory");
+}
+
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
                "r"(sm100::smem_addr(src)), "r"(bytes)
@@ -607,6 +613,14 @@ struct BlockShape {
   static constexpr int NG = kHead / TG, RPT = BS / NG;    // groups, rows of each
 };
 
+constexpr int kKvStages = 3;                   // items of a CTA in flight
+
+// Shared memory of the items in flight: every thread's elements, 64 bytes of a row.
+template <int D, int BS>
+constexpr int kv_bytes() {
+  return kKvStages * BlockShape<D, BS>::RPT * 4 * kRowThreads * 16;
+}
+
 // A block with new rows: [r0, r0 + n), tokens t ..; older rows are below r0.
 struct NewRows {
   int t, pos, n, blk;          // first token, its position, rows, physical block
@@ -615,10 +629,12 @@ struct NewRows {
 // Keys and values of tokens [t0, t0 + n) (kRowThreads at most) to the 8-bit cache: the
 // blocks whose first new token is among them, for `parts` groups of KV heads from
 // `part` on.  A block and a group of heads is one item: its largest magnitudes are
-// taken over the CTA, then its codes are made.  The next item's rows are asked for
-// before an item is worked on.
+// taken over the CTA, then its codes are made.  The rows of the items behind it are on
+// their way to shared memory meanwhile, each thread's elements to a place of its own; a
+// block's angles are read once for all its heads.
 template <int DT, int D, int BS>
-__device__ __forceinline__ void store_run(const RopeArgs& a, int t0, int n, int part, int parts) {
+__device__ __forceinline__ void store_run(const RopeArgs& a, int t0, int n, int part, int parts,
+                                          uint8_t* smem) {
   using S = BlockShape<D, BS>;
   constexpr int TG = S::TG, NG = S::NG, RPT = S::RPT, NW = S::kHead / 32, RV = D / 8;
   constexpr int WARPS = kRowThreads / 32;
@@ -667,26 +683,33 @@ __device__ __forceinline__ void store_run(const RopeArgs& a, int t0, int n, int 
     wt[1] = reinterpret_cast<const uint4*>(a.k_weight)[el.v1];
   }
   const int items = blocks * parts;
-  uint4 kn[RPT][2], vn[RPT][2];                // the next item's rows
+  auto place = [&](int item, int i) {          // 16 bytes of this thread
+    return reinterpret_cast<uint4*>(smem) + (item % kKvStages * (RPT * 4) + i) * kRowThreads + tid;
+  };
   auto ask = [&](int item) {
-    const NewRows at = s_list[item / parts];
-    const int h = (part + item % parts) * S::kHeads + mine, r0 = at.pos % BS;
+    if (item < items) {
+      const NewRows at = s_list[item / parts];
+      const int h = (part + item % parts) * S::kHeads + mine, r0 = at.pos % BS;
 #pragma unroll
-    for (int u = 0; u < RPT; ++u) {
-      const int row = grp + u * NG;
-      kn[u][0] = kn[u][1] = vn[u][0] = vn[u][1] = make_uint4(0, 0, 0, 0);
-      if (h < a.H && row >= r0 && row < r0 + at.n) {
-        const int64_t from = (at.t + row - r0) * (a.kv_stride / 8) + h * RV;
-        const uint4* k = reinterpret_cast<const uint4*>(a.key) + from;
-        const uint4* v = reinterpret_cast<const uint4*>(a.value) + from;
-        kn[u][0] = k[el.v0];
-        kn[u][1] = k[el.v1];
-        vn[u][0] = v[el.v0];
-        vn[u][1] = v[el.v1];
+      for (int u = 0; u < RPT; ++u) {
+        const int row = grp + u * NG;
+        if (h < a.H && row >= r0 && row < r0 + at.n) {
+          const int64_t from = (at.t + row - r0) * (a.kv_stride / 8) + h * RV;
+          const uint4* k = reinterpret_cast<const uint4*>(a.key) + from;
+          const uint4* v = reinterpret_cast<const uint4*>(a.value) + from;
+          copy16(place(item, 4 * u), k + el.v0);
+          copy16(place(item, 4 * u + 1), k + el.v1);
+          copy16(place(item, 4 * u + 2), v + el.v0);
+          copy16(place(item, 4 * u + 3), v + el.v1);
+        }
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (items > 0) ask(0);
+#pragma unroll
+  for (int i = 0; i < kKvStages - 1; ++i) ask(i);
+  bool fresh[RPT];                             // a new row whose position is in range
+  Turn turn[RPT];
   for (int item = 0; item < items; ++item) {
     const NewRows at = s_list[item / parts];
     const int h = (part + item % parts) * S::kHeads + mine, r0 = at.pos % BS;
@@ -699,33 +722,40 @@ __device__ __forceinline__ void store_run(const RopeArgs& a, int t0, int n, int 
       k_old = a.k_scale[tile];
       v_old = a.v_scale[tile];
     }
+    if (item % parts == 0) {                   // a new block
+#pragma unroll
+      for (int u = 0; u < RPT; ++u) {
+        const int row = grp + u * NG;
+        fresh[u] = row >= r0 && row < r0 + at.n;
+        if (fresh[u]) {
+          const float* angles = angles_of(a, at.t + row - r0, at.pos - r0 + row, &fresh[u]);
+          if (!fresh[u] && li == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+          if (el.turns && angles) turn[u] = load_turn(angles, a.rotary, li);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kKvStages - 2) : "memory");
     float kx[RPT][8], ky[RPT][8];
     uint4 vw[RPT][2];
     bool live[RPT], any = false;
     float km = 0.f, vm = 0.f;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
-      const int row = grp + u * NG;
-      vw[u][0] = vn[u][0];
-      vw[u][1] = vn[u][1];
-      widen8<DT>(kn[u][0], kx[u]);
-      widen8<DT>(kn[u][1], ky[u]);
-      live[u] = in && row >= r0 && row < r0 + at.n;
-      const float* angles = nullptr;
-      if (live[u]) {
-        angles = angles_of(a, at.t + row - r0, at.pos - r0 + row, &live[u]);
-        if (!live[u] && li == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
-      }
+      // a row that is not live holds anything, and nobody else's values depend on it
+      widen8<DT>(*place(item, 4 * u), kx[u]);
+      widen8<DT>(*place(item, 4 * u + 1), ky[u]);
+      vw[u][0] = *place(item, 4 * u + 2);
+      vw[u][1] = *place(item, 4 * u + 3);
+      live[u] = in && fresh[u];
       any |= live[u];
       if (a.k_weight) norm<DT, D>(kx[u], ky[u], true, wt[0], wt[1], a.eps);
-      if (el.turns && angles)
-        rotate(kx[u], ky[u], load_turn(angles, a.rotary, li), a.interleaved);
       if (live[u]) {
+        if (el.turns) rotate(kx[u], ky[u], turn[u], a.interleaved);
         km = fmaxf(km, mag16(kx[u], ky[u]));
         vm = fmaxf(vm, mag16<DT>(vw[u][0], vw[u][1]));
       }
     }
-    if (item + 1 < items) ask(item + 1);
+    ask(item + kKvStages - 1);                 // to the place that the item before held
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       km = fmaxf(km, __shfl_xor_sync(kAll, km, o));
@@ -795,10 +825,11 @@ rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int run, int stages, int to
   const int parts = (a.H + heads - 1) / heads, c = (int)blockIdx.x;
   if (run) {
     const int t0 = c / parts * run;
-    store_run<DT, D, BS>(a, t0, min(run, a.total_q - t0), c % parts, 1);
+    store_run<DT, D, BS>(a, t0, min(run, a.total_q - t0), c % parts, 1, ring);
   } else {
     const int t0 = (int)((int64_t)a.total_q * c / kv_ctas);
-    store_run<DT, D, BS>(a, t0, (int)((int64_t)a.total_q * (c + 1) / kv_ctas) - t0, 0, parts);
+    store_run<DT, D, BS>(a, t0, (int)((int64_t)a.total_q * (c + 1) / kv_ctas) - t0, 0, parts,
+                          ring);
   }
 }
 
@@ -974,10 +1005,11 @@ cudaError_t launch_blocks(const RopeArgs& a, const Stream& s, cudaStream_t strea
     kv = ((int64_t)a.total_q + run - 1) / run * ((a.H + heads - 1) / heads);
   }
   if (kv + s.ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem(rope_append_q8_kernel<DT, D, BS>, s.bytes);
+  const int bytes = s.bytes > kv_bytes<D, BS>() ? s.bytes : kv_bytes<D, BS>();
+  const cudaError_t e = allow_smem(rope_append_q8_kernel<DT, D, BS>, bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(rope_append_q8_kernel<DT, D, BS>, dim3((unsigned)(kv + s.ctas)), kRowThreads,
-                    s.bytes, stream, a, (int)kv, run, s.stages, s.together);
+                    bytes, stream, a, (int)kv, run, s.stages, s.together);
 }
 
 template <int DT, int D>
