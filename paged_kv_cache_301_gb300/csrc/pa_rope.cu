@@ -804,12 +804,13 @@ __device__ __forceinline__ void store_run(const RopeArgs& a, int t0, int n, int 
   }
 }
 
-// Prompts and chunks.  CTAs [0, kv_ctas) write keys and values: with `run` = 0 a share
-// of all tokens and every KV head each, else `run` tokens and one group of KV heads.
-// The others hold query rows, of one token each or, with stages, a run of tokens.
+// Prompts and chunks.  CTAs [0, kv_ctas) write keys and values: `groups` of them share a
+// run of `run` tokens (0: all tokens are shared out evenly), some heads each.  The others
+// hold query rows, of one token each or, with stages, a run of tokens.
 template <int DT, int D, int BS>
 __global__ void __launch_bounds__(kRowThreads, 2)
-rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int run, int stages, int together) {
+rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int groups, int run, int stages,
+                      int together) {
   extern __shared__ __align__(128) uint8_t ring[];
   allow_next_grid();
   wait_prior_grid();
@@ -822,15 +823,12 @@ rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int run, int stages, int to
     return;
   }
   constexpr int heads = BlockShape<D, BS>::kHeads;
-  const int parts = (a.H + heads - 1) / heads, c = (int)blockIdx.x;
-  if (run) {
-    const int t0 = c / parts * run;
-    store_run<DT, D, BS>(a, t0, min(run, a.total_q - t0), c % parts, 1, ring);
-  } else {
-    const int t0 = (int)((int64_t)a.total_q * c / kv_ctas);
-    store_run<DT, D, BS>(a, t0, (int)((int64_t)a.total_q * (c + 1) / kv_ctas) - t0, 0, parts,
-                          ring);
-  }
+  const int parts = (a.H + heads - 1) / heads, per = (parts + groups - 1) / groups;
+  const int c = (int)blockIdx.x / groups, runs = kv_ctas / groups;
+  const int part = ((int)blockIdx.x - c * groups) * per;
+  const int t0 = run ? c * run : (int)((int64_t)a.total_q * c / runs);
+  const int t1 = run ? min(t0 + run, a.total_q) : (int)((int64_t)a.total_q * (c + 1) / runs);
+  store_run<DT, D, BS>(a, t0, t1 - t0, part, min(per, parts - part), ring);
 }
 
 // A decode step: one new token per sequence.  CTAs [0, kv_ctas): each group of
@@ -994,22 +992,33 @@ cudaError_t allow_smem(K* kernel, int bytes) {
 template <int DT, int D, int BS>
 cudaError_t launch_blocks(const RopeArgs& a, const Stream& s, cudaStream_t stream) {
   // few tokens: short runs, whose blocks are written one after another, of about as many
-  // tokens as a sequence has; many: as many CTAs as for the queries share them (93 us for
-  // 18,432 tokens; 100 with one CTA of each kind on an SM at a time)
-  int run = 0;
-  int64_t kv = s.ctas;
+  // tokens as a sequence has; many: as many CTAs as for the queries share them (82 us for
+  // 18,432 tokens; 100 with one CTA of each kind on an SM at a time), of about four blocks
+  // each or, where tokens are few, some of the heads of four (8,000 tokens, blocks of 32:
+  // 46.6 us; 51 with all heads of 0 to 2 blocks)
+  constexpr int heads = BlockShape<D, BS>::kHeads;
+  const int parts = (a.H + heads - 1) / heads;
+  int run = 0, groups = parts;
+  int64_t runs;
   if (s.stages == 0) {
-    constexpr int heads = BlockShape<D, BS>::kHeads;
     run = BS < 32 ? BS : 32;
     while (run > 1 && (int64_t)run * a.B > a.total_q) run /= 2;
-    kv = ((int64_t)a.total_q + run - 1) / run * ((a.H + heads - 1) / heads);
+    runs = ((int64_t)a.total_q + run - 1) / run;
+  } else {
+    const int least = (a.total_q - 1) / (kRun - 1) + 1;    // of fewer than kRun tokens
+    const int64_t wish = (int64_t)4 * BS * s.ctas / a.total_q;
+    const int most = (int)(wish < 1 ? 1 : (wish < parts ? wish : parts));
+    const int per = (parts + most - 1) / most;
+    groups = (parts + per - 1) / per;
+    runs = s.ctas / groups > least ? s.ctas / groups : least;
   }
+  const int64_t kv = runs * groups;
   if (kv + s.ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const int bytes = s.bytes > kv_bytes<D, BS>() ? s.bytes : kv_bytes<D, BS>();
   const cudaError_t e = allow_smem(rope_append_q8_kernel<DT, D, BS>, bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(rope_append_q8_kernel<DT, D, BS>, dim3((unsigned)(kv + s.ctas)), kRowThreads,
-                    bytes, stream, a, (int)kv, run, s.stages, s.together);
+                    bytes, stream, a, (int)kv, groups, run, s.stages, s.together);
 }
 
 template <int DT, int D>
