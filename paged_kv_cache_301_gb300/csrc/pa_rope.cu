@@ -281,7 +281,7 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 + u * NG + grp;
-      if (r0 + u * NG >= rows) break;
+      if (r - lane / TG >= rows) break;        // the warp's first row
       const bool is_q = r < a.Hq, is_k = KV16 && !is_q && r < a.Hq + a.H;
       float x[8], y[8];
       widen8<DT>(w[u][0], x);
@@ -501,9 +501,9 @@ __device__ __forceinline__ void stream_rows(const RopeArgs& a, int cta, int ctas
       break;
     }
     uint8_t* stage = stage_of(step);
-    // (token, row) pairs in turn; whole warps stay in the loop for the shuffles
+    // (token, row) pairs in turn; a warp stays in the loop while any of it has a pair
     int i = 0, r = grp;
-    for (int k = 0; k < many * turned; k += NG, r += NG) {
+    for (int k = warp * (32 / TG); k < many * turned; k += NG, r += NG) {
       while (r >= turned && i < many) {
         r -= turned;
         ++i;
