@@ -153,12 +153,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// RMS norm of a head row over its D/16 lanes.  Called by whole warps (it shuffles);
-// `on`: the group's row is normed, by w0 and w1, the weight's vectors v0 and v1.
-// Two-wide fp32 arithmetic: these kernels issue nearly as much as they move.
-template <int DT, int D>
-__device__ __forceinline__ void norm(float (&a)[8], float (&b)[8], bool on, uint4 w0,
-                                     uint4 w1, float eps) {
+// 1 / the root mean square of a head row, over its D/16 lanes.  Called by whole warps
+// (it shuffles).  Two-wide fp32 arithmetic: these kernels issue nearly as much as they
+// move.
+template <int D>
+__device__ __forceinline__ float inv_rms(const float (&a)[8], const float (&b)[8], float eps) {
   using namespace sm100;
   uint64_t sum = 0;                            // two zeros
 #pragma unroll
@@ -171,18 +170,30 @@ __device__ __forceinline__ void norm(float (&a)[8], float (&b)[8], bool on, uint
   float ss = s0 + s1;
 #pragma unroll
   for (int o = D / 32; o; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
+  return rsqrtf(ss * (1.f / D) + eps);
+}
+
+// x <- x r w
+__device__ __forceinline__ void scale8(float (&x)[8], float r, const float (&w)[8]) {
+  using namespace sm100;
+  const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    f2_unpack(mul2(mul2(f2_pack(x[i], x[i + 1]), r2), f2_pack(w[i], w[i + 1])), x[i], x[i + 1]);
+}
+
+// RMS norm of a head row by w0 and w1, the weight's vectors v0 and v1; `on`: the
+// group's row is normed.  Called by whole warps.
+template <int DT, int D>
+__device__ __forceinline__ void norm(float (&a)[8], float (&b)[8], bool on, uint4 w0,
+                                     uint4 w1, float eps) {
+  const float r = inv_rms<D>(a, b, eps);
   if (on) {
-    const float r = rsqrtf(ss * (1.f / D) + eps);
-    const uint64_t r2 = f2_pack(r, r);
     float w[8];
     widen8<DT>(w0, w);
-#pragma unroll
-    for (int i = 0; i < 8; i += 2)
-      f2_unpack(mul2(mul2(f2_pack(a[i], a[i + 1]), r2), f2_pack(w[i], w[i + 1])), a[i], a[i + 1]);
+    scale8(a, r, w);
     widen8<DT>(w1, w);
-#pragma unroll
-    for (int i = 0; i < 8; i += 2)
-      f2_unpack(mul2(mul2(f2_pack(b[i], b[i + 1]), r2), f2_pack(w[i], w[i + 1])), b[i], b[i + 1]);
+    scale8(b, r, w);
   }
 }
 
@@ -317,10 +328,12 @@ __device__ __forceinline__ void token_rows(const RopeArgs& a, int t) {
 // copies, so that no computing warp waits for one to be read out.  Reads of later
 // tokens and writes of earlier ones are in flight all the time, which the register
 // kernel above cannot hold at the occupancy that a row's registers leave it.
-constexpr int kMaxStages = 3;                  // a fourth costs 10%
+constexpr int kMaxStages = 3;                  // 18,432 tokens: 75 us; two 101, four 85
 constexpr int kComputeWarps = kRowThreads / 32 - 1;
 constexpr int kRun = kRowThreads;              // tokens of a CTA at most: one thread places one
-constexpr int kStreamTokens = 8;               // tokens per SM from which on it is taken
+// Tokens per SM from which on it is taken (8 per SM: 10.3 us either way; 4 per SM: 6.2 us
+// with the register kernel, 6.9 so; 120 per SM: 102 us and 75).
+constexpr int kStreamTokens = 8;
 constexpr int kMaxTogether = 8;                // tokens of a stage at most
 constexpr uint64_t kStreamLimitNs = 2000000000ull;
 
@@ -369,6 +382,7 @@ __device__ __forceinline__ void stream_rows(const RopeArgs& a, int cta, int ctas
   __shared__ __align__(8) uint64_t full[kMaxStages], done[kMaxStages];
   __shared__ int64_t s_slot[kRun];             // pool row of the token (-1: none)
   __shared__ int s_pos[kRun];                  // row of cos_sin (-1: leave the token alone)
+  __shared__ float4 s_weight[2][4][TG];        // of q and k, widened, by lane of a row
   __shared__ int s_abort;
   volatile int* abort_flag = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -426,14 +440,17 @@ __device__ __forceinline__ void stream_rows(const RopeArgs& a, int cta, int ctas
   int fetched = min(stages, steps);
   if (copies)
     for (int i = 0; i < fetched; ++i) fetch_rows(i);
-  uint4 qw[2] = {}, kw[2] = {};
-  if (a.q_weight) {
-    qw[0] = reinterpret_cast<const uint4*>(a.q_weight)[part.v0];
-    qw[1] = reinterpret_cast<const uint4*>(a.q_weight)[part.v1];
-  }
-  if (KV16 && a.k_weight) {
-    kw[0] = reinterpret_cast<const uint4*>(a.k_weight)[part.v0];
-    kw[1] = reinterpret_cast<const uint4*>(a.k_weight)[part.v1];
+  if (tid < 2 * TG) {
+    const uint4* from = reinterpret_cast<const uint4*>(tid < TG ? a.q_weight : a.k_weight);
+    if (from && (KV16 || tid < TG)) {
+      float w[8];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        widen8<DT>(from[half ? part.v1 : part.v0], w);
+        s_weight[tid / TG][2 * half][li] = make_float4(w[0], w[1], w[2], w[3]);
+        s_weight[tid / TG][2 * half + 1][li] = make_float4(w[4], w[5], w[6], w[7]);
+      }
+    }
   }
   if (tid < n) {                               // every thread places a token of the run
     bool bad;
@@ -508,16 +525,23 @@ __device__ __forceinline__ void stream_rows(const RopeArgs& a, int cta, int ctas
         r -= turned;
         ++i;
       }
-      const bool live = i < many && s_pos[first + min(i, many - 1)] >= 0;
+      const int at = min(i, many - 1);         // behind the last pair: any row, not stored
+      const bool live = i < many && s_pos[first + at] >= 0;
       const bool is_q = r < a.Hq;
-      uint8_t* token = stage + (uint32_t)i * token_bytes;
-      uint4* row = reinterpret_cast<uint4*>(token) + r * RV;
+      uint8_t* token = stage + (uint32_t)at * token_bytes;
+      uint4* row = reinterpret_cast<uint4*>(token) + min(r, turned - 1) * RV;
       float x[8], y[8];
-      widen8<DT>(live ? row[part.v0] : make_uint4(0, 0, 0, 0), x);
-      widen8<DT>(live ? row[part.v1] : make_uint4(0, 0, 0, 0), y);
-      if (any_norm)
-        norm<DT, D>(x, y, is_q ? a.q_weight != nullptr : KV16 && a.k_weight != nullptr,
-                    pick(is_q, qw[0], kw[0]), pick(is_q, qw[1], kw[1]), a.eps);
+      widen8<DT>(row[part.v0], x);
+      widen8<DT>(row[part.v1], y);
+      if (any_norm) {
+        const float r_rms = inv_rms<D>(x, y, a.eps);
+        if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+          const float4 w0 = s_weight[!is_q][0][li], w1 = s_weight[!is_q][1][li],
+                       w2 = s_weight[!is_q][2][li], w3 = s_weight[!is_q][3][li];
+          scale8(x, r_rms, {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w});
+          scale8(y, r_rms, {w2.x, w2.y, w2.z, w2.w, w3.x, w3.y, w3.z, w3.w});
+        }
+      }
       if (!live) continue;
       if (part.turns)
         rotate(x, y, load_turn(reinterpret_cast<const float*>(token + row_bytes), a.rotary, li),
@@ -955,8 +979,8 @@ struct Stream {
   int stages, together, bytes, ctas;
 };
 
-// `resident` CTAs of an SM at most, `most` of them for this.
-pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int resident, int most,
+// `resident` CTAs of an SM at most.
+pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int resident,
                       Stream* s) {
   *s = {0, 1, 0, tokens};
   int device = 0, sms = 0;
@@ -974,7 +998,7 @@ pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int reside
     s->stages = (int)(room / stage < kMaxStages ? room / stage : kMaxStages);
     s->bytes = (int)(s->stages * stage);
     const int runs = (tokens - 1) / (kRun - 1) + 1;        // of fewer than kRun tokens
-    const int ctas = sms * (per_sm < most ? per_sm : most);
+    const int ctas = sms * per_sm;
     s->ctas = ctas > runs ? ctas : runs;
     break;
   }
@@ -1031,7 +1055,7 @@ cudaError_t launch_q8(const RopeArgs& a, cudaStream_t stream) {
                       stream, a, (int)kv);
   }
   Stream s;
-  if (plan_stream(a.total_q, a.Hq, D, a.rotary, 2, 2, &s) != PA_OK) return cudaErrorUnknown;
+  if (plan_stream(a.total_q, a.Hq, D, a.rotary, 2, &s) != PA_OK) return cudaErrorUnknown;
   switch (a.bs) {
     case 8: return launch_blocks<DT, D, 8>(a, s, stream);
     case 16: return launch_blocks<DT, D, 16>(a, s, stream);
@@ -1042,8 +1066,13 @@ cudaError_t launch_q8(const RopeArgs& a, cudaStream_t stream) {
 
 template <int DT, int D>
 cudaError_t launch_16(const RopeArgs& a, cudaStream_t stream) {
+  // Tokens of 12 KB and more: two CTAs of an SM with two tokens to a stage, whose rows keep
+  // a CTA's warps busy (48 rows of 128, 18,432 tokens: 75 us, four CTAs 81; 96 rows: 147,
+  // four 176).  Smaller ones: four CTAs (48 rows of 64: 41 us, two 44; 12 rows: 27, two 35)
+  const int rows = a.Hq + 2 * a.H, per_sm = rows * D * 2 + a.rotary * 4 >= 12 * 1024 ? 2 : 4;
   Stream s;
-  if (plan_stream(a.total_q, a.Hq + 2 * a.H, D, a.rotary, 4, 4, &s) != PA_OK) return cudaErrorUnknown;
+  if (plan_stream(a.total_q, rows, D, a.rotary, per_sm, &s) != PA_OK)
+    return cudaErrorUnknown;
   if (!s.stages)
     return launch_pdl(rope_append_kernel<DT, D>, dim3((unsigned)a.total_q), kRowThreads, 0, stream,
                       a);
