@@ -2,8 +2,8 @@
 //
 // A decode step makes these calls once per layer with about fifteen tensors each.
 // Reading shapes, strides, types, devices and addresses from Python and handing
-// thirty numbers to ctypes takes 9-14 us of host time a call; here it is well under
-// one.  The checks are of what the C entry points cannot see: that every tensor is
+// thirty numbers to ctypes takes 15-22 us of host time a call; here a call takes 3 us,
+// its launches included.  The checks are of what the C entry points cannot see: that every tensor is
 // on the current device, and that shapes, types and strides fit one another.
 #include <Python.h>
 
@@ -67,7 +67,8 @@ struct Args {
     for (int i = 0; i < count; ++i) {
       need(!(dense >> i & 1) || seen[i]->is_contiguous(), "tensors must be contiguous");
       need(seen[i]->is_cuda(), "every tensor must be on the current CUDA device");
-      for (const int64_t n : seen[i]->sizes()) need(n <= 0x7FFFFFFF, "a size does not fit 32 bits");
+      for (const int64_t n : seen[i]->sizes())
+        need(n <= 0x7FFFFFFF, "a size does not fit 32 bits");
     }
     const int device = c10::cuda::current_device();
     for (int i = 0; i < count; ++i)

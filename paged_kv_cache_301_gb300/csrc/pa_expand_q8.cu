@@ -6,7 +6,10 @@
 // element at HBM bandwidth.  The two layouts differ in order: codes are
 // [head][row][dim], the 16-bit block is [row][head][dim].  Threads run in the
 // order of the 16-bit block, eight codes each, so that a warp's stores are one
-// contiguous 512 bytes and its loads are whole 64- or 128-byte rows.
+// contiguous 512 bytes and its loads are whole 64- or 128-byte rows (16 codes each, with
+// stores 32 bytes apart: 70 us).  Four such vectors of K and of V are in flight per
+// thread.  Measured: 65,536 tokens of 8 heads of 128, 403 MB, 62.7 us, 6.43 TB/s, 0.96 of
+// a plain copy; a handful of blocks 2.1 us.
 #include "pa_common.cuh"
 #include "pa_q8.cuh"
 
