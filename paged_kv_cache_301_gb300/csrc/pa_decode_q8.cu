@@ -40,7 +40,7 @@
 //   8 sequences of 32,768..131,072, 8 query heads each: 203 us, 6.62 TB/s, 0.99
 //   2,048 sequences of 16..1,024, 4 heads: 346-350 us, 6.37 TB/s, 0.95
 //   64 sequences of 128..4,096, 4 heads: 50.5 us, 5.5 TB/s, 0.82
-//   one sequence of 50,001, 5 heads: 28.1 us, 3.65 TB/s, 0.54
+//   one sequence of 50,001, 5 heads: 27.4 us, 3.74 TB/s, 0.56
 //   4 sequences of at most 64, 4 heads of 64: 4.8-5.5 us
 // About 9 us of a call do not shrink with its bytes: lengths -> window -> block ids ->
 // first tile 4 us, last tile and partials 2 us, join 2.7 us.  With 16 heads to a KV head
@@ -1026,34 +1026,70 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
 
 // Joins the partials of items that window boundaries cut: CTA c looks at the boundary
 // where window c + 1 begins, and joins its item, of kJoinHeads heads at most, if that
-// boundary is the item's first.  Its time is the chain of loads (window, then all
-// partials), so the partials are asked for before the weights are known: a warp
-// takes a head's maximum and weights, the other threads are elements of a head, the
-// parts dealt out to kJoinThreads / D groups of them.
+// boundary is the item's first.  With kByItem, for few items and many parts of each, CTA
+// (x, y) joins kJoinHeads heads of item x, and looks for its first boundary among all.
+// Its time is the chain of loads (window, then all partials), so the partials are asked
+// for before the weights are known: a warp takes a head's maximum and weights, the other
+// threads are elements of a head, the parts dealt out to kJoinThreads / D groups of them.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinAhead = 4;                  // parts of a group asked for at once
+constexpr int kPartsAhead = 4;                 // parts of a group asked for at once
 
-template <int D, int kJoinHeads>
+// Does boundary c cut an item for the first time?
+__device__ __forceinline__ bool first_cut(const Window& at, const Window& before, bool* same) {
+  *same = before.b == at.b && before.item == at.item;
+  // not an empty window, not a boundary between items, no earlier boundary in this item
+  return at.tiles > 0 && at.j > 0 && !(*same && before.j > 0);
+}
+
+template <int D, int kJoinHeads, bool kByItem>
 __global__ void __launch_bounds__(kJoinThreads, 2) join_q8_kernel(const Q8Args a, int grid) {
   constexpr int GROUPS = kJoinThreads / D;
+  constexpr int kJoinAhead = kByItem ? 4 * kPartsAhead : kPartsAhead;
+  static_assert(kMaxGrid <= kJoinThreads, "a thread per boundary");
   __shared__ float s_w[kJoinHeads][kMaxGrid];
   __shared__ float s_sum[GROUPS][kJoinHeads][D];
   allow_next_grid();
   wait_prior_grid();
-  const int c = (int)blockIdx.x + 1;
-  const Window at = a.info[c], before = a.info[c - 1];
-  if (at.tiles <= 0 || at.j == 0) return;      // an empty window, or a boundary between items
-  const bool same = before.b == at.b && before.item == at.item;
-  if (same && before.j > 0) return;            // an earlier boundary cuts this item
+  Window at;
+  bool same;
+  int c, h0 = 0;                               // boundary; first head of the chunk's
+  if (kByItem) {
+    __shared__ Window s_at;
+    __shared__ int s_c, s_same;
+    const int items = a.H * a.chunks, x = (int)blockIdx.x;
+    if (threadIdx.x == 0) s_c = 0;
+    __syncthreads();
+    c = (int)threadIdx.x + 1;
+    if (c < grid) {
+      at = a.info[c];
+      if (first_cut(at, a.info[c - 1], &same) && at.b * items + at.item == x) {
+        s_at = at;
+        s_same = same;
+        s_c = c;
+      }
+    }
+    __syncthreads();
+    c = s_c;
+    if (c == 0) return;                        // in one window
+    at = s_at;
+    same = s_same;
+    h0 = (int)blockIdx.y * kJoinHeads;
+  } else {
+    c = (int)blockIdx.x + 1;
+    at = a.info[c];
+    if (!first_cut(at, a.info[c - 1], &same)) return;
+  }
   // the parts: the segment of window c - 1 that ends there, then the first segments of
   // windows c .. last, last holding the item's final tile
   const int64_t windows = at.total / 4 < grid ? at.total / 4 : grid;   // fewer: of a tile each
   const int last = (int)min(((at.final + 1) * windows - 1) / at.total, windows - 1);
   const int parts = last - c + 2;
-  const int h = at.item / a.chunks, G = a.Hq / a.H, g0 = (at.item - h * a.chunks) * a.hch;
-  const int n = min(a.hch, G - g0);
+  const int h = at.item / a.chunks, G = a.Hq / a.H;
+  const int g0 = (at.item - h * a.chunks) * a.hch + h0;
+  const int n = min(kJoinHeads, min(a.hch - h0, G - g0));
+  if (n <= 0) return;                          // a last chunk of fewer heads
   const int64_t head = 2 * (int64_t)(c - 1) + (same ? 0 : 1);
-  auto row = [&](int k) { return (k == 0 ? head : 2 * (int64_t)(c + k - 1)) * a.hch; };
+  auto row = [&](int k) { return (k == 0 ? head : 2 * (int64_t)(c + k - 1)) * a.hch + h0; };
   const int d = threadIdx.x % D, group = threadIdx.x / D;
   float x[kJoinAhead][kJoinHeads];
 #pragma unroll
@@ -1197,10 +1233,19 @@ cudaError_t launch_heads(const CUtensorMap& k, const CUtensorMap& v, const Q8Arg
 
 // One CTA to a boundary and all of an item's heads: every CTA is resident at once (8
 // sequences of 32,768..131,072: 202.7 us; with a CTA to every cut segment 204.9).
+// Items of at least twice as many parts as such a CTA asks for at once: a CTA to an item
+// and two heads, whose loads are all asked for at once (one sequence of 131,072 and one KV
+// head of 5, 304 parts: 24.8 us for 30.2; one of 50,001 and eight of 5, 38 parts: 27.4 for
+// 28.1; four of 8,000, 9 parts: 22.2 for 21.2, so not those).
 template <int D>
 cudaError_t launch_join(const Q8Args& a, int grid, cudaStream_t stream) {
-  auto join = a.hch <= 2 ? join_q8_kernel<D, 2>
-                         : (a.hch <= 4 ? join_q8_kernel<D, 4> : join_q8_kernel<D, 8>);
+  const int64_t items = (int64_t)a.B * a.H * a.chunks;
+  if (items * 2 * kPartsAhead * (kJoinThreads / D) <= grid)
+    return launch_pdl(join_q8_kernel<D, 2, true>,
+                      dim3((unsigned)items, (unsigned)((a.hch + 1) / 2)), kJoinThreads, 0, stream,
+                      a, grid);
+  auto join = a.hch <= 2 ? join_q8_kernel<D, 2, false>
+                         : (a.hch <= 4 ? join_q8_kernel<D, 4, false> : join_q8_kernel<D, 8, false>);
   return launch_pdl(join, dim3((unsigned)(grid - 1)), kJoinThreads, 0, stream, a, grid);
 }
 

@@ -172,6 +172,14 @@ def test_decode_many_tiles_per_window(pa, D, G, bs):
             assert not bad.any(), (b, h, int(bad.sum()))
 
 
+@pytest.mark.parametrize("D,G,n", [(128, 1, 40001), (128, 3, 6500), (128, 5, 40001), (128, 9, 40001),
+                                   (64, 7, 80003)])
+def test_decode_one_item_in_many_parts(pa, D, G, n):
+    """One KV head and one sequence: every window boundary cuts the same item(s)."""
+    b = Batch([n], G, 1, D, 32, "bf16", seed=G)
+    b.check(b.run(pa))
+
+
 @pytest.mark.parametrize("G", [1, 8])
 def test_decode_d64_segments_of_one_tile(pa, G):
     """head_dim 64: segments of one tile follow one another to the end of every window, and
