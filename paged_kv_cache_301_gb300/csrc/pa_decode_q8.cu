@@ -9,9 +9,11 @@
 // everything 16- or 32-bit is brought to them:
 //   - q is split into three e4m3 digits of four bits, q = s (d0 + d1/16 + d2/256)
 //     with s a power of two: 12 bits, which is all of bf16's 8 and fp16's 11;
-//   - the softmax weights, times the block's V scale over the largest V scale of
-//     the tile, are rounded to fp16 and split the same way: 2^-11 of each weight (a
-//     single e4m3 weight would be off by 2^-4), and 2^-26 of the largest.
+//   - the softmax weights, times the block's V scale, in units of their own largest
+//     in the tile (of each head, a power of two), are rounded to fp16 and split the same
+//     way: 2^-11 of each (a single e4m3 weight would be off by 2^-4), and 2^-25 of the
+//     largest.  The unit follows weight and scale together: a block of a large scale and
+//     no weight takes nothing from the others.
 // Products of digits are exact and the sums are fp32.  K scales multiply the
 // finished scores.
 //
@@ -126,10 +128,13 @@ struct Tail {
   float qscale[2][GP];
   uint32_t q[2][GP][D / 2];      // q as it is, of a segment and the one behind it
   float inv[4][GP];              // per warp: 1 / the weights' sums of a finished segment
-  float red[2][4][GP + 1];       // per warp: heads' maxima, the largest V scale
-  struct alignas(8) {            // per warp: heads' running maxima, then 2^(before - now)
-    float now[2 * GP];
-  } top[4][2];
+  float red[2][4][2 * GP];       // per warp: heads' maxima of s, then of s + log2(V scale)
+  struct alignas(8) {            // per warp: heads' running maxima of s
+    float now[GP];
+  } top[4];
+  struct alignas(8) {            // per warp: heads' 2^(before - now), then the weights' units
+    float by[2 * GP];
+  } fold[4][2];
   float lred[2][4][GP];          // of a finished segment, per warp: weights' sums
   float mred[2][GP];             // ... and the maxima
   float half[2][D == 64 ? GP * 64 : 1];   // head_dim 64: the other parity's sums, by segment
@@ -315,6 +320,17 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / x of a power of two from 2^-126 to 2^126.
+__device__ __forceinline__ float inverse_pow2(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
 }
 
 // Byte `col` of row n of a K-major operand with 128-byte rows and 128-byte swizzle.
@@ -759,7 +775,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
     for (int c = 0; c < 8; ++c) put[c] = smem + S::kPOff + (((r >> 4) ^ c) << 4) + (r & 15);
     float x[TPR][GP];                           // scores of the tile ahead
-    float l[GP], acc[GP], unit = 0.f;           // unit: of the tile behind
+    float l[GP], acc[GP];
     float m_lane = -CUDART_INF_F;               // head `lane`: the running maximum
     int seg = 0;                                // segment of tile t
 
@@ -793,13 +809,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
           if (g1 > g) x[v][g1] = live ? x1 : -CUDART_INF_F;
         }
       }
+      const float lv = lg2_approx(vs);            // -inf: no token, or a bad block
+      float mine = 0.f;
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
-        const float w = warp_max(TPR == 2 ? fmaxf(x[0][g], x[TPR - 1][g]) : x[0][g]);
-        if (lane == g) tail->red[slot][wq][g] = w;
+        const float s_row = TPR == 2 ? fmaxf(x[0][g], x[TPR - 1][g]) : x[0][g];
+        const float w = warp_max(s_row), wv = warp_max(s_row + lv);
+        if (lane == g) mine = w;
+        if (lane == GP + g) mine = wv;
       }
-      const float wv = warp_max(vs);
-      if (lane == 0) tail->red[slot][wq][GP] = wv;
+      if (lane < 2 * GP) tail->red[slot][wq][lane] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->red_bar[slot]);
       return true;
@@ -813,18 +832,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       load_cols<cols_for(3 * GP)>(tmem + lanes + (2 + slot) * N + par * 3 * GP, o);
       const uint64_t c16 = f2_pack(1.f / 16.f, 1.f / 16.f);
       const uint64_t c256 = f2_pack(1.f / 256.f, 1.f / 256.f);
-      const uint64_t unit2 = f2_pack(unit, unit);
+      const float* by = tail->fold[wq][slot].by;
 #pragma unroll
       for (int g = 0; g < GP; g += 2) {
         const int g1 = g + 1 < GP ? g + 1 : g;
         const uint64_t sum =
             f2_fma(f2_pack(o[2 * GP + g], o[2 * GP + g1]), c256,
                    f2_fma(f2_pack(o[GP + g], o[GP + g1]), c16, f2_pack(o[g], o[g1])));
-        const uint64_t was = f2_mul(f2_pack(acc[g], acc[g1]),
-                                    f2_pack(tail->top[wq][slot].now[GP + g],
-                                            tail->top[wq][slot].now[GP + g1]));
+        const uint64_t was = f2_mul(f2_pack(acc[g], acc[g1]), f2_pack(by[g], by[g1]));
         float y0, y1;
-        f2_unpack(f2_fma(sum, unit2, was), y0, y1);
+        f2_unpack(f2_fma(sum, f2_pack(by[GP + g], by[GP + g1]), was), y0, y1);
         acc[g] = y0;
         if (g1 > g) acc[g1] = y1;
       }
@@ -893,7 +910,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
       const bool have = cur.left > 0;
       const bool ends = have && (cur.j + 1 == cur.nt || cur.left == 1);
       const Walk<TOKENS> ahead = walk;          // tile t + 1
-      float ks2 = 0.f, vs2 = 0.f, vmax = 0.f;
+      float ks2 = 0.f, vs2 = 0.f;
       if (ahead.left > 0) {
         walk.next(a);
         scales_of(walk, ks2, vs2);              // tile t + 2
@@ -907,27 +924,31 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
         }
         if (!wait_all(&tail->red_bar[slot], (t >> 1) & 1)) { ok = false; break; }
         {
-          const float* red = &tail->red[slot][0][min(lane, GP)];
+          const float* red = &tail->red[slot][0][min(lane, 2 * GP - 1)];
           const float top =
-              fmaxf(fmaxf(red[0], red[GP + 1]), fmaxf(red[2 * GP + 2], red[3 * GP + 3]));
-          vmax = __shfl_sync(kAll, top, GP);
+              fmaxf(fmaxf(red[0], red[2 * GP]), fmaxf(red[4 * GP], red[6 * GP]));
+          const float top_v = __shfl_sync(kAll, top, (lane + GP) & 31);
           if (lane < GP) {
             const float now = fmaxf(m_lane, top);
-            tail->top[wq][slot].now[lane] = now;
-            tail->top[wq][slot].now[GP + lane] = ex2_approx(m_lane - now);
+            // the largest weight times scale is 2^e or less; where it is below 2^-110 (a
+            // tile that adds nothing to the running maximum's, or no live block), 2^-110
+            const int e = min(127, __float2int_ru(fmaxf(top_v - now, -110.f)));
+            tail->top[wq].now[lane] = now;
+            tail->fold[wq][slot].by[lane] = ex2_approx(m_lane - now);
+            tail->fold[wq][slot].by[GP + lane] = __uint_as_float((uint32_t)(127 - 8 + e) << 23);
             m_lane = now;
           }
           __syncwarp();
         }
-        // weights, in units of the tile's largest V scale and 256 at most
-        const float to = vmax > 0.f ? vs_cur * (256.f / vmax) : 0.f;
-        const float* top = tail->top[wq][slot].now;
-        const uint64_t to2 = f2_pack(to, to);
+        // weights times V scale, in units that leave 256 at most
+        const float *top = tail->top[wq].now, *by = tail->fold[wq][slot].by;
+        const uint64_t vs_both = f2_pack(vs_cur, vs_cur);
 #pragma unroll
         for (int g = 0; g < GP; g += 2) {
           const int g1 = g + 1 < GP ? g + 1 : g;
           const uint64_t m2 = f2_pack(top[g], top[g1]);
-          uint64_t sum = f2_mul(f2_pack(l[g], l[g1]), f2_pack(top[GP + g], top[GP + g1]));
+          const uint64_t per_unit = f2_pack(inverse_pow2(by[GP + g]), inverse_pow2(by[GP + g1]));
+          uint64_t sum = f2_mul(f2_pack(l[g], l[g1]), f2_pack(by[g], by[g1]));
 #pragma unroll
           for (int v = 0; v < TPR; ++v) {
             float p0, p1;                         // 0 behind the end
@@ -937,7 +958,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
             const uint64_t p2 = f2_pack(p0, p1);
             sum = f2_add(sum, p2);
             float w0, w1;
-            f2_unpack(f2_mul(p2, to2), w0, w1);
+            f2_unpack(f2_mul(f2_mul(p2, vs_both), per_unit), w0, w1);
             uint32_t d[3];
             digits2(__floats2half2_rn(w0, w1), d);
 #pragma unroll
@@ -995,7 +1016,6 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
         ok = false;
         break;
       }
-      unit = vmax * (1.f / 256.f);
       fin = ends;
       if (ends) {
         fin_b = cur.b;

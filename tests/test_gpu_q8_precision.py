@@ -1,0 +1,124 @@
+"""How exact the 8-bit cache's decode attention is where its digits could lose something:
+blocks of one sequence whose V scales are far apart, against the definition in fp64.
+
+Bounds, for one query head, with p the softmax weights, w_t = p_t (V scale of t's block),
+A = sum_t p_t |V_t| and C = sum_t |code of V_t| per output element, U = max_t w_t, and
+S = max_t scale sum_d |q_d K_td|:
+  - scores: at most 3 x 128 products summed in fp32, 384 * 2^-24 S = 2^-15.4 S in natural
+    units; a weight is off by twice that (itself and the normaliser);
+  - weights: e4m3 digits of an fp16 number, 2^-11 of each;
+  - the last digit's steps are 2^-17 where the tile's largest w is between 128 and 256, so
+    half a step is at most 2^-25 U of a w, and that many codes: 2^-25 U C;
+  - exponentials, products and sums in fp32: taken as 2^-16 A;
+  - the store: half a step of the type."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_q8 as oq
+from tests.gpu_helpers import lib
+from tests.test_gpu_cache_q8 import Batch, f64
+
+pytestmark = pytest.mark.gpu
+WEIGHT = 2.0 ** -11
+
+
+@pytest.fixture(scope="module")
+def pa():
+    return lib()
+
+
+def check(b, out):
+    """`out` against fp64 attention over b's codes and scales, within the bounds above."""
+    half = torch.finfo(b.dt).eps / 2
+    tiny = float(torch.finfo(b.dt).smallest_normal) * half
+    q, got = f64(b.q), f64(out)
+    values = [oq.values_q8(c, s) for c, s in zip(b.codes, b.scales)]
+    for i, n in enumerate(b.lens):
+        if n == 0:
+            continue
+        pos = np.arange(n)
+        blk = b.tables[i, pos // b.bs]
+        for hq in range(q.shape[1]):
+            h = hq * b.H // q.shape[1]
+            k, v = (x[blk, pos % b.bs, h] for x in values)
+            s = b.scale * (k @ q[i, hq])
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            size = b.scale * (np.abs(k) @ np.abs(q[i, hq])).max()
+            scale_v = b.scales[1][blk, h].astype(np.float64)
+            a = p @ np.abs(v)
+            c = (np.abs(v) / scale_v[:, None]).sum(0)
+            e = (WEIGHT + 2.0 ** -14.4 * size + 2.0 ** -16) * a + 2.0 ** -25 * (p * scale_v).max() * c
+            ref = p @ v
+            bad = ~(np.abs(got[i, hq] - ref) <= half * (np.abs(ref) + e) + e + tiny)
+            assert not bad.any(), (i, hq, int(bad.sum()), np.abs(got[i, hq] - ref).max(), ref[bad][:3])
+
+
+def put(b):
+    """b's codes and scales to the GPU."""
+    for x, y in zip(b.pools + b.sc, b.codes + b.scales):
+        x.copy_(torch.from_numpy(y))
+
+
+def lean(b, i, blocks, by):
+    """Sequence i's scores in `blocks` (places in its table) rise by `by` (base 2) over what
+    they are elsewhere, by K's first channel; its second one spreads them by a factor of a
+    few, and q sees no other."""
+    b.q[i] = 0
+    b.q[i, :, 0] = 1
+    b.q[i, :, 1] = 1.0 / by
+    for j in range(-(-b.lens[i] // b.bs)):
+        blk = b.tables[i, j]
+        n = min(b.bs, b.lens[i] - j * b.bs)
+        b.codes[0][blk, :, :n, 0] = oq.encode_e4m3(np.array(64.0 if j in blocks else 0.0))
+        b.scales[0][blk] = by * np.log(2.0) / b.scale / 64.0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,G", [(128, 1), (128, 4), (128, 5), (128, 8), (64, 2), (64, 8)])
+@pytest.mark.parametrize("apart", [16, 20, 24, 30, 60])
+def test_a_block_of_large_scale_and_no_weight(pa, D, G, dt, apart):
+    """A tile of eight blocks: one has a V scale 2^apart times the others' and 2^-(apart + 6)
+    of their weight.  The others decide the output, and keep their bits."""
+    b = Batch([128, 100, 1000], G, 2, D, 16, dt, seed=apart)
+    for i, n in enumerate(b.lens):
+        used = -(-n // 16)
+        lean(b, i, [j for j in range(used) if j != 2], apart + 6)
+        for j in range(used):
+            b.scales[1][b.tables[i, j]] = 2.0 ** (apart - 6 if j == 2 else -6)
+    put(b)
+    check(b, b.run(pa))
+
+
+@pytest.mark.parametrize("D,G", [(128, 3), (64, 4)])
+def test_scales_over_their_whole_range(pa, D, G):
+    """V scales from 2^-100 to 2^80, block by block, with weights that make up for them or
+    do not: every sequence's own largest weight times scale sets its bits."""
+    spans = [(-40, 81), (-100, 81), (-64, 20), (-100, -60), (-64, 64)]
+    b = Batch([64, 128, 200, 777, 1300], G, 2, D, 8, "bf16", seed=3)
+    g = np.random.default_rng(5)
+    for i, (n, span) in enumerate(zip(b.lens, spans)):
+        used = -(-n // 8)
+        b.scales[1][b.tables[i, :used]] = 2.0 ** g.integers(*span, size=(used, 2))
+    put(b)
+    check(b, b.run(pa))
+
+
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 5)])
+@pytest.mark.parametrize("by", [100, 140, 400])
+def test_a_tile_far_below_the_running_maximum(pa, D, G, by):
+    """Later tiles whose weights are 2^-by of the first one's: they add next to nothing, or
+    nothing, and no NaN; and first ones that a later tile leaves that far behind."""
+    b = Batch([512, 700, 640], G, 2, D, 16, "bf16", seed=by)
+    lean(b, 0, range(0, 8), by)
+    lean(b, 1, range(40, 44), by)
+    lean(b, 2, [], by)                       # weights of one size throughout
+    for i in (0, 1):
+        used = -(-b.lens[i] // 16)
+        b.scales[1][b.tables[i, :used]] = 2.0 ** -70
+        b.scales[1][b.tables[i, 20]] = 2.0 ** 30
+    put(b)
+    out = b.run(pa)
+    assert torch.isfinite(out).all()
+    check(b, out)
