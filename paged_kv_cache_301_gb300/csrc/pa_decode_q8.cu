@@ -10,10 +10,10 @@
 //   - q is split into three e4m3 digits of four bits, q = s (d0 + d1/16 + d2/256)
 //     with s a power of two: 12 bits, which is all of bf16's 8 and fp16's 11;
 //   - the softmax weights, times the block's V scale, in units of their own largest
-//     in the tile (of each head, a power of two), are rounded to fp16 and split the same
-//     way: 2^-11 of each (a single e4m3 weight would be off by 2^-4), and 2^-25 of the
-//     largest.  The unit follows weight and scale together: a block of a large scale and
-//     no weight takes nothing from the others.
+//     in the tile (of each head, a power of two), are split the same way: each is off by
+//     2^-13.6 of itself (a single digit would be off by 2^-4), or 2^-25 of the largest
+//     where that is more.  The unit follows weight and scale together: a block of a large
+//     scale and no weight takes nothing from the others.
 // Products of digits are exact and the sums are fp32.  K scales multiply the
 // finished scores.
 //
@@ -290,8 +290,10 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// The three digits of x (|x| <= 448): x = d0 + d1 / 16 + d2 / 256 up to 2^-12 |x|
-// or 2^-18.  For two values at once; digit i of the first in byte 0 of d[i].
+// The three digits of x (|x| <= 448): x = d0 + d1 / 16 + d2 / 256.  With 2^e <= |x| < 2^(e+1)
+// a digit of four bits leaves 2^(e-4) at most; times 16 that is 2^e, whose digit leaves
+// 2^(e-5), times 16 again 2^(e-1), and the last one leaves 2^(e-6), 2^-14 |x| in all, or half
+// a subnormal step, 2^-18.  For two values at once; digit i of the first in byte 0 of d[i].
 __device__ __forceinline__ void digits2(float x, float y, uint32_t (&d)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -304,22 +306,27 @@ __device__ __forceinline__ void digits2(float x, float y, uint32_t (&d)[3]) {
   }
 }
 
-// The same of two values held as fp16 (11 bits, so exact up to 2^-18).
-__device__ __forceinline__ void digits2(__half2 x, uint32_t (&d)[3]) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    d[i] = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E4M3);
-    if (i < 2) {
-      const __half2 v(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)d[i], __NV_E4M3));
-      x = __hmul2(__hsub2(x, v), __half2half2(__float2half(16.f)));
-    }
-  }
-}
-
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// The same of the weights, the bulk of the softmax warps' work: what the first digit leaves
+// is exact in fp32 and goes on as fp16, two values to an instruction (2^-16 |x| more).
+__device__ __forceinline__ void digits2_short(uint64_t x, uint32_t (&d)[3]) {
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  d[0] = e4m3x2(x0, x1);
+  const float2 v = e4m3_widen2(d[0]);
+  const uint64_t left = f2_mul(f2_sub(x, f2_pack(v.x, v.y)), f2_pack(16.f, 16.f));
+  f2_unpack(left, x0, x1);
+  const __half2 h = __floats2half2_rn(x0, x1);
+  d[1] = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(h), __NV_SATFINITE, __NV_E4M3);
+  const __half2 w(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)d[1], __NV_E4M3));
+  d[2] = __nv_cvt_halfraw2_to_fp8x2(
+      __half2_raw(__hmul2(__hsub2(h, w), __half2half2(__float2half(16.f)))), __NV_SATFINITE,
+      __NV_E4M3);
 }
 
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -957,10 +964,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
             p1 = ex2_approx(p1);
             const uint64_t p2 = f2_pack(p0, p1);
             sum = f2_add(sum, p2);
-            float w0, w1;
-            f2_unpack(f2_mul(f2_mul(p2, vs_both), per_unit), w0, w1);
             uint32_t d[3];
-            digits2(__floats2half2_rn(w0, w1), d);
+            digits2_short(f2_mul(f2_mul(p2, vs_both), per_unit), d);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
               const int row = (v * 3 + i) * GP + g;

@@ -1,12 +1,15 @@
 """How exact the 8-bit cache's decode attention is where its digits could lose something:
-blocks of one sequence whose V scales are far apart, against the definition in fp64.
+weights of any size, blocks of one sequence whose V scales are far apart, against the
+definition in fp64.
 
 Bounds, for one query head, with p the softmax weights, w_t = p_t (V scale of t's block),
 A = sum_t p_t |V_t| and C = sum_t |code of V_t| per output element, U = max_t w_t, and
 S = max_t scale sum_d |q_d K_td|:
   - scores: at most 3 x 128 products summed in fp32, 384 * 2^-24 S = 2^-15.4 S in natural
     units; a weight is off by twice that (itself and the normaliser);
-  - weights: e4m3 digits of an fp16 number, 2^-11 of each;
+  - weights: three e4m3 digits of an fp32 number, 2^-14 of each (four bits of it, then five
+    and five of what is left), of which the last two may go by fp16, whose half step is
+    2^-12 of at most 2^-4 of it: 2^-13.6 in all;
   - the last digit's steps are 2^-17 where the tile's largest w is between 128 and 256, so
     half a step is at most 2^-25 U of a w, and that many codes: 2^-25 U C;
   - exponentials, products and sums in fp32: taken as 2^-16 A;
@@ -20,7 +23,7 @@ from tests.gpu_helpers import lib
 from tests.test_gpu_cache_q8 import Batch, f64
 
 pytestmark = pytest.mark.gpu
-WEIGHT = 2.0 ** -11
+WEIGHT = 2.0 ** -13.6
 
 
 @pytest.fixture(scope="module")
@@ -73,6 +76,26 @@ def lean(b, i, blocks, by):
         n = min(b.bs, b.lens[i] - j * b.bs)
         b.codes[0][blk, :, :n, 0] = oq.encode_e4m3(np.array(64.0 if j in blocks else 0.0))
         b.scales[0][blk] = by * np.log(2.0) / b.scale / 64.0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,G", [(128, 1), (128, 2), (128, 5), (128, 8), (64, 4), (64, 7)])
+def test_weights_keep_their_bits(pa, D, G, dt):
+    """Three tokens: the first has the largest weight and no V, the others opposite V, so
+    that the output is the difference of their weights."""
+    b = Batch([3] * 40, G, 2, D, 16, dt, seed=G)
+    g = np.random.default_rng(D + G)
+    b.q.zero_()
+    b.q[:, :, 0] = torch.from_numpy(g.uniform(0.5, 1, size=b.q.shape[:2])).to(b.dt)
+    for i in range(len(b.lens)):
+        blk = b.tables[i, 0]
+        b.codes[0][blk, :, 0, 0] = oq.encode_e4m3(np.array(64.0))
+        b.codes[0][blk, :, 1:3, 0] = oq.encode_e4m3(g.uniform(-60, 60, size=(2, 2)))
+        b.scales[0][blk] = 1.0 / (64 * b.scale)              # scores of 1 and less
+        b.codes[1][blk, :, 0] = 0
+        b.codes[1][blk, :, 2] = b.codes[1][blk, :, 1] ^ 0x80
+    put(b)
+    check(b, b.run(pa))
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
