@@ -51,6 +51,20 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _bytes_on(n: int, device, stream) -> torch.Tensor:
+    """n bytes for a call on `stream` (as _stream takes it), allocated under that stream: the
+    caching allocator hands them out again in its order, whatever becomes of the tensor.
+    Under another stream it could do so while the call still uses them."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)                       # 1 is the legacy default stream, as 0 is
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1) else
+                  torch.cuda.ExternalStream(handle, device=device))
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _dtype(t: torch.Tensor) -> int:
     try:
         return _DTYPES[t.dtype]
@@ -89,9 +103,10 @@ def pa_decode_workspace_bytes_for(num_seqs: int, num_q_heads: int, num_kv_heads:
 
 def workspace_for(q: torch.Tensor, k_pool: torch.Tensor, block_tables: torch.Tensor,
                   max_seq_len: int, partition_tokens: int = 0,
-                  strict: bool = True) -> torch.Tensor:
+                  strict: bool = True, stream=None) -> torch.Tensor:
     """The workspace of exactly the size the decode kernel serving this call
-    needs (pa_decode_workspace_bytes_for, under the current kernel selection).
+    needs (pa_decode_workspace_bytes_for, under the current kernel selection),
+    for calls on `stream` (None: the current one).
     For arguments the library would reject: ValueError, or with strict=False an
     empty tensor, so that the decode call itself reports the library's status."""
     B, Hq, D = q.shape
@@ -100,7 +115,7 @@ def workspace_for(q: torch.Tensor, k_pool: torch.Tensor, block_tables: torch.Ten
                                       int(max_seq_len), _dtype(q), partition_tokens)
     if n == 0 and strict:
         raise ValueError("invalid decode arguments")
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+    return _bytes_on(n, q.device, stream)
 
 
 def pa_decode(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -120,7 +135,7 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_pool: 
         max_seq_len = MB * bs
     if workspace is None:
         workspace = workspace_for(q, k_pool, block_tables, max_seq_len, partition_tokens,
-                                  strict=False)
+                                  strict=False, stream=stream)
     st = lib().pa_decode(
         _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(seq_lens),
         B, Hq, Hkv, D, bs, MB, NB, int(max_seq_len), float(scale), _dtype(q),
@@ -146,7 +161,7 @@ def pa_decode_append(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
         max_seq_len = MB * bs
     if workspace is None:
         workspace = workspace_for(q, k_pool, block_tables, max_seq_len, partition_tokens,
-                                  strict=False)
+                                  strict=False, stream=stream)
     st = lib().pa_decode_append(
         _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(key), _ptr(value),
         _ptr(block_tables), _ptr(seq_lens), B, Hq, Hkv, D, bs, MB, NB, int(max_seq_len),
@@ -397,14 +412,16 @@ def pa_rope_append_q8(q_out: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.T
     return q_out
 
 
-def workspace_for_q8(q: torch.Tensor, k_pool: torch.Tensor, max_seq_len: int) -> torch.Tensor:
-    """The workspace of pa_decode_q8 for q [B, Hq, D] over an 8-bit pool."""
+def workspace_for_q8(q: torch.Tensor, k_pool: torch.Tensor, max_seq_len: int,
+                     stream=None) -> torch.Tensor:
+    """The workspace of pa_decode_q8 for q [B, Hq, D] over an 8-bit pool, for calls on
+    `stream` (None: the current one)."""
     B, Hq, D = q.shape
     _, H, bs, _ = k_pool.shape
     n = int(lib().pa_decode_q8_workspace_bytes(B, Hq, H, D, bs, int(max_seq_len)))
     if n == 0:
         raise ValueError("invalid decode arguments")
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+    return _bytes_on(n, q.device, stream)
 
 
 def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -416,7 +433,7 @@ def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor, v_poo
     max_seq_len and workspace default as in pa_decode."""
     if workspace is None:
         most = block_tables.shape[1] * k_pool.shape[2] if max_seq_len is None else max_seq_len
-        workspace = workspace_for_q8(q, k_pool, most)
+        workspace = workspace_for_q8(q, k_pool, most, stream)
     st = (_native or _bind()).decode_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
                                         seq_lens, scale, max_seq_len, workspace, status, stream)
     _check(st, "pa_decode_q8")
