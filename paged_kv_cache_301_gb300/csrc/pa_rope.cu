@@ -18,6 +18,8 @@
 // sequences with norms 3.2-3.5 us; prompts of 18,432 tokens 75.4 us, 6.04 TB/s, 0.90 of
 // a plain copy (the register kernel alone: 102 us); into the 8-bit cache: 256 sequences
 // 3.5-4.1 us, 18,432 tokens with norms 81 us, 5.1 TB/s.
+#include <mutex>
+
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_q8.cuh"
@@ -986,23 +988,26 @@ pa_status check_rope_pointers(const RopeArgs& a, int head_dim) {
 }
 
 // How tokens of `rows` head rows go through shared memory: stages of a CTA (0: the
-// register kernel), tokens of a stage, bytes of all stages, CTAs.
+// register kernel), tokens of a stage, bytes of all stages, CTAs; the current device.
 struct Stream {
-  int stages, together, bytes, ctas;
+  int stages, together, bytes, ctas, device;
 };
+
+constexpr int kSmemOfSm = 227 * 1024;
+constexpr int kSmemStatic = 9 * 1024;          // more than either kernel's own, and 1 KB a CTA
 
 // `resident` CTAs of an SM at most.
 pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int resident, Stream* s) {
-  *s = {0, 1, 0, tokens};
-  int device = 0, sms = 0;
-  if (cudaGetDevice(&device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+  *s = {0, 1, 0, tokens, 0};
+  int sms = 0;
+  if (cudaGetDevice(&s->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, s->device) != cudaSuccess)
     return PA_ERR_CUDA;
   if (tokens < kStreamTokens * sms) return PA_OK;
   // where two stages of each fit the SM's shared memory, else fewer
   const int64_t token = (int64_t)rows * head_dim * 2 + rotary * 4;
   for (int per_sm = resident; per_sm; --per_sm) {
-    const int64_t room = (227 * 1024) / per_sm - 9 * 1024;
+    const int64_t room = kSmemOfSm / per_sm - kSmemStatic;
     if (2 * token > room) continue;
     while (s->together < kMaxTogether && 3 * 2 * s->together * token <= room) s->together *= 2;
     const int64_t stage = s->together * token;
@@ -1016,12 +1021,19 @@ pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int reside
   return PA_OK;
 }
 
-// Shared memory above 48 KB, static included (under 9 KB in each kernel), has to be
-// asked for.
-template <typename K>
-cudaError_t allow_smem(K* kernel, int bytes) {
-  if (bytes <= 39 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// Shared memory above 48 KB has to be asked for.  The kernel's limit is a property of the
+// kernel, not of a launch: it is set once per device, to the most that any plan takes, so
+// that no call lowers it between another thread's setting and launch.
+template <auto Kernel>
+cudaError_t allow_smem(int device) {
+  static std::mutex lock;
+  static uint64_t done = 0;                    // devices whose limit is set
+  std::lock_guard<std::mutex> hold(lock);
+  if (device < 64 && (done >> device & 1)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSmemOfSm - kSmemStatic);
+  if (e == cudaSuccess && device < 64) done |= 1ull << device;
+  return e;
 }
 
 template <int DT, int D, int BS>
@@ -1050,7 +1062,8 @@ cudaError_t launch_blocks(const RopeArgs& a, const Stream& s, cudaStream_t strea
   const int64_t kv = runs * groups;
   if (kv + s.ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const int bytes = s.bytes > kv_bytes<D, BS>() ? s.bytes : kv_bytes<D, BS>();
-  const cudaError_t e = allow_smem(rope_append_q8_kernel<DT, D, BS>, bytes);
+  static_assert(kv_bytes<D, BS>() <= kSmemOfSm - kSmemStatic, "within the kernel's limit");
+  const cudaError_t e = allow_smem<rope_append_q8_kernel<DT, D, BS>>(s.device);
   if (e != cudaSuccess) return e;
   return launch_pdl(rope_append_q8_kernel<DT, D, BS>, dim3((unsigned)(kv + s.ctas)), kRowThreads,
                     bytes, stream, a, (int)kv, groups, run, s.stages, s.together);
@@ -1087,7 +1100,7 @@ cudaError_t launch_16(const RopeArgs& a, cudaStream_t stream) {
   if (!s.stages)
     return launch_pdl(rope_append_kernel<DT, D>, dim3((unsigned)a.total_q), kRowThreads, 0, stream,
                       a);
-  const cudaError_t e = allow_smem(rope_stream_kernel<DT, D>, s.bytes);
+  const cudaError_t e = allow_smem<rope_stream_kernel<DT, D>>(s.device);
   if (e != cudaSuccess) return e;
   return launch_pdl(rope_stream_kernel<DT, D>, dim3((unsigned)s.ctas), kRowThreads, s.bytes,
                     stream, a, s.stages, s.together);
