@@ -1321,12 +1321,13 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   const Plan p = plan_of(num_q_heads, num_kv_heads, head_dim, max_seq_len);
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.total)
     return PA_ERR_WORKSPACE;
-  // 32-bit costs of tiles, rows and grid
+  // 32-bit rows, tiles of all sequences, and cost of one sequence's items (4 a tile and at
+  // most 4 an item, which the kernel takes apart in 32 bits)
   const int block_rows = block_size * head_dim / 128;
   const long long rows = (long long)num_blocks * num_kv_heads * block_rows;
   if (rows >= (1ll << 31) || (long long)num_seqs * p.tiles >= (1ll << 28) ||
       (long long)num_kv_heads * p.chunks >= (1ll << 20) ||
-      p.tiles * num_kv_heads * p.chunks >= (1ll << 31))
+      4 * (p.tiles + 1) * num_kv_heads * p.chunks >= (1ll << 31))
     return PA_ERR_INVALID_ARG;
   int device = 0, sms = 0;
   if (!encode_fn() || cudaGetDevice(&device) != cudaSuccess ||
