@@ -68,6 +68,13 @@ __device__ __forceinline__ void allow_next_grid() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The error of a CUDA call, taken out of the runtime's last-error slot: the call that failed
+// reports it, and no later PA_CHECK_LAUNCH does so again.
+inline cudaError_t taken(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem,
                        cudaStream_t stream, Args&&... args) {
@@ -81,7 +88,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int sme
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+  return taken(cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...));
 }
 
 }  // namespace pa

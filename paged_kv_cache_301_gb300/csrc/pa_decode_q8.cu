@@ -1236,8 +1236,8 @@ cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const Q8Ar
   {
     std::lock_guard<std::mutex> hold(lock);
     if (device >= 64 || !(done >> device & 1)) {
-      const cudaError_t e = cudaFuncSetAttribute(
-          decode_q8_kernel<D, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      const cudaError_t e = taken(cudaFuncSetAttribute(
+          decode_q8_kernel<D, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
       if (e != cudaSuccess) return e;
       if (device < 64) done |= 1ull << device;
     }
@@ -1330,8 +1330,8 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
       4 * (p.tiles + 1) * num_kv_heads * p.chunks >= (1ll << 31))
     return PA_ERR_INVALID_ARG;
   int device = 0, sms = 0;
-  if (!encode_fn() || cudaGetDevice(&device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+  if (!encode_fn() || taken(cudaGetDevice(&device)) != cudaSuccess ||
+      taken(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
     return PA_ERR_CUDA;
   CUtensorMap k, v;
   if (!encode_pool(&k, k_pool, rows, block_rows) || !encode_pool(&v, v_pool, rows, block_rows))

@@ -1000,8 +1000,9 @@ constexpr int kSmemStatic = 9 * 1024;          // more than either kernel's own,
 pa_status plan_stream(int tokens, int rows, int head_dim, int rotary, int resident, Stream* s) {
   *s = {0, 1, 0, tokens, 0};
   int sms = 0;
-  if (cudaGetDevice(&s->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, s->device) != cudaSuccess)
+  if (taken(cudaGetDevice(&s->device)) != cudaSuccess ||
+      taken(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, s->device)) !=
+          cudaSuccess)
     return PA_ERR_CUDA;
   if (tokens < kStreamTokens * sms) return PA_OK;
   // where two stages of each fit the SM's shared memory, else fewer
@@ -1030,8 +1031,8 @@ cudaError_t allow_smem(int device) {
   static uint64_t done = 0;                    // devices whose limit is set
   std::lock_guard<std::mutex> hold(lock);
   if (device < 64 && (done >> device & 1)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmemOfSm - kSmemStatic);
+  const cudaError_t e = taken(cudaFuncSetAttribute(
+      Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOfSm - kSmemStatic));
   if (e == cudaSuccess && device < 64) done |= 1ull << device;
   return e;
 }
