@@ -370,7 +370,12 @@ def _bind():
     global _native
     if _native is None:
         lib()
-        from . import _binding
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError("the compiled binding (_binding.so) of this call is missing or "
+                              "built for another Python or PyTorch; build it with `python -m "
+                              f"paged_kv_cache_301_gb300.build`: {e}") from e
         _native = _binding
     return _native
 

@@ -1,10 +1,11 @@
 """Compile libpagedattn.so in-tree for GB300 (sm_103a).
 
 Each translation unit is compiled in parallel with nvcc into _build/, then
-linked into paged_kv_cache_301_gb300/libpagedattn.so; the Python binding of some
-calls (_binding.so, host code against PyTorch's headers) is linked to it.  A stamp
-records the host machine and the Python and PyTorch versions, so that what was built
-for others is rebuilt.
+linked into paged_kv_cache_301_gb300/libpagedattn.so, which is all that users of the C ABI
+need; a stamp records the host machine, so that a library built on another architecture
+is rebuilt.  The Python binding of some calls (_binding.so) is host code against Python's
+and PyTorch's headers, linked to the library, with a stamp of their versions.  Where it
+cannot be built the library is made all the same.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +26,7 @@ LIB = os.path.join(PKG, "libpagedattn.so")
 BINDING = os.path.join(PKG, "_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "pa_binding.cpp")
 STAMP = os.path.join(BUILD, "machine.txt")
+BINDING_STAMP = os.path.join(BUILD, "binding.txt")
 
 SOURCES = [
     "pa_api.cu",
@@ -60,16 +63,24 @@ def _built_for() -> str:
     return f"{platform.machine()} python {platform.python_version()} torch {torch.__version__}"
 
 
-def _stale() -> bool:
-    if not all(os.path.exists(p) for p in (LIB, BINDING, STAMP)):
+def _stale(target: str, stamp: str, built_for: str, deps: list) -> bool:
+    if not os.path.exists(target) or not os.path.exists(stamp):
         return True
-    with open(STAMP) as f:
-        if f.read().strip() != _built_for():
+    with open(stamp) as f:
+        if f.read().strip() != built_for:
             return True
-    lib_t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    deps = [os.path.join(CSRC, s) for s in SOURCES] + HEADERS + [BINDING_SOURCE]
+    made = os.path.getmtime(target)
+    return any(os.path.getmtime(d) > made for d in deps)
+
+
+def _library_stale() -> bool:
+    deps = [os.path.join(CSRC, s) for s in SOURCES] + HEADERS
     deps += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    return any(os.path.getmtime(d) > lib_t for d in deps)
+    return _stale(LIB, STAMP, platform.machine(), deps)
+
+
+def _binding_stale() -> bool:
+    return _stale(BINDING, BINDING_STAMP, _built_for(), [BINDING_SOURCE] + HEADERS)
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -115,13 +126,8 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Build (if needed) and return the path of libpagedattn.so."""
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+def _build_library(verbose: bool) -> None:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH
@@ -129,9 +135,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding.result())
     with open(STAMP, "w") as f:
-        f.write(_built_for())
+        f.write(platform.machine())
+
+
+def _compile_stale_binding(force: bool):
+    """The binding's object where it has to be linked anew, else None."""
+    return _compile_binding() if force or _binding_stale() else None
+
+
+def build(force: bool = False, verbose: bool = False, need_binding: bool = False) -> str:
+    """Build (if needed) and return the path of libpagedattn.so.  Without a binding there is a
+    warning, or with need_binding an error, once the library is made."""
+    os.makedirs(BUILD, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_compile_stale_binding, force)
+        if force or _library_stale():
+            _build_library(verbose)
+    try:
+        obj = binding.result()
+        if obj:
+            _link_binding(obj)
+            with open(BINDING_STAMP, "w") as f:
+                f.write(_built_for())
+    except Exception as e:                   # a tool or a header that is not there
+        for p in (BINDING, BINDING_STAMP):   # nor one that was built for others
+            if os.path.exists(p):
+                os.remove(p)
+        if need_binding:
+            raise
+        warnings.warn(f"libpagedattn.so is built, its Python binding is not (pa_rope_append and "
+                      f"the 8-bit cache's calls need it): {e}", RuntimeWarning)
     return LIB
 
 
