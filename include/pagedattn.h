@@ -484,9 +484,9 @@ pa_status pa_rope_append_q8(void* q_out, void* k_pool, void* v_pool, float* k_sc
  * aligned, contents arbitrary, not shared by calls that overlap on the GPU.
  * Supported: fp16 / bf16, head_dim 64 or 128, block_size 8/16/32/64, num_q_heads a
  * multiple of num_kv_heads.  With n = max_seq_len in tiles of 128 tokens (256 at
- * head_dim 64) and c = ceil(num_q_heads / num_kv_heads / 8): num_seqs * n < 2^28,
- * 4 (n + 1) * num_kv_heads * c < 2^31, num_kv_heads * c < 2^20, and a pool of less than
- * 2^38 bytes.
+ * head_dim 64) and c = ceil(num_q_heads / num_kv_heads / 8): max_seq_len <= 2^31 - 2048,
+ * num_seqs * n < 2^28, 4 (n + 1) * num_kv_heads * c < 2^31, num_kv_heads * c < 2^20, and a
+ * pool of less than 2^38 bytes.
  */
 size_t pa_decode_q8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                     int block_size, int max_seq_len);

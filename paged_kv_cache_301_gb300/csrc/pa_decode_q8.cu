@@ -1321,11 +1321,13 @@ extern "C" pa_status pa_decode_q8(void* out, const void* q, const void* k_pool, 
   const Plan p = plan_of(num_q_heads, num_kv_heads, head_dim, max_seq_len);
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.total)
     return PA_ERR_WORKSPACE;
-  // 32-bit rows, tiles of all sequences, and cost of one sequence's items (4 a tile and at
-  // most 4 an item, which the kernel takes apart in 32 bits)
+  // 32-bit rows, tiles of all sequences, positions up to a tile of blocks behind the end, and
+  // cost of one sequence's items (4 a tile and at most 4 an item, which the kernel takes
+  // apart in 32 bits)
   const int block_rows = block_size * head_dim / 128;
   const long long rows = (long long)num_blocks * num_kv_heads * block_rows;
-  if (rows >= (1ll << 31) || (long long)num_seqs * p.tiles >= (1ll << 28) ||
+  if (rows >= (1ll << 31) || max_seq_len > 0x7FFFFFFF - 2047 ||
+      (long long)num_seqs * p.tiles >= (1ll << 28) ||
       (long long)num_kv_heads * p.chunks >= (1ll << 20) ||
       4 * (p.tiles + 1) * num_kv_heads * p.chunks >= (1ll << 31))
     return PA_ERR_INVALID_ARG;

@@ -19,6 +19,9 @@ def lib():
     dict(mx=1 << 30, H=1, Hq=512, bs=64, MB=1 << 24),            # of 64 chunks of one head
     dict(mx=1 << 30, H=128, Hq=128, D=64, bs=64, MB=1 << 24),    # 2^22 tiles of 128 heads
     dict(mx=(1 << 31) - 128, H=32, Hq=32, bs=64, MB=1 << 25),
+    # a length rounded up to tiles, and a block's place in a tile, are ints
+    dict(mx=(1 << 31) - 1, bs=64, MB=1 << 25),
+    dict(mx=(1 << 31) - 2047, H=1, Hq=1, D=64, bs=64, MB=1 << 25),
     # what was refused before
     dict(mx=1 << 30, B=32, bs=64, MB=1 << 24),                   # tiles of all sequences
     dict(H=1 << 20, Hq=1 << 20),                                 # items of a sequence
