@@ -28,7 +28,7 @@
 //
 // Work: the tiles of all (sequence, KV head, head chunk) items in a row, cut into
 // windows of equal cost, one per CTA (two CTAs per SM); an item costs its tiles and
-// something for its beginning and end.  An item that a window boundary cuts leaves
+// something for its beginning and end (pa_q8_window.cuh).  An item that a window boundary cuts leaves
 // partial (m, l, acc) in the workspace; the join kernel takes them together:
 // M = max m, out = sum acc 2^(m - M) / sum l 2^(m - M).
 //
@@ -56,6 +56,7 @@
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_q8.cuh"
+#include "pa_q8_window.cuh"
 #include "pa_sm100.cuh"
 
 namespace pa {
@@ -69,13 +70,6 @@ constexpr int kStageBytes = kTileRows * 128;
 constexpr int kMaxGrid = 320;                  // CTAs at most (two per SM)
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr unsigned kAll = 0xFFFFFFFFu;
-
-// Where a CTA's window begins: sequence, item of it, tile; tiles in the window; where
-// that item's final tile begins; the cost of all items (both in units of cost).
-struct alignas(16) Window {
-  int b, item, j, tiles;
-  int64_t final, total;
-};
 
 struct Q8Args {
   void* out;
@@ -452,85 +446,38 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
     all_tiles += sum.x;
     all_seqs += sum.y;
   }
-  const int64_t work = (int64_t)all_tiles * items;
-  const int64_t ctas = work < (int64_t)gridDim.x ? work : (int64_t)gridDim.x;
-  const bool in = (int64_t)blockIdx.x < ctas;
-  // every window holds a tile: the cost of an item's ends counts only where windows are
-  // longer than it
-  int ends_cost = item_cost<D, GP>();
-  int64_t total = (4 * (int64_t)all_tiles + ends_cost * all_seqs) * items;
-  if (total < ctas * 2 * (4 + ends_cost)) {
-    ends_cost = 0;
-    total = 4 * work;
-  }
-  if (in && ctas == work) {                     // a tile each: the shortest way, latency counts
-    const int w = (int)blockIdx.x, t = w / items;
-    if (tiles_to <= t && t < tiles_to + tiles) {
-      int b = b0, tile = tiles_to, len = 0, nt = 0;
-      for (;; ++b) {
-        len = clamp_len(a, b);
-        nt = (len + TOKENS - 1) / TOKENS;
-        if (t < tile + nt) break;
-        tile += nt;
-      }
-      const int at = w - tile * items, item = at / nt;
-      tail->start[0] = b;
-      tail->start[1] = item;
-      tail->start[2] = at - item * nt;
-      tail->start[3] = len;
-      tail->lin[0] = w;
-      tail->lin[1] = w + 1;
-      tail->final = 4 * (int64_t)(tile * items + item * nt + nt - 1);
+  const Cut cut = cut_of(all_tiles, all_seqs, items, (int)gridDim.x, item_cost<D, GP>());
+  const Share share = {b0, b1, tiles, seqs, tiles_to, seqs_to};
+  const bool in = (int64_t)blockIdx.x < cut.ctas;
+  auto len_of = [&](int b) { return clamp_len(a, b); };
+  if (in && cut.ctas == cut.work) {             // a tile each: the shortest way, latency counts
+    TilePlace p;
+    if (place_of_tile<TOKENS>(share, items, (int)blockIdx.x, len_of, &p)) {
+      tail->start[0] = p.b;
+      tail->start[1] = p.item;
+      tail->start[2] = p.j;
+      tail->start[3] = p.len;
+      tail->lin[0] = p.lin;
+      tail->lin[1] = p.lin + 1;
+      tail->final = p.final;
     }
   } else if (in) {
-    const int before = 4 * tiles_to + ends_cost * seqs_to;      // of one item of each
-    const int mine = 4 * tiles + ends_cost * seqs;
 #pragma unroll 1
     for (int end = 0; end < 2; ++end) {
-      // 64-bit division takes half a microsecond; most batches fit 32 bits
-      const bool narrow = total < (1 << 22);
-      const int64_t w = narrow ? (int64_t)((uint32_t)total * (blockIdx.x + end) / (uint32_t)ctas)
-                               : total * (blockIdx.x + end) / ctas;
-      const int t = narrow ? (int)((uint32_t)w / (uint32_t)items) : (int)(w / items);
-      if (w == total) {
-        if (tid == 0) tail->lin[end] = work;
+      const Bound w = bound_of(cut, items, blockIdx.x + end);
+      if (w.at == cut.total) {
+        if (tid == 0) tail->lin[end] = cut.work;
         continue;
       }
-      if (t < before || t >= before + mine) continue;
-      int b = b0, cost = before, tile = tiles_to, nt = 0, len = 0;
-      for (;; ++b) {
-        len = clamp_len(a, b);
-        nt = (len + TOKENS - 1) / TOKENS;
-        const int c = nt ? 4 * nt + ends_cost : 0;
-        if (t < cost + c || b + 1 >= b1) break;
-        cost += c;
-        tile += nt;
-      }
-      // tile 0 of an item begins at 0, tile j at 4 j + ends_cost: the first one from w on
-      const int c = 4 * nt + ends_cost;
-      const int at = (int)(w - (int64_t)cost * items);
-      int item = at / c;
-      const int r = at - item * c;
-      int j = r == 0 ? 0 : max(1, (r - ends_cost + 3) >> 2);
-      tail->lin[end] = (int64_t)tile * items + (int64_t)item * nt + j;
+      TilePlace p;
+      if (!place_of_cost<TOKENS>(cut, share, a.B, items, w, end == 0, len_of, &p)) continue;
+      tail->lin[end] = p.lin;
       if (end == 0) {
-        int64_t base = (int64_t)cost * items + (int64_t)item * c;
-        if (j >= nt) {                          // the next item, maybe of a later sequence
-          j = 0;
-          base += c;
-          if (++item == items) {
-            item = 0;
-            do {
-              len = ++b < a.B ? clamp_len(a, b) : 0;
-              nt = (len + TOKENS - 1) / TOKENS;
-            } while (nt == 0 && b < a.B);
-          }
-        }
-        tail->start[0] = b;
-        tail->start[1] = item;
-        tail->start[2] = j;
-        tail->start[3] = len;
-        tail->final = base + (nt > 1 ? 4 * (nt - 1) + ends_cost : 0);
+        tail->start[0] = p.b;
+        tail->start[1] = p.item;
+        tail->start[2] = p.j;
+        tail->start[3] = p.len;
+        tail->final = p.final;
       }
     }
   } else if (tid < 4) {
@@ -547,7 +494,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
   walk.L = tail->start[3];
   walk.nt = (walk.L + TOKENS - 1) / TOKENS;
   if (tid == 0)
-    a.info[blockIdx.x] = Window{walk.b, tail->start[1], walk.j, walk.left, tail->final, total};
+    a.info[blockIdx.x] = Window{walk.b, tail->start[1], walk.j, walk.left, tail->final,
+                                cut.total};
   const uint32_t tmem = tail->tmem;
   const uint32_t ring = smem_addr(smem), qb = smem_addr(smem + S::kQOff),
                  pb = smem_addr(smem + S::kPOff);
@@ -1059,13 +1007,6 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k,
 constexpr int kJoinThreads = 512;
 constexpr int kPartsAhead = 4;                 // parts of a group asked for at once
 
-// Does boundary c cut an item for the first time?
-__device__ __forceinline__ bool first_cut(const Window& at, const Window& before, bool* same) {
-  *same = before.b == at.b && before.item == at.item;
-  // not an empty window, not a boundary between items, no earlier boundary in this item
-  return at.tiles > 0 && at.j > 0 && !(*same && before.j > 0);
-}
-
 template <int D, int kJoinHeads, bool kByItem>
 __global__ void __launch_bounds__(kJoinThreads, 2) join_q8_kernel(const Q8Args a, int grid) {
   constexpr int GROUPS = kJoinThreads / D;
@@ -1104,17 +1045,12 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_q8_kernel(const Q8Args a
     at = a.info[c];
     if (!first_cut(at, a.info[c - 1], &same)) return;
   }
-  // the parts: the segment of window c - 1 that ends there, then the first segments of
-  // windows c .. last, last holding the item's final tile
-  const int64_t windows = at.total / 4 < grid ? at.total / 4 : grid;   // fewer: of a tile each
-  const int last = (int)min(((at.final + 1) * windows - 1) / at.total, windows - 1);
-  const int parts = last - c + 2;
+  const int parts = last_window(at, grid) - c + 2;
   const int h = at.item / a.chunks, G = a.Hq / a.H;
   const int g0 = (at.item - h * a.chunks) * a.hch + h0;
   const int n = min(kJoinHeads, min(a.hch - h0, G - g0));
   if (n <= 0) return;                          // a last chunk of fewer heads
-  const int64_t head = 2 * (int64_t)(c - 1) + (same ? 0 : 1);
-  auto row = [&](int k) { return (k == 0 ? head : 2 * (int64_t)(c + k - 1)) * a.hch + h0; };
+  auto row = [&](int k) { return part_of_item(c, same, k) * a.hch + h0; };
   const int d = threadIdx.x % D, group = threadIdx.x / D;
   float x[kJoinAhead][kJoinHeads];
 #pragma unroll
