@@ -476,10 +476,14 @@ pa_status pa_rope_append_q8(void* q_out, void* k_pool, void* v_pool, float* k_sc
 
 /*
  * pa_decode over the 8-bit cache: the same result definition over
- * K = code * k_scale, V = code * v_scale, fp32 softmax and sums; out and q
- * [num_seqs, num_q_heads, head_dim] fp16 or bf16.  max_seq_len, scale, bad lengths
- * and empty sequences as in pa_decode; a bad block id's keys and values read as
- * zeros (reported in checked mode).  workspace: at least
+ * K = code * k_scale, V = code * v_scale, fp32 scores, softmax statistics and sums; out
+ * and q [num_seqs, num_q_heads, head_dim] fp16 or bf16.  What enters the products:
+ *   - q exactly where an element is at least 2^-17 (bf16; fp16 2^-14) of its row's largest
+ *     magnitude; a smaller one to 2^-25 of that magnitude, or 2^-82 if that is more;
+ *   - w = softmax weight * v_scale of its block to 2^-13.6 of itself, or to 2^-25 of the
+ *     largest w among the 128 tokens (256 at head_dim 64) of its tile where that is more.
+ * max_seq_len, scale, bad lengths and empty sequences as in pa_decode; a bad block id's
+ * keys and values read as zeros (reported in checked mode).  workspace: at least
  * pa_decode_q8_workspace_bytes(...) bytes (0 for invalid arguments), 256-byte
  * aligned, contents arbitrary, not shared by calls that overlap on the GPU.
  * Supported: fp16 / bf16, head_dim 64 or 128, block_size 8/16/32/64, num_q_heads a

@@ -8,7 +8,10 @@
 // the codes go from HBM to shared memory to the tensor cores as they are, and
 // everything 16- or 32-bit is brought to them:
 //   - q is split into three e4m3 digits of four bits, q = s (d0 + d1/16 + d2/256)
-//     with s a power of two: 12 bits, which is all of bf16's 8 and fp16's 11;
+//     with s the power of two that brings the row's largest |q| to (224, 448].  The last
+//     digit's steps are 2^-17 s: all of bf16's 8 bits of an element from 2^-10 s on (2^-17
+//     of the largest), all of fp16's 11 from 2^-7 s on (2^-14 of it); what is smaller is off
+//     by 2^-18 s, under 2^-25 of the largest;
 //   - the softmax weights, times the block's V scale, in units of their own largest
 //     in the tile (of each head, a power of two), are split the same way: each is off by
 //     2^-13.6 of itself (a single digit would be off by 2^-4), or 2^-25 of the largest

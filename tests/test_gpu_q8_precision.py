@@ -1,15 +1,18 @@
 """How exact the 8-bit cache's decode attention is where its digits could lose something:
-weights of any size, blocks of one sequence whose V scales are far apart, against the
-definition in fp64.
+weights of any size, blocks of one sequence whose V scales are far apart, a q with one
+large channel, against the definition in fp64.
 
 Bounds, for one query head, with p the softmax weights, w_t = p_t (V scale of t's block),
 A = sum_t p_t |V_t| and C = sum_t |code of V_t| per output element, U = max_t w_t, and
 S = max_t scale sum_d |q_d K_td|:
   - scores: at most 3 x 128 products summed in fp32, 384 * 2^-24 S = 2^-15.4 S in natural
-    units; a weight is off by twice that (itself and the normaliser);
+    units; with a score off by x, weight and normaliser are off by a factor of e^(2x);
   - weights: three e4m3 digits of an fp32 number, 2^-14 of each (four bits of it, then five
     and five of what is left), of which the last two may go by fp16, whose half step is
     2^-12 of at most 2^-4 of it: 2^-13.6 in all;
+  - q: its digits' last steps are 2^-17 where the row's largest |q| is between 224 and 448,
+    so an element is exact where its own last bit is 2^-17 or more, and off by 2^-18 / 224 =
+    2^-25.8 of the largest otherwise (only where a test has such elements);
   - the last digit's steps are 2^-17 where the tile's largest w is between 128 and 256, so
     half a step is at most 2^-25 U of a w, and that many codes: 2^-25 U C;
   - exponentials, products and sums in fp32: taken as 2^-16 A;
@@ -31,7 +34,7 @@ def pa():
     return lib()
 
 
-def check(b, out):
+def check(b, out, inexact_q=False):
     """`out` against fp64 attention over b's codes and scales, within the bounds above."""
     half = torch.finfo(b.dt).eps / 2
     tiny = float(torch.finfo(b.dt).smallest_normal) * half
@@ -52,7 +55,10 @@ def check(b, out):
             scale_v = b.scales[1][blk, h].astype(np.float64)
             a = p @ np.abs(v)
             c = (np.abs(v) / scale_v[:, None]).sum(0)
-            e = (WEIGHT + 2.0 ** -14.4 * size + 2.0 ** -16) * a + 2.0 ** -25 * (p * scale_v).max() * c
+            off = 2.0 ** -15.4 * size                     # of a score
+            if inexact_q:
+                off += b.scale * 2.0 ** -25.8 * np.abs(q[i, hq]).max() * np.abs(k).sum(1).max()
+            e = (WEIGHT + np.expm1(2 * off) + 2.0 ** -16) * a + 2.0 ** -25 * (p * scale_v).max() * c
             ref = p @ v
             bad = ~(np.abs(got[i, hq] - ref) <= half * (np.abs(ref) + e) + e + tiny)
             assert not bad.any(), (i, hq, int(bad.sum()), np.abs(got[i, hq] - ref).max(), ref[bad][:3])
@@ -145,3 +151,24 @@ def test_a_tile_far_below_the_running_maximum(pa, D, G, by):
     out = b.run(pa)
     assert torch.isfinite(out).all()
     check(b, out)
+
+
+@pytest.mark.parametrize("dt,large,exact", [("bf16", 2 ** 7, True), ("bf16", 2 ** 16, True),
+                                            ("bf16", 2 ** 20, False), ("bf16", 2 ** 24, False),
+                                            ("fp16", 2 ** 7, True), ("fp16", 2 ** 13, True),
+                                            ("fp16", 2 ** 15, False)])
+@pytest.mark.parametrize("D,G", [(128, 1), (128, 4), (64, 8)])
+def test_one_large_channel_of_q(pa, D, G, dt, large, exact):
+    """One channel of q is large and K is zero there: the others, from 1/2 to 2 in size, decide
+    the scores."""
+    b = Batch([1, 100, 300], G, 2, D, 16, dt, seed=D + G)
+    g = np.random.default_rng(G)
+    q = g.uniform(0.5, 2, size=b.q.shape) * g.choice([-1, 1], size=b.q.shape)
+    q[..., 7] = large
+    b.q.copy_(torch.from_numpy(q))
+    for i, n in enumerate(b.lens):
+        blk = b.tables[i, :-(-n // 16)]
+        b.codes[0][blk, :, :, 7] = 0
+        b.scales[0][blk] = 2.0 ** -8
+    put(b)
+    check(b, b.run(pa), inexact_q=not exact)
