@@ -42,10 +42,11 @@
 // drained, TMEM is freed and PA_ERR_TIMEOUT is reported through status_dev.
 //
 // Measured (GB300, 8 KV heads of 128, graph of calls; of a plain copy's bandwidth):
-//   8 sequences of 32,768..131,072, 8 query heads each: 203 us, 6.62 TB/s, 0.99
-//   2,048 sequences of 16..1,024, 4 heads: 346-350 us, 6.37 TB/s, 0.95
-//   64 sequences of 128..4,096, 4 heads: 50.5 us, 5.5 TB/s, 0.82
-//   one sequence of 50,001, 5 heads: 27.4 us, 3.74 TB/s, 0.56
+//   8 sequences of 32,768..131,072, 8 query heads each: 204-207 us, 6.5 TB/s, 0.98
+//   2,048 sequences of 16..1,024, 4 heads: 349-351 us, 6.33 TB/s, 0.95
+//   64 sequences of 128..4,096, 4 heads: 50.3-50.9 us, 5.5 TB/s, 0.82; 8 heads 55.6,
+//     16 heads 96, 4 heads of 64 36, 8 heads of 64 46
+//   one sequence of 50,001, 5 heads: 27.4 us, 3.73 TB/s, 0.56
 //   4 sequences of at most 64, 4 heads of 64: 4.8-5.5 us
 // About 9 us of a call do not shrink with its bytes: lengths -> window -> block ids ->
 // first tile 4 us, last tile and partials 2 us, join 2.7 us.  With 16 heads to a KV head
@@ -1147,8 +1148,9 @@ struct Plan {
 };
 
 // Chunks of at most 8 query heads, of equal size: a softmax thread keeps a score, a sum
-// and an accumulator per head, and two CTAs of an SM leave it 146 registers.  So the
-// cache is read twice with 16 heads: 94 us where 8 take 55 (64 sequences of 128..4,096).
+// and an accumulator per head, and two CTAs of an SM leave it 128 registers (seven warps are
+// allotted as eight), all of them in use for 5 and 8 heads and from 4 heads of 64 on.  So the
+// cache is read twice with 16 heads: 96 us where 8 take 56 (64 sequences of 128..4,096).
 Plan plan_of(int Hq, int H, int D, int max_seq_len) {
   Plan p;
   const int G = Hq / H, most = 8;

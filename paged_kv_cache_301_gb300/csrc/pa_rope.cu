@@ -15,9 +15,10 @@
 // rotation stays inside a lane and only the norm's sum is shuffled.
 //
 // Measured (GB300, 32 query and 8 KV heads of 128, graph of calls): decode step of 64
-// sequences with norms 3.2-3.5 us; prompts of 18,432 tokens 75.4 us, 6.04 TB/s, 0.90 of
-// a plain copy (the register kernel alone: 102 us); into the 8-bit cache: 256 sequences
-// 3.5-4.1 us, 18,432 tokens with norms 81 us, 5.1 TB/s.
+// sequences with norms 3.2-3.5 us; prompts of 18,432 tokens 75.0 us, 6.07 TB/s, 0.91 of
+// a plain copy (the register kernel alone: 102 us), with norms 80.5; into the 8-bit cache:
+// 18,432 tokens 73 us, with norms 81; a step of 256 sequences 3.3-4.1 us while no older
+// block's scale rises, and more where one does (rope_step_q8_kernel).
 #include <mutex>
 
 #include "pa_common.cuh"
@@ -564,6 +565,7 @@ __device__ __forceinline__ void stream_rows(const RopeArgs& a, int cta, int ctas
   }
 }
 
+// Three CTAs of an SM leave a thread 80 registers: 8 bytes (bf16) or 40 (fp16) of it spill.
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads, 3)
 rope_append_kernel(const RopeArgs a) {
@@ -666,8 +668,8 @@ struct NewRows {
 // their way to shared memory meanwhile, each thread's elements to a place of its own (no
 // barrier, only its own copies to wait for); a block's angles are read once for all its
 // heads.  18,432 tokens: 82 us, with the next item's rows in registers 93.  What bounds
-// it: an item's chain of maxima over the CTA, scale, codes, with two CTAs of an SM (the
-// registers of a row); a third CTA spills.
+// it in this form: an item's chain of maxima over the CTA, scale, codes, with two CTAs of an
+// SM (the registers of a row); a third CTA spills.
 template <int DT, int D, int BS>
 __device__ __forceinline__ void store_run(const RopeArgs& a, int t0, int n, int part, int parts,
                                           uint8_t* smem) {
@@ -870,8 +872,12 @@ rope_append_q8_kernel(const RopeArgs a, int kv_ctas, int groups, int run, int st
 // A decode step: one new token per sequence.  CTAs [0, kv_ctas): each group of
 // D/16 lanes takes the K or the V row of one (sequence, KV head); the others hold
 // one token's query rows.  Bound by the chain length -> block id -> old scale, which the
-// row's load and norm overlap; a block's older rows are touched only when its scale
-// rises (256 sequences, 32 / 8 heads: 3.5-4.1 us, 1.4-1.7 TB/s).
+// row's load and norm overlap (256 sequences, 32 / 8 heads: 3.3-4.1 us, 1.4-1.7 TB/s).
+// A block's older rows are touched only when its scale rises; its group then reads, converts
+// and stores them row after row, and the step lasts as long as its slowest group.  256
+// sequences, 2,048 scales each of K and V, of which 2.5% rise (normal rows in blocks of 16
+// raise 2.2% of them): 8.8 us with 7 older rows, 15.4 with 15, 27 with 63 in blocks of 64;
+// where all rise 11, 19.5 and 66.
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads)
 rope_step_q8_kernel(const RopeArgs a, int kv_ctas) {
