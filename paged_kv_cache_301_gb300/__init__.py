@@ -52,13 +52,15 @@ def _stream(stream) -> int:
 
 
 def _bytes_on(n: int, device, stream) -> torch.Tensor:
-    """n bytes for a call on `stream` (as _stream takes it), allocated under that stream: the
-    caching allocator hands them out again in its order, whatever becomes of the tensor.
-    Under another stream it could do so while the call still uses them."""
+    """n bytes for a call on `stream` (a stream, a handle, or what holds one as cuda_stream),
+    allocated under that stream: the caching allocator hands them out again in its order,
+    whatever becomes of the tensor.  Under another stream it could do so while the call
+    still uses them."""
     if stream is None:
         return torch.empty(n, dtype=torch.uint8, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        handle = int(stream)                       # 1 is the legacy default stream, as 0 is
+        handle = int(getattr(stream, "cuda_stream", stream))
+        # 1 is the legacy default stream, as 0 is
         stream = (torch.cuda.default_stream(device) if handle in (0, 1) else
                   torch.cuda.ExternalStream(handle, device=device))
     with torch.cuda.stream(stream):

@@ -31,7 +31,7 @@ class Recorder:
 
 
 @pytest.mark.parametrize("call", ["pa_decode", "pa_decode_append", "pa_decode_q8"])
-@pytest.mark.parametrize("given", ["none", "stream", "handle", "default handle"])
+@pytest.mark.parametrize("given", ["none", "stream", "handle", "default handle", "wrapper"])
 def test_workspace_is_allocated_under_the_launch_stream(monkeypatch, call, given):
     import paged_kv_cache_301_gb300 as pa
     current, side, default = FakeStream(0x10), FakeStream(0x70), FakeStream(0)
@@ -58,10 +58,13 @@ def test_workspace_is_allocated_under_the_launch_stream(monkeypatch, call, given
         cuda=cuda, empty=empty, uint8=torch.uint8, float16=torch.float16))
     monkeypatch.setattr(pa, "lib", lambda: fake)
     monkeypatch.setattr(pa, "_native", fake)
+    if given == "wrapper" and call != "pa_decode_q8":
+        pytest.skip("the binding alone takes any object with a cuda_stream")
     q, k = torch.zeros(2, 4, 64, dtype=torch.float16), torch.zeros(2, 4, 64, dtype=torch.float16)
     pool = torch.zeros(6, 16, 4, 64, dtype=torch.float16)
     tables, lens = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
-    stream = {"none": None, "stream": side, "handle": 0x70, "default handle": 0}[given]
+    stream = {"none": None, "stream": side, "handle": 0x70, "default handle": 0,
+              "wrapper": types.SimpleNamespace(cuda_stream=0x70)}[given]
     want = {"none": 0x10, "default handle": 0}.get(given, 0x70)
     if call == "pa_decode":
         pa.pa_decode(q, q, pool, pool, tables, lens, 0.1, stream=stream)
