@@ -31,9 +31,9 @@
 //
 // Work: the tiles of all (sequence, KV head, head chunk) items in a row, cut into
 // windows of equal cost, one per CTA (two CTAs per SM); an item costs its tiles and
-// something for its beginning and end (pa_q8_window.cuh).  An item that a window boundary cuts leaves
-// partial (m, l, acc) in the workspace; the join kernel takes them together:
-// M = max m, out = sum acc 2^(m - M) / sum l 2^(m - M).
+// something for its beginning and end (pa_q8_window.cuh).  An item that a window
+// boundary cuts leaves partial (m, l, acc) in the workspace; the join kernel takes them
+// together: M = max m, out = sum acc 2^(m - M) / sum l 2^(m - M).
 //
 // Roles (224 threads): warp 0 block ids and TMA; warp 1 TMEM and MMA issue; warp 2
 // q digits; warps 3-6 softmax and sums, one thread per tile row, then one per
