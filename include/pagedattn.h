@@ -519,6 +519,168 @@ pa_status pa_expand_blocks_q8(void* k_pool, void* v_pool, const void* k_pool8, c
                               cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Drafted trees and the latent cache                                        */
+/* ------------------------------------------------------------------------ */
+/*
+ * The pages have no counterpart to this section: verification of drafted token
+ * trees, and models whose keys and values come from one latent row per token.
+ */
+
+/*
+ * Decode attention for several new tokens per sequence, split over the length:
+ * verification of drafted tokens.  Rows q_start[b] .. q_start[b+1]-1 of q are sequence
+ * b's n_b new tokens, its LAST n_b tokens, already in the cache (pa_rope_append writes
+ * them; its `positions` gives a tree's tokens their depths).  New token i of sequence b
+ * sees every token t < seq_lens[b] - n_b and, of the new ones, those whose bit is set:
+ *   out = softmax_t(scale * q . K[slot_t, h]) . V[slot_t, h]  over the t it sees.
+ *   tree_mask    [total_q, mask_words] int32: bit j % 32 of word j / 32 of row
+ *                q_start[b] + i says whether new token i sees new token j (itself
+ *                included); bits from n_b on are not looked at.  NULL: a chain, new
+ *                token i sees new tokens 0 .. i.
+ *   q_start      [num_seqs + 1] int32 as in pa_prefill, or NULL: one new token per
+ *                sequence (total_q = num_seqs); an empty sequence's row becomes zeros.
+ *   max_q_len    host upper bound of every n_b, at most 32 * mask_words with a mask
+ *   max_seq_len  host upper bound of every seq_len
+ *   out, q       [total_q, num_q_heads, head_dim]
+ * A row that sees nothing (or only scores of -inf) becomes zeros.  What a row does not
+ * see has no part in it: tokens behind the sequence's end may hold infinities or NaN,
+ * and a new token's values only reach the rows that see it, whatever they are.
+ * A sequence with n_b > seq_lens[b], n_b > max_q_len, seq_lens[b] > max_seq_len (or
+ * past its table), or rows outside [0, total_q) is skipped (rows untouched; reported
+ * in checked mode); a bad block id's rows read as zeros (reported).  Rows behind the
+ * last sequence are left alone.
+ * Scores, softmax statistics and sums are fp32.  The softmax weights enter the product
+ * with V as two terms of the storage type (15 bits or more).
+ * workspace: at least pa_decode_tree_workspace_bytes(...) bytes (0 for invalid
+ * arguments), 256-byte aligned, contents arbitrary, not shared by calls that overlap on
+ * the GPU.
+ * Supported: fp16 / bf16, head_dim 64 or 128, block_size 8/16/32/64, num_q_heads a
+ * multiple of num_kv_heads; max_q_len * num_q_heads / num_kv_heads <= 65536,
+ * max_seq_len < 2^30, a pool of less than 2^31 rows.
+ */
+size_t pa_decode_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim,
+                                      int max_q_len);
+pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const void* v_pool,
+                         const int32_t* block_tables, const int32_t* seq_lens,
+                         const int32_t* q_start, const int32_t* tree_mask, int num_seqs,
+                         int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+                         int block_size, int max_blocks, int num_blocks, int max_q_len,
+                         int mask_words, int max_seq_len, float scale, int dtype,
+                         void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                         cudaStream_t stream);
+
+/*
+ * The latent cache: pool [num_blocks, block_size, latent_dim + rope_dim], one row
+ * [c | r] per token, shared by all heads.  c is what keys and values are expanded from,
+ * r the rotated part of every head's key.  Copy-on-write and swaps of its blocks are
+ * pa_copy_blocks_multi / pa_swap_blocks.
+ *
+ * pa_latent_append: the cache write of new tokens (rows q_start[b] .. q_start[b+1]-1, a
+ * sequence's LAST n_b tokens, as in pa_rope_append):
+ *   c = latent * rsqrt(mean(latent^2) + eps) * weight     (weight non-NULL; RMS norm)
+ *   r = key_rope rotated by the token's row of cos_sin    (pairs as in pa_rope_append)
+ * and, with q_rope, every query head's rotated part:
+ *   q_out = q_rope rotated likewise.
+ * fp32 throughout, rounded once to the storage type; without a weight c is a bit copy,
+ * without cos_sin r and q_out are.
+ *   latent       [total_q, latent_dim], token stride latent_token_stride (0 = packed)
+ *   key_rope     [total_q, rope_dim], token stride key_token_stride (0 = packed)
+ *   q_rope       [total_q, num_q_heads, rope_dim] with token and head strides (0 =
+ *                packed), or NULL (num_q_heads is ignored); q_out likewise.  The strides
+ *                let both be parts of wider rows, as [.., latent_dim:] of the absorbed
+ *                query.  q_out may be q_rope itself (same strides), or other columns
+ *                of the same rows; any other overlap with an input is rejected.
+ *   weight       [latent_dim] storage type, nullable
+ *   cos_sin      [max_position, rope_dim] fp32, nullable; positions as in pa_rope_append
+ * Strides are multiples of 8 elements, addresses 16-byte aligned.  q_start, bad
+ * sequences, positions and block ids as in pa_rope_append.
+ * Supported: fp16 / bf16, latent_dim 256 or 512, rope_dim 64, block_size 8/16/32/64.
+ */
+pa_status pa_latent_append(void* pool, const void* latent, const void* key_rope,
+                           const void* weight, float eps, const float* cos_sin, int max_position,
+                           int interleaved, const int32_t* positions, const void* q_rope,
+                           void* q_out, const int32_t* block_tables, const int32_t* seq_lens,
+                           const int32_t* q_start, int num_seqs, int total_q,
+                           int64_t latent_token_stride, int64_t key_token_stride,
+                           int64_t q_token_stride, int64_t q_head_stride,
+                           int64_t q_out_token_stride, int64_t q_out_head_stride,
+                           int num_q_heads, int latent_dim, int rope_dim, int block_size,
+                           int max_blocks, int num_blocks, int dtype, int32_t* status_dev,
+                           cudaStream_t stream);
+
+/*
+ * Rows of the latent cache as one matrix, what the expanding projection of a prompt over
+ * a cached prefix takes: rows kv_start[b] .. kv_start[b+1]-1 of out are tokens
+ * 0 .. n_b - 1 of sequence b.  Bit copies.
+ *   out          [total_kv, latent_dim + rope_dim], token stride out_token_stride (0 =
+ *                packed; a multiple of 8 elements)
+ *   kv_start     [num_seqs + 1] int32, non-decreasing
+ * A sequence with n_b > seq_lens[b], seq_lens[b] past its table, or rows outside [0,
+ * total_kv) is skipped (reported in checked mode); a bad block id's rows become zeros
+ * (reported).  Rows behind the last sequence are left alone.  Supported as
+ * pa_latent_append.
+ */
+pa_status pa_latent_gather(void* out, const void* pool, const int32_t* block_tables,
+                           const int32_t* seq_lens, const int32_t* kv_start, int num_seqs,
+                           int total_kv, int64_t out_token_stride, int latent_dim, int rope_dim,
+                           int block_size, int max_blocks, int num_blocks, int dtype,
+                           int32_t* status_dev, cudaStream_t stream);
+
+/*
+ * Attention in the absorbed form: queries that the key expansion was multiplied into
+ * ([.., latent_dim + rope_dim]) against the cache's rows themselves; values are the rows'
+ * c, so that out ([.., latent_dim]) still has the value expansion before it.
+ *   out = sum_t softmax_t(scale * q . [c_t | r_t]) c_t
+ * over the t that the row sees: one new token per sequence (q_start NULL) or several, a
+ * chain or a tree, all as in pa_decode_tree, with its rules for bad data and rows that
+ * see nothing.
+ * The softmax weights enter the product as two terms of the storage type where a call
+ * has at most 32 columns (max_q_len * num_q_heads), else rounded to it once (bf16 2^-8
+ * of the weight at most, fp16 2^-11): with more columns the second term is no longer
+ * hidden behind the cache's bytes.
+ * Supported: fp16 / bf16, latent_dim 256 or 512, rope_dim 64, block_size 8/16/32/64,
+ * any num_q_heads; max_q_len * num_q_heads <= 65536, max_seq_len < 2^30, a pool of less
+ * than 2^31 rows.
+ */
+size_t pa_latent_decode_workspace_bytes(int num_q_heads, int latent_dim, int rope_dim,
+                                        int max_q_len);
+pa_status pa_latent_decode(void* out, const void* q, const void* pool,
+                           const int32_t* block_tables, const int32_t* seq_lens,
+                           const int32_t* q_start, const int32_t* tree_mask, int num_seqs,
+                           int total_q, int num_q_heads, int latent_dim, int rope_dim,
+                           int block_size, int max_blocks, int num_blocks, int max_q_len,
+                           int mask_words, int max_seq_len, float scale, int dtype,
+                           void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                           cudaStream_t stream);
+
+/*
+ * Attention in the expanded form, for prompts: keys and values of every head stand
+ * expanded in one matrix, the rotated part of the keys is shared.  Causal: sequence b's
+ * queries (rows q_start[b] .. q_start[b+1]-1) are the last n_b of its m_b tokens (rows
+ * kv_start[b] .. kv_start[b+1]-1 of kv and key_rope), and query i sees tokens
+ * 0 .. m_b - n_b + i.  For head h
+ *   out = sum_t softmax_t(scale * (q[:nope] . kv[t, h, :nope] + q[nope:] . key_rope[t]))
+ *               kv[t, h, nope:]
+ *   out          [total_q, num_heads, value_dim], packed
+ *   q            [total_q, num_heads, nope_dim + rope_dim], packed
+ *   kv           [total_kv, num_heads, nope_dim + value_dim], packed: one projection's
+ *                output
+ *   key_rope     [total_kv, rope_dim], token stride key_token_stride (0 = packed; a
+ *                multiple of 8 elements): the last columns of pa_latent_gather's rows
+ *   max_q_len    host upper bound of every n_b
+ * A sequence with n_b > m_b, n_b > max_q_len, or rows outside [0, total_q) or [0,
+ * total_kv) is skipped (rows untouched; reported in checked mode).  Infinities and NaN of
+ * tokens that a row does not see have no part in it.  fp32 sums and statistics; the
+ * softmax weights enter the product rounded to the storage type.
+ * Supported: fp16 / bf16, nope_dim 128, rope_dim 64, value_dim 128.  No workspace.
+ */
+pa_status pa_latent_prefill(void* out, const void* q, const void* kv, const void* key_rope,
+                            const int32_t* q_start, const int32_t* kv_start, int num_seqs,
+                            int total_q, int total_kv, int64_t key_token_stride, int num_heads,
+                            int nope_dim, int rope_dim, int value_dim, int max_q_len, float scale,
+                            int dtype, int32_t* status_dev, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Host block manager                                                        */
 /* ------------------------------------------------------------------------ */
 /*

@@ -3,8 +3,8 @@
 Argument marshalling only: every computation runs in the library's CUDA
 kernels (or, for the block manager, its C++ host code).  Tensors are PyTorch
 tensors used as device buffers; the current CUDA stream is passed through.
-The calls of the 8-bit cache and the rotated writes are marshalled by a compiled
-module (_binding, csrc/pa_binding.cpp), the others by ctypes.
+The calls of the 8-bit cache, the rotated writes, the drafted trees and the latent cache
+are marshalled by a compiled module (_binding, csrc/pa_binding.cpp), the others by ctypes.
 """
 from __future__ import annotations
 
@@ -458,6 +458,148 @@ def pa_expand_blocks_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_pool8: tor
     _check(st, "pa_expand_blocks_q8")
 
 
+def _most_rows(starts: Optional[torch.Tensor], given: Optional[int]) -> int:
+    """max_q_len: as given, else read from q_start (a device sync); 1 without q_start."""
+    if given is not None:
+        return int(given)
+    if starts is None:
+        return 1
+    return max(0, int((starts[1:] - starts[:-1]).max().item())) if starts.numel() > 1 else 0
+
+
+def tree_mask(parents: Sequence[Sequence[int]], device="cuda") -> torch.Tensor:
+    """The tree_mask of drafted trees: parents[b][i] is the drafted token that token i of
+    sequence b hangs on, an earlier one of its sequence, or -1 for the context itself.  Each
+    token sees itself and its ancestors.  [sum of lengths, words] int32."""
+    words = max(1, -(-max((len(p) for p in parents), default=0) // 32))
+    rows = []
+    for sequence in parents:
+        seen = []
+        for i, parent in enumerate(sequence):
+            if not -1 <= parent < i:
+                raise ValueError("a drafted token hangs on an earlier one, or on -1")
+            seen.append((1 << i) | (seen[parent] if parent >= 0 else 0))
+        rows += [[(s >> (32 * w)) & 0xFFFFFFFF for w in range(words)] for s in seen]
+    mask = torch.tensor(rows, dtype=torch.int64).reshape(-1, words)
+    return torch.where(mask >= 1 << 31, mask - (1 << 32), mask).to(torch.int32).to(device)
+
+
+def workspace_for_tree(q: torch.Tensor, k_pool: torch.Tensor, max_q_len: int,
+                       stream=None) -> torch.Tensor:
+    """The workspace of pa_decode_tree for q [T, Hq, D] over k_pool, at most max_q_len new
+    tokens of a sequence, for calls on `stream` (None: the current one).  It depends on
+    neither the sequences nor their lengths."""
+    n = int(lib().pa_decode_tree_workspace_bytes(q.shape[1], k_pool.shape[2], q.shape[2],
+                                                 int(max_q_len)))
+    if n == 0:
+        raise ValueError("invalid decode arguments")
+    return _bytes_on(n, q.device, stream)
+
+
+def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
+                   v_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                   q_start: Optional[torch.Tensor], scale: float,
+                   tree_mask: Optional[torch.Tensor] = None, max_q_len: Optional[int] = None,
+                   max_seq_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Decode attention of each sequence's last n_b tokens, a chain or (tree_mask) a tree,
+    split over the length (see include/pagedattn.h, pa_decode_tree).  max_q_len is read from
+    q_start, with a device sync, when omitted; max_seq_len and workspace as in pa_decode."""
+    most_q = _most_rows(q_start, max_q_len)
+    if max_seq_len is None:
+        max_seq_len = block_tables.shape[1] * k_pool.shape[1]
+    if workspace is None:
+        workspace = workspace_for_tree(q, k_pool, most_q, stream)
+    st = (_native or _bind()).decode_tree(out, q, k_pool, v_pool, block_tables, seq_lens, q_start,
+                                          tree_mask, scale, most_q, max_seq_len, workspace, status,
+                                          stream)
+    _check(st, "pa_decode_tree")
+    return out
+
+
+ROPE_DIM = 64          # of the latent cache
+
+
+def alloc_latent_cache(num_blocks: int, block_size: int, latent_dim: int,
+                       dtype=torch.bfloat16, device="cuda") -> torch.Tensor:
+    """An empty latent cache: [num_blocks, block_size, latent_dim + 64]."""
+    return torch.zeros(num_blocks, block_size, latent_dim + ROPE_DIM, dtype=dtype, device=device)
+
+
+def pa_latent_append(pool: torch.Tensor, latent: torch.Tensor, key_rope: torch.Tensor,
+                     cos_sin: Optional[torch.Tensor], block_tables: torch.Tensor,
+                     seq_lens: torch.Tensor, q_start: Optional[torch.Tensor] = None,
+                     weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     interleaved: bool = False, positions: Optional[torch.Tensor] = None,
+                     q_rope: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Cache write of each sequence's last n_b tokens: latent [T, R] is RMS-normed, key_rope
+    [T, 64] rotated, and with q_rope [T, Hq, 64] the queries' parts go to q_out, rotated (see
+    include/pagedattn.h, pa_latent_append).  latent, key_rope, q_rope and q_out may be parts of
+    wider rows; q_start None: one token per sequence."""
+    st = (_native or _bind()).latent_append(pool, latent, key_rope, cos_sin, block_tables, seq_lens,
+                                            q_start, weight, eps, interleaved, positions, q_rope,
+                                            q_out, status, stream)
+    _check(st, "pa_latent_append")
+
+
+def pa_latent_gather(out: torch.Tensor, pool: torch.Tensor, block_tables: torch.Tensor,
+                     seq_lens: torch.Tensor, kv_start: torch.Tensor,
+                     status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rows of the latent cache, sequence after sequence: rows kv_start[b] .. kv_start[b+1]-1 of
+    out [S, R + 64] are the first tokens of sequence b (see include/pagedattn.h)."""
+    st = (_native or _bind()).latent_gather(out, pool, block_tables, seq_lens, kv_start, ROPE_DIM,
+                                            status, stream)
+    _check(st, "pa_latent_gather")
+    return out
+
+
+def workspace_for_latent(out: torch.Tensor, pool: torch.Tensor, max_q_len: int = 1,
+                         stream=None) -> torch.Tensor:
+    """The workspace of pa_latent_decode for out [T, Hq, R] over pool, at most max_q_len new
+    tokens of a sequence, for calls on `stream` (None: the current one).  It depends on
+    neither the sequences nor their lengths."""
+    n = int(lib().pa_latent_decode_workspace_bytes(out.shape[1], out.shape[2],
+                                                   pool.shape[2] - out.shape[2], int(max_q_len)))
+    if n == 0:
+        raise ValueError("invalid decode arguments")
+    return _bytes_on(n, out.device, stream)
+
+
+def pa_latent_decode(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                     q_start: Optional[torch.Tensor] = None,
+                     tree_mask: Optional[torch.Tensor] = None, max_q_len: Optional[int] = None,
+                     max_seq_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention in the absorbed form over the latent cache: q [T, Hq, R + 64], out [T, Hq, R],
+    one new token per sequence or (q_start) several, a chain or a tree (see
+    include/pagedattn.h, pa_latent_decode).  Defaults as in pa_decode_tree."""
+    most_q = _most_rows(q_start, max_q_len)
+    if max_seq_len is None:
+        max_seq_len = block_tables.shape[1] * pool.shape[1]
+    if workspace is None:
+        workspace = workspace_for_latent(out, pool, most_q, stream)
+    st = (_native or _bind()).latent_decode(out, q, pool, block_tables, seq_lens, q_start,
+                                            tree_mask, scale, most_q, max_seq_len, workspace,
+                                            status, stream)
+    _check(st, "pa_latent_decode")
+    return out
+
+
+def pa_latent_prefill(out: torch.Tensor, q: torch.Tensor, kv: torch.Tensor,
+                      key_rope: torch.Tensor, q_start: torch.Tensor, kv_start: torch.Tensor,
+                      scale: float, max_q_len: Optional[int] = None,
+                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention in the expanded form: q [T, H, 128 + 64], kv [S, H, 128 + 128] (a head's
+    key part, then its value), key_rope [S, 64] shared by the heads (see include/pagedattn.h,
+    pa_latent_prefill).  max_q_len is read from q_start, with a device sync, when omitted."""
+    st = (_native or _bind()).latent_prefill(out, q, kv, key_rope, q_start, kv_start, scale,
+                                             _most_rows(q_start, max_q_len), status, stream)
+    _check(st, "pa_latent_prefill")
+    return out
+
+
 def pa_stream_read(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, stream=None) -> None:
     """Read every byte of `buf` once (a plain contiguous read stream, see
     include/pagedattn.h, pa_stream_read): the read bandwidth measured beside the
@@ -618,4 +760,7 @@ __all__ = [
     "BlockManager", "lib", "simulate_allocator", "pa_stream_read",
     "pa_rope_append", "pa_rope_append_q8", "pa_decode_q8", "pa_expand_blocks_q8", "rope_table",
     "alloc_cache_q8", "workspace_for_q8",
+    "pa_decode_tree", "workspace_for_tree", "tree_mask", "alloc_latent_cache",
+    "pa_latent_append", "pa_latent_gather", "pa_latent_decode", "pa_latent_prefill",
+    "workspace_for_latent",
 ]

@@ -63,6 +63,19 @@ SIGNATURES = {
     "pa_decode_q8": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_float, c_int, c_void_p, c_size_t,
                                                             c_void_p, c_void_p]),
     "pa_expand_blocks_q8": (c_int, [c_void_p] * 7 + [c_int] * 7 + [c_void_p, c_void_p]),
+    "pa_decode_tree_workspace_bytes": (c_size_t, [c_int] * 4),
+    "pa_decode_tree": (c_int, [c_void_p] * 8 + [c_int] * 11 + [c_float, c_int, c_void_p, c_size_t,
+                                                               c_void_p, c_void_p]),
+    "pa_latent_append": (c_int, [c_void_p] * 4 + [c_float, c_void_p, c_int, c_int] +
+                         [c_void_p] * 6 + [c_int] * 2 + [c_int64] * 6 + [c_int] * 7 +
+                         [c_void_p, c_void_p]),
+    "pa_latent_gather": (c_int, [c_void_p] * 5 + [c_int, c_int, c_int64] + [c_int] * 6 +
+                         [c_void_p, c_void_p]),
+    "pa_latent_decode_workspace_bytes": (c_size_t, [c_int] * 4),
+    "pa_latent_decode": (c_int, [c_void_p] * 7 + [c_int] * 11 + [c_float, c_int, c_void_p, c_size_t,
+                                                                 c_void_p, c_void_p]),
+    "pa_latent_prefill": (c_int, [c_void_p] * 6 + [c_int] * 3 + [c_int64] + [c_int] * 5 +
+                          [c_float, c_int, c_void_p, c_void_p]),
     "pa_stream_read": (c_int, [c_void_p, c_size_t, c_void_p, c_void_p]),
     "pa_decode_slots": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                 c_void_p, c_void_p]),

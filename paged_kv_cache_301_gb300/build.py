@@ -39,6 +39,7 @@ SOURCES = [
     "pa_decode_tcg.cu", "pa_blocks.cu", "pa_prefill_tc.cu", "pa_prefill_simt.cu",
     "pa_stream.cu",
     "pa_rope.cu", "pa_decode_q8.cu", "pa_expand_q8.cu",
+    "pa_latent_cache.cu", "pa_latent_decode.cu", "pa_latent_prefill.cu", "pa_decode_tree.cu",
 ]
 HEADERS = [
     os.path.join(ROOT, "include", "pagedattn.h"),

@@ -1,4 +1,5 @@
-// Python binding of the rotated cache writes and the 8-bit cache.
+// Python binding of the rotated cache writes, the 8-bit cache, the drafted trees and the
+// latent cache.
 //
 // A decode step makes these calls once per layer with about fifteen tensors each.
 // Reading shapes, strides, types, devices and addresses from Python and handing
@@ -250,6 +251,209 @@ long expand_q8(Args a) {
                              a.dtype(kp), ptr_as<int32_t>(status), a.stream(8));
 }
 
+// A count given as a Python int.
+int64_t whole(const Args& a, int i, const char* what) {
+  const int64_t n = PyLong_AsLongLong(a.v[i]);
+  if (PyErr_Occurred()) throw Bad("");
+  a.need(n >= 0 && n <= 0x7FFFFFFF, what);
+  return n;
+}
+
+// Elements from row to row of [T, n] with packed rows (0: packed).
+int64_t row_stride(const Args& a, const Tensor& t) {
+  a.need(t.stride(1) == 1, "the elements of a row must be packed");
+  if (t.size(0) <= 1) return 0;
+  a.need(t.stride(0) >= t.size(1), "rows that share elements are no token rows");
+  return t.stride(0);
+}
+
+// What the attention calls over a cache share: block_tables, seq_lens, q_start, tree_mask of
+// T query rows; the mask's words.
+int check_rows(const Args& a, int64_t T, const Tensor& tables, const Tensor& lens,
+               const Tensor* q_start, const Tensor* mask) {
+  a.need(tables.dim() == 2 && lens.numel() == tables.size(0), "block_tables [B, MB], seq_lens [B]");
+  a.need(q_start ? q_start->numel() == tables.size(0) + 1 : T == tables.size(0),
+         "q_start [B + 1], or None and one row per sequence");
+  a.need(!mask || (mask->dim() == 2 && mask->size(0) == T && mask->size(1) > 0),
+         "tree_mask is [T, words] int32");
+  return mask ? (int)mask->size(1) : 0;
+}
+
+// out, q, k_pool, v_pool, block_tables, seq_lens, q_start, tree_mask, scale, max_q_len,
+// max_seq_len, workspace, status, stream.
+long decode_tree(Args a) {
+  const Tensor& out = *a.packed(0);
+  const Tensor& q = *a.packed(1);
+  const Tensor& k = *a.packed(2);
+  const Tensor& v = *a.packed(3);
+  const Tensor& tables = *a.index(4);
+  const Tensor& lens = *a.index(5);
+  const Tensor* q_start = a.index(6, true);
+  const Tensor* mask = a.index(7, true);
+  const double scale = a.number(8);
+  const Tensor& ws = *a.packed(11);
+  const Tensor* status = a.status(12);
+  const auto dt = q.scalar_type();
+  a.need(q.dim() == 3 && out.sizes() == q.sizes() && out.scalar_type() == dt,
+         "out as q [T, Hq, D]");
+  a.need(k.dim() == 4 && v.sizes() == k.sizes() && k.size(3) == q.size(2) &&
+             k.scalar_type() == dt && v.scalar_type() == dt,
+         "pools are [NB, bs, Hkv, D] of q's dtype");
+  const int words = check_rows(a, q.size(0), tables, lens, q_start, mask);
+  const int most_q = (int)whole(a, 9, "max_q_len does not fit 32 bits");
+  const int most = (int)whole(a, 10, "max_seq_len does not fit 32 bits");
+  a.placed();
+  return pa_decode_tree(ptr(&out), ptr(&q), ptr(&k), ptr(&v), ptr_as<int32_t>(&tables),
+                        ptr_as<int32_t>(&lens), ptr_as<int32_t>(q_start), ptr_as<int32_t>(mask),
+                        (int)tables.size(0), (int)q.size(0), (int)q.size(1), (int)k.size(2),
+                        (int)q.size(2), (int)k.size(1), (int)tables.size(1), (int)k.size(0),
+                        most_q, words, most, (float)scale, a.dtype(q), ptr(&ws),
+                        ws.numel() * ws.element_size(), ptr_as<int32_t>(status), a.stream(13));
+}
+
+// out, q, pool, block_tables, seq_lens, q_start, tree_mask, scale, max_q_len, max_seq_len,
+// workspace, status, stream.
+long latent_decode(Args a) {
+  const Tensor& out = *a.packed(0);
+  const Tensor& q = *a.packed(1);
+  const Tensor& pool = *a.packed(2);
+  const Tensor& tables = *a.index(3);
+  const Tensor& lens = *a.index(4);
+  const Tensor* q_start = a.index(5, true);
+  const Tensor* mask = a.index(6, true);
+  const double scale = a.number(7);
+  const Tensor& ws = *a.packed(10);
+  const Tensor* status = a.status(11);
+  const auto dt = q.scalar_type();
+  a.need(q.dim() == 3 && out.dim() == 3 && out.size(0) == q.size(0) && out.size(1) == q.size(1) &&
+             out.size(2) < q.size(2) && out.scalar_type() == dt,
+         "q [T, Hq, latent + rope], out [T, Hq, latent]");
+  a.need(pool.dim() == 3 && pool.size(2) == q.size(2) && pool.scalar_type() == dt,
+         "the pool is [NB, bs, latent + rope] of q's dtype");
+  const int words = check_rows(a, q.size(0), tables, lens, q_start, mask);
+  const int most_q = (int)whole(a, 8, "max_q_len does not fit 32 bits");
+  const int most = (int)whole(a, 9, "max_seq_len does not fit 32 bits");
+  a.placed();
+  return pa_latent_decode(ptr(&out), ptr(&q), ptr(&pool), ptr_as<int32_t>(&tables),
+                          ptr_as<int32_t>(&lens), ptr_as<int32_t>(q_start), ptr_as<int32_t>(mask),
+                          (int)tables.size(0), (int)q.size(0), (int)q.size(1), (int)out.size(2),
+                          (int)(q.size(2) - out.size(2)), (int)pool.size(1), (int)tables.size(1),
+                          (int)pool.size(0), most_q, words, most, (float)scale, a.dtype(q),
+                          ptr(&ws), ws.numel() * ws.element_size(), ptr_as<int32_t>(status),
+                          a.stream(12));
+}
+
+// pool, latent, key_rope, cos_sin, block_tables, seq_lens, q_start, weight, eps, interleaved,
+// positions, q_rope, q_out, status, stream.
+long latent_append(Args a) {
+  const Tensor& pool = *a.packed(0);
+  const Tensor& x = *a.tensor(1);
+  const Tensor& k = *a.tensor(2);
+  const Tensor* cs = a.packed(3, true);
+  const Tensor& tables = *a.index(4);
+  const Tensor& lens = *a.index(5);
+  const Tensor* q_start = a.index(6, true);
+  const Tensor* w = a.packed(7, true);
+  const double eps = a.number(8);
+  const int interleaved = PyObject_IsTrue(a.v[9]);
+  if (interleaved < 0) throw Bad("");
+  const Tensor* pos = a.index(10, true);
+  const Tensor* q = a.tensor(11, true);
+  const Tensor* out = a.tensor(12, true);
+  const Tensor* status = a.status(13);
+  const auto dt = pool.scalar_type();
+  a.need(x.dim() == 2 && k.dim() == 2 && k.size(0) == x.size(0) && x.scalar_type() == dt &&
+             k.scalar_type() == dt,
+         "latent [T, latent], key_rope [T, rope], of the pool's dtype");
+  const int64_t T = x.size(0), R = x.size(1), P = k.size(1);
+  a.need(pool.dim() == 3 && pool.size(2) == R + P, "the pool is [NB, bs, latent + rope]");
+  a.need(!w || (w->dim() == 1 && w->size(0) == R && w->scalar_type() == dt),
+         "weight is [latent], of the pool's dtype");
+  a.need(!cs || (cs->dim() == 2 && cs->scalar_type() == kFloat && cs->size(1) == P),
+         "cos_sin is fp32 [max_position, rope]");
+  a.need(!q == !out, "q_rope and q_out go together");
+  int64_t qs = 0, qh = 0, os = 0, oh = 0, Hq = 0;
+  if (q) {
+    a.need(q->dim() == 3 && out->sizes() == q->sizes() && q->size(0) == T && q->size(2) == P &&
+               q->scalar_type() == dt && out->scalar_type() == dt,
+           "q_rope and q_out are [T, Hq, rope], of the pool's dtype");
+    Hq = q->size(1);
+    a.need(Hq > 0, "no query heads");
+    for (const Tensor* t : {q, out}) {
+      a.need(t->stride(2) == 1, "the elements of a head must be packed");
+      int64_t& s = t == q ? qs : os;
+      int64_t& h = t == q ? qh : oh;
+      h = Hq > 1 ? t->stride(1) : P;
+      s = T > 1 ? t->stride(0) : Hq * h;
+      a.need(h >= P && s >= (Hq - 1) * h + P, "heads or tokens that share elements");
+    }
+  }
+  a.need(tables.dim() == 2 && lens.numel() == tables.size(0) && (!pos || pos->numel() == T) &&
+             (q_start ? q_start->numel() == tables.size(0) + 1 : T == tables.size(0)),
+         "block_tables [B, MB], seq_lens [B], q_start [B + 1] or one token per sequence, "
+         "positions [T]");
+  const int64_t xs = row_stride(a, x), ks = row_stride(a, k);
+  a.placed();
+  return pa_latent_append(ptr(&pool), ptr(&x), ptr(&k), ptr(w), (float)eps, ptr_as<float>(cs),
+                          cs ? (int)cs->size(0) : 0, interleaved, ptr_as<int32_t>(pos), ptr(q),
+                          ptr(out), ptr_as<int32_t>(&tables), ptr_as<int32_t>(&lens),
+                          ptr_as<int32_t>(q_start), (int)tables.size(0), (int)T, xs, ks, qs, qh,
+                          os, oh, (int)Hq, (int)R, (int)P, (int)pool.size(1), (int)tables.size(1),
+                          (int)pool.size(0), a.dtype(pool), ptr_as<int32_t>(status), a.stream(14));
+}
+
+// out, pool, block_tables, seq_lens, kv_start, rope_dim, status, stream.
+long latent_gather(Args a) {
+  const Tensor& out = *a.tensor(0);
+  const Tensor& pool = *a.packed(1);
+  const Tensor& tables = *a.index(2);
+  const Tensor& lens = *a.index(3);
+  const Tensor& starts = *a.index(4);
+  const int64_t P = whole(a, 5, "rope_dim does not fit 32 bits");
+  const Tensor* status = a.status(6);
+  a.need(pool.dim() == 3 && out.dim() == 2 && out.size(1) == pool.size(2) &&
+             out.scalar_type() == pool.scalar_type() && pool.size(2) > P,
+         "out [S, latent + rope] as the pool's rows [NB, bs, latent + rope]");
+  a.need(tables.dim() == 2 && lens.numel() == tables.size(0) &&
+             starts.numel() == tables.size(0) + 1,
+         "block_tables [B, MB], seq_lens [B], kv_start [B + 1]");
+  const int64_t s = row_stride(a, out);
+  a.placed();
+  return pa_latent_gather(ptr(&out), ptr(&pool), ptr_as<int32_t>(&tables), ptr_as<int32_t>(&lens),
+                          ptr_as<int32_t>(&starts), (int)tables.size(0), (int)out.size(0), s,
+                          (int)(pool.size(2) - P), (int)P, (int)pool.size(1), (int)tables.size(1),
+                          (int)pool.size(0), a.dtype(pool), ptr_as<int32_t>(status), a.stream(7));
+}
+
+// out, q, kv, key_rope, q_start, kv_start, scale, max_q_len, status, stream.
+long latent_prefill(Args a) {
+  const Tensor& out = *a.packed(0);
+  const Tensor& q = *a.packed(1);
+  const Tensor& kv = *a.packed(2);
+  const Tensor& k = *a.tensor(3);
+  const Tensor& qs = *a.index(4);
+  const Tensor& ks = *a.index(5);
+  const double scale = a.number(6);
+  const int most = (int)whole(a, 7, "max_q_len does not fit 32 bits");
+  const Tensor* status = a.status(8);
+  const auto dt = q.scalar_type();
+  a.need(q.dim() == 3 && out.dim() == 3 && kv.dim() == 3 && k.dim() == 2 &&
+             out.size(0) == q.size(0) && out.size(1) == q.size(1) && kv.size(1) == q.size(1) &&
+             k.size(0) == kv.size(0) && out.scalar_type() == dt && kv.scalar_type() == dt &&
+             k.scalar_type() == dt,
+         "out [T, H, value], q [T, H, nope + rope], kv [S, H, nope + value], key_rope [S, rope], "
+         "of one dtype");
+  const int64_t P = k.size(1), N = q.size(2) - P, V = out.size(2);
+  a.need(N > 0 && kv.size(2) == N + V, "kv is [S, H, nope + value]");
+  a.need(qs.numel() >= 1 && ks.numel() == qs.numel(), "q_start and kv_start are [B + 1]");
+  const int64_t stride = row_stride(a, k);
+  a.placed();
+  return pa_latent_prefill(ptr(&out), ptr(&q), ptr(&kv), ptr(&k), ptr_as<int32_t>(&qs),
+                           ptr_as<int32_t>(&ks), (int)qs.numel() - 1, (int)q.size(0),
+                           (int)kv.size(0), stride, (int)q.size(1), (int)N, (int)P, (int)V, most,
+                           (float)scale, a.dtype(q), ptr_as<int32_t>(status), a.stream(9));
+}
+
 template <typename F>
 PyObject* call(const char* where, PyObject* const* v, Py_ssize_t n, Py_ssize_t want, F f) {
   if (n != want) {
@@ -278,12 +482,32 @@ PyObject* py_decode_q8(PyObject*, PyObject* const* v, Py_ssize_t n) {
 PyObject* py_expand_q8(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return call("pa_expand_blocks_q8", v, n, 9, expand_q8);
 }
+PyObject* py_decode_tree(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call("pa_decode_tree", v, n, 14, decode_tree);
+}
+PyObject* py_latent_decode(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call("pa_latent_decode", v, n, 13, latent_decode);
+}
+PyObject* py_latent_append(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call("pa_latent_append", v, n, 15, latent_append);
+}
+PyObject* py_latent_gather(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call("pa_latent_gather", v, n, 8, latent_gather);
+}
+PyObject* py_latent_prefill(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call("pa_latent_prefill", v, n, 10, latent_prefill);
+}
 
 PyMethodDef kMethods[] = {
     {"rope_append", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, nullptr},
     {"rope_append_q8", (PyCFunction)(void (*)(void))py_rope_q8, METH_FASTCALL, nullptr},
     {"decode_q8", (PyCFunction)(void (*)(void))py_decode_q8, METH_FASTCALL, nullptr},
     {"expand_blocks_q8", (PyCFunction)(void (*)(void))py_expand_q8, METH_FASTCALL, nullptr},
+    {"decode_tree", (PyCFunction)(void (*)(void))py_decode_tree, METH_FASTCALL, nullptr},
+    {"latent_decode", (PyCFunction)(void (*)(void))py_latent_decode, METH_FASTCALL, nullptr},
+    {"latent_append", (PyCFunction)(void (*)(void))py_latent_append, METH_FASTCALL, nullptr},
+    {"latent_gather", (PyCFunction)(void (*)(void))py_latent_gather, METH_FASTCALL, nullptr},
+    {"latent_prefill", (PyCFunction)(void (*)(void))py_latent_prefill, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,

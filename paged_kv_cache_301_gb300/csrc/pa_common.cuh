@@ -55,6 +55,23 @@ __device__ __forceinline__ void report(int32_t* status_dev, int code) {
   if (status_dev) atomicCAS(status_dev, 0, code);
 }
 
+// The sequence of token t: the number of sequences that end at or before it
+// (q_start is non-decreasing).  Called by whole warps with a uniform t; every
+// round narrows 32-fold.
+__device__ __forceinline__ int find_seq(const int32_t* q_start, int B, int t, int lane) {
+  int lo = 0, n = B;                 // the answer is in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int j = lo + (lane + 1) * step;          // boundary q_start[j] ends sequence j - 1
+    const bool before = j <= lo + n && q_start[j] <= t;
+    const int k = __popc(__ballot_sync(0xFFFFFFFFu, before));
+    lo += k * step;
+    // the next boundary at lo + step (if in range) is past t
+    n = min(step - 1, n - k * step);
+  }
+  return lo;
+}
+
 // Programmatic dependent launch.  A kernel launched with launch_pdl may be
 // scheduled before the previous kernel in the stream has finished; it calls
 // wait_prior_grid() before touching data that kernel produces (returns at once

@@ -60,23 +60,6 @@ struct Place {
   int b, pos, ok;
 };
 
-// The sequence of token t: the number of sequences that end at or before it
-// (q_start is non-decreasing).  Called by whole warps with a uniform t; every
-// round narrows 32-fold.
-__device__ __forceinline__ int find_seq(const int32_t* q_start, int B, int t, int lane) {
-  int lo = 0, n = B;                 // the answer is in [lo, lo + n]
-  while (n > 0) {
-    const int step = (n + 31) / 32;
-    const int j = lo + (lane + 1) * step;          // boundary q_start[j] ends sequence j - 1
-    const bool before = j <= lo + n && q_start[j] <= t;
-    const int k = __popc(__ballot_sync(kAll, before));
-    lo += k * step;
-    // the next boundary at lo + step (if in range) is past t
-    n = min(step - 1, n - k * step);
-  }
-  return lo;
-}
-
 // Sequence b's token t (host bounds: b in [0, B]).  A sequence whose rows or
 // length do not fit is not written at all; `bad` says to report it.
 __device__ __forceinline__ Place place_of(const RopeArgs& a, int b, int t, bool* bad) {
