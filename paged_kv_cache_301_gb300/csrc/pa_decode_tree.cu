@@ -1,10 +1,21 @@
 // pa_decode_tree: decode attention of several new tokens per sequence, a chain or a tree,
-// over the paged cache.
-#include <math.h>
-
+// over the paged cache (the kernel: pa_multi.cuh).
 #include "pa_common.cuh"
 #include "pa_internal.h"
-#include "pa_rows.cuh"
+#include "pa_multi.cuh"
+
+namespace pa {
+namespace {
+
+// The second term of the weights is free: the cache's bytes and the softmax take longer than
+// both products.
+template <int N>
+using Tree128 = multi::Shape<128, 2, 2, false, N, 2>;
+template <int N>
+using Tree64 = multi::Shape<128, 1, 1, false, N, 2>;
+
+}  // namespace
+}  // namespace pa
 
 using namespace pa;
 
@@ -20,7 +31,8 @@ static pa_status check_tree(int num_q_heads, int num_kv_heads, int head_dim, int
 extern "C" size_t pa_decode_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim,
                                                  int max_q_len) {
   if (check_tree(num_q_heads, num_kv_heads, head_dim, max_q_len) != PA_OK) return 0;
-  return 256;
+  const int64_t most = (int64_t)(max_q_len > 1 ? max_q_len : 1) * (num_q_heads / num_kv_heads);
+  return multi::layout_of(multi::columns_for(most).n, head_dim).total;
 }
 
 extern "C" pa_status pa_decode_tree(void* out, const void* q, const void* k_pool,
@@ -32,45 +44,22 @@ extern "C" pa_status pa_decode_tree(void* out, const void* q, const void* k_pool
                                     int mask_words, int max_seq_len, float scale, int dtype,
                                     void* workspace, size_t workspace_bytes, int32_t* status_dev,
                                     cudaStream_t stream) {
-  const pa_status st = check_tree(num_q_heads, num_kv_heads, head_dim, max_q_len);
+  pa_status st = check_tree(num_q_heads, num_kv_heads, head_dim, max_q_len);
   if (st != PA_OK) return st;
-  if (num_seqs < 0 || total_q < 0 || max_blocks <= 0 || num_blocks <= 0 || max_seq_len < 0 ||
-      max_seq_len >= (1 << 30) || !isfinite(scale) || (!q_start && total_q != num_seqs) ||
-      (tree_mask && (mask_words <= 0 || (int64_t)mask_words * 32 < max_q_len)) ||
-      (int64_t)num_blocks * block_size >= (1ll << 31) ||
-      (int64_t)total_q * num_q_heads >= (1ll << 31))
-    return PA_ERR_INVALID_ARG;
-  if ((block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64) ||
-      (dtype != PA_FLOAT16 && dtype != PA_BFLOAT16))
-    return PA_ERR_UNSUPPORTED;
-  if (num_seqs == 0 || total_q == 0) return PA_OK;
-  if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens) return PA_ERR_INVALID_ARG;
-  if ((((uintptr_t)out | (uintptr_t)q | (uintptr_t)k_pool | (uintptr_t)v_pool) & 15u) != 0)
-    return PA_ERR_INVALID_ARG;
-  if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < pa_decode_tree_workspace_bytes(num_q_heads, num_kv_heads, head_dim, max_q_len))
-    return PA_ERR_WORKSPACE;
-  RowsArgs a = {};
-  a.out = out;
-  a.q = q;
-  a.k = k_pool;
-  a.v = v_pool;
-  a.tables = block_tables;
-  a.lens = seq_lens;
-  a.q_start = q_start;
-  a.mask = tree_mask;
-  a.B = num_seqs;
-  a.total_q = total_q;
-  a.Hq = num_q_heads;
-  a.H = num_kv_heads;
-  a.bs = block_size;
-  a.max_blocks = max_blocks;
-  a.num_blocks = num_blocks;
-  a.max_q = q_start ? max_q_len : 1;
-  a.words = mask_words;
-  a.max_len = max_seq_len;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  a.status_dev = status_dev;
-  const cudaError_t e = head_dim == 128 ? launch_rows<128, 128, kRowsTree>(a, dtype, stream)
-                                        : launch_rows<64, 64, kRowsTree>(a, dtype, stream);
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const multi::Call c = {out, q, k_pool, v_pool, block_tables, seq_lens, q_start, tree_mask,
+                         num_seqs, total_q, num_q_heads, num_kv_heads, block_size, max_blocks,
+                         num_blocks, max_q_len, mask_words, max_seq_len, scale, dtype, workspace,
+                         workspace_bytes, status_dev, stream};
+  bool work;
+  st = multi::check(c, pa_decode_tree_workspace_bytes(num_q_heads, num_kv_heads, head_dim,
+                                                      max_q_len), &work);
+  if (st != PA_OK || !work) return st;
+  return multi::run(c, 128, head_dim, head_dim / 64, true, [&](int n, auto&&... x) {
+    if (head_dim == 128)
+      return dtype == PA_BFLOAT16
+                 ? multi::launch_columns<Tree128, PA_BFLOAT16>(n, x..., stream)
+                 : multi::launch_columns<Tree128, PA_FLOAT16>(n, x..., stream);
+    return dtype == PA_BFLOAT16 ? multi::launch_columns<Tree64, PA_BFLOAT16>(n, x..., stream)
+                                : multi::launch_columns<Tree64, PA_FLOAT16>(n, x..., stream);
+  });
 }

@@ -1,0 +1,1195 @@
+// Attention of several new tokens per sequence over a paged cache, split over the length, on
+// the Blackwell tensor cores (tcgen05 + TMEM) with TMA loads: pa_decode_tree (K and V per
+// head) and pa_latent_decode (one row per token, whose first part is the value too).
+//
+//   out = sum_t p_t V_t / sum_t p_t,   p_t = 2^(s_t - m),   s_t = log2(e) scale q . K_t
+//
+// over the tokens t that a query token sees: all older ones, and the new ones of its set.
+//
+// The cache rows are the M side of both products and the columns are (new token, query head)
+// pairs of one KV head, so that a tile of the cache is read once for up to 64 of them:
+//   S^T[TOK x N] = K_tile . Q^T            O^T[Dv x N] += V_tile^T . P^T
+// A thread of the softmax owns a token (a row of S^T): sums over tokens stay in its registers
+// until the item ends.  The running maximum of a column is raised only where a tile exceeds it
+// by more than 2^8, which one vote a tile finds out; only then, and in an item's first tile,
+// the column maxima are reduced over the tokens and O is rescaled.
+//
+// A tile stands in shared memory as the TMA unit writes it, [8-token group][64-element slab]
+// [8 tokens][128 bytes] with the 128-byte swizzle, one copy to a block of any size.  The same
+// bytes are K-major for S (group stride between its 8-row groups) and MN-major for O.
+//
+// Work: the tiles of all (sequence, KV head, pair of column groups) items in a row, cut into
+// windows of equal cost (pa_multi_window.cuh), one to a set of `gs` CTAs: one CTA, or two that
+// take the two column groups of a pair and read the same tiles at the same time, the second
+// time from L2.  What a window boundary cuts leaves partial (m, l, acc) in the workspace, and
+// the join kernel takes the parts together.
+//
+// Values that a row does not see have no part in it: tokens behind the end are zeroed in
+// shared memory.  A new token's V may hold infinities or NaN that only some columns see, and
+// 0 times those is no zero: such a row is zeroed too, and what it gives to the columns that
+// see it is added by the softmax warps (rare, and as slow as it may be).
+//
+// Roles (224 threads): warp 0 block ids and TMA; warp 1 TMEM and MMA issue; warp 2 loads q;
+// warps 3-6 softmax, one thread per token, then one per row of O^T.  Every wait is bounded; one
+// that runs out sets an abort flag, copies and MMAs in flight are drained, TMEM is freed and
+// PA_ERR_TIMEOUT is reported through status_dev.
+#pragma once
+
+#include <math.h>
+#include <math_constants.h>
+
+#include <mutex>
+
+#include "pa_common.cuh"
+#include "pa_multi_window.cuh"
+#include "pa_q8.cuh"
+#include "pa_sm100.cuh"
+
+namespace pa {
+namespace multi {
+
+using namespace sm100;
+
+constexpr int kThreads = 224;
+constexpr int kMaxCtas = 160;                  // CTAs at most (one per SM; GB300: 152)
+constexpr uint64_t kLimitNs = 2000000000ull;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kEnds = 4;                       // cost of an item's ends, in quarters of a tile
+constexpr float kRaise = 8.f;                  // log2 by which a tile may exceed the maximum
+
+struct Args {
+  void* out;
+  const void* q;
+  const void* v_src;             // the pool whose rows hold the values
+  const int32_t* tables;
+  const int32_t* lens;
+  const int32_t* q_start;
+  const int32_t* mask;
+  int B, total_q, Hq, H, G, bs_shift, max_blocks, num_blocks, max_q, words, max_len;
+  int gs;                        // CTAs of a set: column groups of an item
+  float scale_log2;
+  Window* info;                  // [sets]
+  float* ws_m;                   // [2 CTAs, N]
+  float* ws_l;
+  float* ws_acc;                 // [2 CTAs, N, Dv]
+  int32_t* status_dev;
+};
+
+// Layout of one kernel.  TOK: tokens of a tile; QS: 64-element slabs of a key; VS: of a value;
+// SHARED: the value is the key's first slabs (one tile holds both), else V has tiles of its
+// own; N: columns; TERMS: storage-type terms of a softmax weight.
+template <int TOK_, int QS_, int VS_, bool SHARED_, int N_, int TERMS_>
+struct Shape {
+  static constexpr int TOK = TOK_, QS = QS_, VS = VS_, N = N_, TERMS = TERMS_;
+  static constexpr bool SHARED = SHARED_;
+  static constexpr int DV = 64 * VS;
+  static constexpr int VM = VS == 1 ? 64 : 128;          // rows of O^T in one product
+  static constexpr int VT = DV / VM;
+  static constexpr int GS = QS * 1024;                   // bytes between 8-token groups
+  static constexpr int VGS = SHARED ? GS : VS * 1024;
+  static constexpr int UNIT = TOK / 8 * GS;              // a tile of K (and V)
+  static_assert(SHARED || VS == QS, "K and V tiles of one size share a ring");
+  static constexpr int QBYTES = N * QS * 128;
+  // the second term stands in the other half of a weight row, or in rows of its own
+  static constexpr int PBYTES = SHARED ? 0 : TOK * 128 * (TERMS == 2 && N > 32 ? 2 : 1);
+  static constexpr int kTailBytes = 6144;
+  static constexpr int kBudget = 232448 - 1024 - kTailBytes;
+  // two q operands where they leave room for as many tiles
+  static constexpr int units_with(int qbufs) {
+    return (kBudget - qbufs * QBYTES - 2 * PBYTES) / UNIT;
+  }
+  static constexpr int QBUFS = units_with(2) >= (SHARED ? 2 : 4) ? 2 : 1;
+  static constexpr int RING = units_with(QBUFS) > 8 ? 8 : units_with(QBUFS);
+  static_assert(RING >= (SHARED ? 2 : 3), "ring too shallow");
+  static constexpr int kQOff = RING * UNIT;
+  static constexpr int kPOff = kQOff + QBUFS * QBYTES;
+  static constexpr int kTailOff = kPOff + 2 * PBYTES;
+  static constexpr int kSmem = kTailOff + kTailBytes + 1024;
+  static constexpr int kUsedCols = (2 + VT) * N;
+  static constexpr uint32_t kCols =
+      kUsedCols <= 32 ? 32 : (kUsedCols <= 64 ? 64 : (kUsedCols <= 128 ? 128
+                                                      : (kUsedCols <= 256 ? 256 : 512)));
+  static_assert(kUsedCols <= 512 && kSmem <= 232448, "fits an SM");
+};
+
+template <class S>
+struct Tail {
+  uint64_t full[8], empty[8];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_free, drain;
+  int64_t lin[2];
+  int64_t sums[kThreads / 32][2];
+  Place start;
+  int64_t out_at[S::N];          // element of out where a column's row begins, -1: none
+  int query[S::N];               // the column's new token, -1: none
+  float top[S::N];               // running maximum
+  float neg[S::N];               // what is added to a score before its power of two
+  float by[S::N];                // 2^(maximum before - now), then 1 / the weights' sum
+  float red[4][S::N];
+  float share[S::N];             // weights of a row whose values are added apart, -1: unseen
+  uint32_t odd[4];               // such rows of a tile, a word of a warp
+  uint32_t tmem;
+  int abort_flag;
+};
+
+struct Seq {
+  int L, n, qs, nt, items;
+};
+
+// A sequence's lengths and work; nt 0: none.  *bad: it is skipped and reported.
+template <class S>
+__device__ __forceinline__ Seq seq_of(const Args& a, int b, bool* bad) {
+  Seq s;
+  s.L = a.lens[b];
+  s.qs = b;
+  s.n = 1;
+  if (a.q_start) {
+    s.qs = a.q_start[b];
+    s.n = a.q_start[b + 1] - s.qs;
+  }
+  *bad = s.L < 0 || s.L > a.max_len ||
+         (int64_t)s.L > ((int64_t)a.max_blocks << a.bs_shift) || s.qs < 0 || s.n < 0 ||
+         s.n > a.max_q || s.n > a.total_q - s.qs || (a.q_start && s.n > s.L);
+  s.nt = *bad || s.n == 0 ? 0 : (s.L + S::TOK - 1) / S::TOK;
+  const int wide = S::N * a.gs;
+  s.items = s.nt == 0 ? 0 : a.H * ((s.n * a.G + wide - 1) / wide);
+  return s;
+}
+
+// Walks the segments of a window: its part of one item after another.
+struct Segment {
+  int b, h, col0, j0, j1, nt, L, n, qs;
+  int part;                      // 0: the window's first segment, else 1
+  bool active;                   // the CTA's column group has a column
+};
+
+template <class S>
+struct Walk {
+  Seq s;
+  int b, item, j, left, part;
+
+  __device__ __forceinline__ bool next(const Args& a, int r, Segment* g) {
+    if (left <= 0) return false;
+    while (j >= s.nt || item >= s.items) {
+      j = 0;
+      if (++item >= s.items) {
+        item = 0;
+        do {
+          if (++b >= a.B) {
+            left = 0;
+            return false;
+          }
+          bool bad;
+          s = seq_of<S>(a, b, &bad);
+        } while (s.items == 0);
+      }
+    }
+    const int pairs = s.items / a.H;
+    g->b = b;
+    g->h = item / pairs;
+    g->col0 = ((item - g->h * pairs) * a.gs + r) * S::N;
+    g->active = g->col0 < s.n * a.G;
+    g->j0 = j;
+    g->j1 = s.nt - j <= left ? s.nt : j + left;
+    g->nt = s.nt;
+    g->L = s.L;
+    g->n = s.n;
+    g->qs = s.qs;
+    g->part = part;
+    part = 1;
+    left -= g->j1 - j;
+    j = g->j1;
+    return true;
+  }
+};
+
+// One block of the cache to shared memory: [8-token groups][slabs][8][64].
+__device__ __forceinline__ void tma_block(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                          int group, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(0), "r"(0),
+      "r"(group), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_block_head(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                               int group, int h, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(0), "r"(0),
+      "r"(group), "r"(h), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+
+// Is any of 128 threads' predicates true?
+__device__ __forceinline__ bool any_of_128(int id, bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return y != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t t, float (&v)[N]) {
+  if constexpr (N == 64) tmem_ld64(t, v);
+  else if constexpr (N == 32) tmem_ld32(t, v);
+  else tmem_ld16(t, v);
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+struct MaxOf {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct SumOf {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// Sixteen values of every lane, reduced over the lanes: each step hands the other half of the
+// columns to the lane's partner, so that sixteen shuffles do.  Lanes 2 c and 2 c + 1 end with
+// one column, stored by the first.
+template <class F>
+__device__ __forceinline__ void reduce16(float (&v)[16], float* to, int lane, const F& f) {
+  int col = 0;
+#pragma unroll
+  for (int o = 16, n = 8; o > 1; o >>= 1, n >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float mine = up ? v[i + n] : v[i], other = up ? v[i] : v[i + n];
+      v[i] = f(mine, __shfl_xor_sync(kAll, other, o));
+    }
+    col += up ? n : 0;
+  }
+  v[0] = f(v[0], __shfl_xor_sync(kAll, v[0], 1));
+  if (!(lane & 1)) to[col] = v[0];
+}
+
+template <int N, class F>
+__device__ __forceinline__ void reduce_columns(const float (&x)[N], float* to, int lane,
+                                               const F& f) {
+#pragma unroll
+  for (int c0 = 0; c0 < N; c0 += 16) {
+    float v[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] = x[c0 + c];
+    reduce16(v, to + c0, lane, f);
+  }
+}
+
+// Of two storage-type values in a word: is one infinite or NaN?
+template <int DT>
+__device__ __forceinline__ bool odd2(uint32_t w) {
+  constexpr uint32_t e = DT == PA_BFLOAT16 ? 0x7F80u : 0x7C00u;
+  return (w & e) == e || (w >> 16 & e) == e;
+}
+
+template <class S, int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+             const Args a) {
+  constexpr int N = S::N, R = S::RING, QB = S::QBUFS, TOK = S::TOK;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  static_assert(sizeof(Tail<S>) <= S::kTailBytes, "barrier block");
+  Tail<S>* tail = reinterpret_cast<Tail<S>*>(smem + S::kTailOff);
+  volatile int* abort_flag = &tail->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int set = (int)blockIdx.x / a.gs, r = (int)blockIdx.x - set * a.gs;
+  const int sets = (int)gridDim.x / a.gs;
+
+  allow_next_grid();
+  if (tid == 0) {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&tail->full[i], 1);
+      mbar_init(&tail->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tail->q_full[i], 1);
+      mbar_init(&tail->q_empty[i], 1);
+      mbar_init(&tail->s_full[i], 1);
+      mbar_init(&tail->p_full[i], 4);
+      mbar_init(&tail->o_done[i], 1);
+    }
+    mbar_init(&tail->o_free, 4);
+    mbar_init(&tail->drain, 1);
+    tail->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&map_k);
+    if (!S::SHARED) tma_prefetch_desc(&map_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tail->tmem, S::kCols);
+    tmem_relinquish();
+  }
+  wait_prior_grid();
+
+  // this set's window
+  const int per = (a.B + kThreads - 1) / kThreads;
+  Share share;
+  share.b0 = min(a.B, tid * per);
+  share.b1 = min(a.B, share.b0 + per);
+  share.tiles = share.items = 0;
+  auto work_of = [&](int b) {
+    bool bad;
+    const Seq s = seq_of<S>(a, b, &bad);
+    return Work{s.nt, s.items};
+  };
+  for (int b = share.b0; b < share.b1; ++b) {
+    const Work w = work_of(b);
+    share.tiles += (int64_t)w.nt * w.items;
+    share.items += w.items;
+  }
+  share.tiles_to = share.tiles;
+  share.items_to = share.items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(kAll, share.tiles_to, o);
+    const int64_t n = __shfl_up_sync(kAll, share.items_to, o);
+    if (lane >= o) {
+      share.tiles_to += t;
+      share.items_to += n;
+    }
+  }
+  if (lane == 31) {
+    tail->sums[warp][0] = share.tiles_to;
+    tail->sums[warp][1] = share.items_to;
+  }
+  share.tiles_to -= share.tiles;
+  share.items_to -= share.items;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int64_t tiles = 0, items = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) {
+      share.tiles_to += tail->sums[w][0];
+      share.items_to += tail->sums[w][1];
+    }
+    tiles += tail->sums[w][0];
+    items += tail->sums[w][1];
+  }
+  const Cut cut = cut_of(tiles, items, sets, kEnds);
+  if (set < cut.windows) {
+    Place p;
+    if (place_of(cut, share, a.B, bound_of(cut, set), work_of, &p)) {
+      tail->start = p;
+      tail->lin[0] = p.lin;
+    }
+    if (set + 1 == cut.windows) {
+      if (tid == 0) tail->lin[1] = cut.tiles;
+    } else if (place_of(cut, share, a.B, bound_of(cut, set + 1), work_of, &p)) {
+      tail->lin[1] = p.lin;
+    }
+  } else if (tid == 0) {
+    tail->start = Place{0, -1, -1, 0};
+    tail->lin[0] = tail->lin[1] = 0;
+  }
+  __syncthreads();
+  Walk<S> walk;
+  walk.b = tail->start.b;
+  walk.item = tail->start.item;
+  walk.j = tail->start.j;
+  walk.left = (int)(tail->lin[1] - tail->lin[0]);
+  walk.part = 0;
+  if (tid == 0 && r == 0) a.info[set] = Window{walk.b, walk.item, walk.j, walk.left};
+  walk.s = Seq{};
+  if (walk.left > 0) {
+    bool bad;
+    walk.s = seq_of<S>(a, walk.b, &bad);
+  }
+  const uint32_t tmem = tail->tmem, ocol = tmem + 2 * N;
+  const uint32_t ring = smem_addr(smem), qb = smem_addr(smem + S::kQOff);
+  Segment g;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ block ids, TMA --
+    // read again by the other column groups of the item, else once
+    const uint64_t policy = a.gs > 1 ? policy_evict_last() : policy_evict_first();
+    const int bs = 1 << a.bs_shift, per_tile = TOK >> a.bs_shift;
+    const int outside = a.num_blocks << a.bs_shift >> 3;        // such a copy reads zeros
+    int u = 0;
+    while (ok && walk.next(a, r, &g)) {
+      if (!g.active) continue;
+      const int32_t* table = a.tables + (int64_t)g.b * a.max_blocks;
+      auto id_of = [&](int j) {
+        return lane < per_tile && (int64_t)j * TOK + lane * bs < g.L ? table[j * per_tile + lane]
+                                                                     : -1;
+      };
+      int id = id_of(g.j0);
+      for (int j = g.j0; j < g.j1 && ok; ++j) {
+        const int nb = (min(TOK, g.L - j * TOK) + bs - 1) >> a.bs_shift;
+        int group = outside;
+        if (lane < nb) {
+          if (id >= 0 && id < a.num_blocks) group = id << a.bs_shift >> 3;
+          else report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+        }
+        if (j + 1 < g.j1) id = id_of(j + 1);
+#pragma unroll
+        for (int kv = 0; kv < (S::SHARED ? 1 : 2); ++kv) {
+          const int stage = u % R;
+          if (lane == 0) {
+            ok = mbar_wait(&tail->empty[stage], ((u / R) & 1) ^ 1, abort_flag, kLimitNs);
+            if (ok) mbar_arrive_expect_tx(&tail->full[stage], (uint32_t)((nb * bs >> 3) * S::GS));
+          }
+          ok = __shfl_sync(kAll, (int)ok, 0) != 0;
+          if (!ok) break;
+          if (lane < nb) {
+            uint8_t* dst = smem + stage * S::UNIT + (lane * bs >> 3) * S::GS;
+            if (S::SHARED) tma_block(dst, &map_k, &tail->full[stage], group, policy);
+            else tma_block_head(dst, kv ? &map_v : &map_k, &tail->full[stage], group, g.h, policy);
+          }
+          ++u;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      report(a.status_dev, PA_ERR_TIMEOUT);
+    }
+    if (*abort_flag && lane == 0) {             // copies in flight land before the CTA ends
+      for (int i = max(0, u - R); i < u; ++i)
+        mbar_wait_drain(&tail->full[i % R], (i / R) & 1, kLimitNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issue --
+    // K . q of tile t, then V . p of tile t - 1: the softmax of a tile runs while the tensor
+    // cores have the next tile's scores.  Where an item begins, q may still be on its way, so
+    // V . p goes first.
+    constexpr uint32_t ab = DT == PA_BFLOAT16 ? 1u : 0u;
+    constexpr uint32_t idesc_s = idesc_f16(ab, 0, 0, TOK, N);
+    constexpr uint32_t idesc_o = idesc_f16(ab, 1, 1, S::VM, N);
+    if (lane == 0) {
+      int t = 0, seg = 0;
+      bool prev_first = false;
+      int prev_seg = 0;
+      auto issue_pv = [&](int p) -> bool {
+        const int u = S::SHARED ? p : 2 * p + 1, slot = p & 1;
+        // the weights are there, and with them: S of tile p is read
+        if ((!S::SHARED &&
+             !mbar_wait(&tail->full[u % R], (u / R) & 1, abort_flag, kLimitNs)) ||
+            !mbar_wait(&tail->p_full[slot], (p >> 1) & 1, abort_flag, kLimitNs) ||
+            (prev_first && prev_seg > 0 &&
+             !mbar_wait(&tail->o_free, (prev_seg - 1) & 1, abort_flag, kLimitNs)))
+          return false;
+        tc_fence_after();
+        const uint32_t va = ring + (u % R) * S::UNIT;
+        const uint32_t pw = S::SHARED ? va + (S::QS - 1) * 1024
+                                      : smem_addr(smem + S::kPOff + slot * S::PBYTES);
+        constexpr int PGS = S::SHARED ? S::GS : 1024;
+#pragma unroll
+        for (int v = 0; v < S::VT; ++v)
+#pragma unroll
+          for (int k = 0; k < TOK / 16; ++k)
+#pragma unroll
+            for (int term = 0; term < S::TERMS; ++term)
+              mma_f16(ocol + v * N,
+                      smem_desc_sw128(va + v * (S::VM / 64) * 1024 + k * 2 * S::VGS, 1024, S::VGS),
+                      smem_desc_sw128(pw + k * 2 * PGS + term * (N > 32 ? TOK * 128 : 64), 1024,
+                                      PGS),
+                      idesc_o, !prev_first || (k | term) != 0);
+        mma_commit(&tail->empty[u % R]);
+        mma_commit(&tail->o_done[slot]);
+        return true;
+      };
+      while (ok && walk.next(a, r, &g)) {
+        if (!g.active) continue;
+        const int qs = seg % QB;
+        for (int j = g.j0; j < g.j1 && ok; ++j) {
+          const int u = S::SHARED ? t : 2 * t;
+          const bool first = j == g.j0;
+          if (first && t > 0) ok = issue_pv(t - 1);
+          ok = ok && (!first || mbar_wait(&tail->q_full[qs], (seg / QB) & 1, abort_flag, kLimitNs)) &&
+               mbar_wait(&tail->full[u % R], (u / R) & 1, abort_flag, kLimitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ka = ring + (u % R) * S::UNIT, qa = qb + qs * S::QBYTES;
+#pragma unroll
+          for (int k = 0; k < 4 * S::QS; ++k)
+            mma_f16(tmem + (t & 1) * N,
+                    smem_desc_sw128(ka + (k >> 2) * 1024 + (k & 3) * 32, 16, S::GS),
+                    smem_desc_sw128(qa + (k >> 2) * (N * 128) + (k & 3) * 32, 16, 1024), idesc_s,
+                    k > 0);
+          if (!S::SHARED) mma_commit(&tail->empty[u % R]);
+          mma_commit(&tail->s_full[t & 1]);
+          if (j + 1 == g.j1) mma_commit(&tail->q_empty[qs]);
+          if (!first) ok = issue_pv(t - 1);
+          prev_first = first;
+          prev_seg = seg;
+          ++t;
+        }
+        ++seg;
+      }
+      if (ok && t > 0) ok = issue_pv(t - 1);
+      if (!ok) {
+        *abort_flag = 1;
+        report(a.status_dev, PA_ERR_TIMEOUT);
+      }
+      // every product and commit issued here ends before TMEM is freed
+      if (t > 0) {
+        mma_commit(&tail->drain);
+        mbar_wait_drain(&tail->drain, 0, kLimitNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ----------------------------------------------------------------------- q --
+    int seg = 0;
+    while (ok && walk.next(a, r, &g)) {
+      if (!g.active) continue;
+      const int slot = seg % QB;
+      if (seg >= QB) {
+        ok = mbar_wait(&tail->q_empty[slot], (seg / QB - 1) & 1, abort_flag, kLimitNs);
+        ok = __all_sync(kAll, ok);
+        if (!ok) break;
+      }
+      const int cols = g.n * a.G;
+      for (int c = 0; c < N; ++c) {
+        const int u = g.col0 + c;
+        const bool live = u < cols;
+        const int i = live ? u / a.G : 0, head = g.h * a.G + (live ? u - i * a.G : 0);
+        const uint8_t* row = static_cast<const uint8_t*>(a.q) +
+                             ((int64_t)(g.qs + i) * a.Hq + head) * (S::QS * 128);
+        for (int x = lane; x < 8 * S::QS; x += 32)
+          cp_async16(qb + slot * S::QBYTES + (x >> 3) * (N * 128) + c * 128 +
+                         (((x & 7) ^ (c & 7)) << 4),
+                     row + x * 16, live);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->q_full[slot]);
+      ++seg;
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      report(a.status_dev, PA_ERR_TIMEOUT);
+    }
+    // sequences without work: empty ones of a step without q_start, and bad ones
+    for (int b = (int)blockIdx.x; b < a.B; b += (int)gridDim.x) {
+      bool bad;
+      const Seq s = seq_of<S>(a, b, &bad);
+      if (bad) {
+        if (lane == 0) report(a.status_dev, PA_ERR_BAD_BLOCK_ID);
+      } else if (!a.q_start && s.L == 0) {
+        uint4* row = static_cast<uint4*>(a.out) + (int64_t)b * a.Hq * (S::DV / 8);
+        for (int i = lane; i < a.Hq * (S::DV / 8); i += 32) row[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax and output rows --
+    const int wq = warp & 3;                     // TMEM lane quarter of this warp
+    const int st = tid - 96;                     // 0 .. 127
+    const uint32_t quarter = (uint32_t)(wq * 32) << 16;
+    // S^T of 64 tokens: sixteen lanes of each quarter hold a row
+    const bool has_row = TOK == 128 || lane < 16;
+    const int row = TOK == 128 ? wq * 32 + lane : wq * 16 + (lane & 15);
+    const float sl2 = a.scale_log2;
+    // fp16 weights stand 2^7 higher: below 2^-14 they would lose bits.  A weight is at most
+    // 2^kRaise times that.
+    constexpr float kShift = DT == PA_BFLOAT16 ? 0.f : 7.f;
+    float l[N];
+    int t = 0;
+    auto wait_all = [&](uint64_t* bar, int parity) -> bool {
+      return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kLimitNs));
+    };
+    // V . p of tile i; whoever has S of tile i + 1 or i knows that of tile i - 2 to be done
+    auto wait_product = [&](int i) -> bool { return wait_all(&tail->o_done[i & 1], (i >> 1) & 1); };
+    auto sync = [&]() { named_barrier(1, 128); };
+    while (ok && walk.next(a, r, &g)) {
+      if (!g.active) continue;
+      const int ctx = g.L - g.n;
+      // the columns of this item (those of the one before have been read)
+      sync();
+      if (st < N) {
+        const int u = g.col0 + st, i = u / a.G;
+        const bool live = u < g.n * a.G;
+        tail->query[st] = live ? i : -1;
+        tail->out_at[st] =
+            live ? ((int64_t)(g.qs + i) * a.Hq + g.h * a.G + (u - i * a.G)) * S::DV : -1;
+      }
+      sync();
+      auto sees = [&](int c, int jj) -> bool {
+        const int i = tail->query[c];
+        if (i < 0) return false;
+        return a.mask ? (a.mask[(int64_t)(g.qs + i) * a.words + (jj >> 5)] >> (jj & 31)) & 1
+                      : jj <= i;
+      };
+      for (int j = g.j0; j < g.j1; ++j, ++t) {
+        const bool first = j == g.j0, last = j + 1 == g.j1;
+        const int u = S::SHARED ? t : 2 * t + 1;              // the tile of V
+        if (!wait_all(&tail->s_full[t & 1], (t >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        float s[N];
+        load_scores<N>(tmem + quarter + (t & 1) * N, s);
+        const uint64_t scale2 = f2_pack(sl2, sl2);
+#pragma unroll
+        for (int c = 0; c < N; c += 2)
+          f2_unpack(mul2(f2_pack(s[c], s[c + 1]), scale2), s[c], s[c + 1]);
+        const int tok = j * TOK + row;
+        if (!has_row || tok >= g.L) {
+#pragma unroll
+          for (int c = 0; c < N; ++c) s[c] = -CUDART_INF_F;
+        } else if (tok >= ctx) {
+#pragma unroll
+          for (int c = 0; c < N; ++c)
+            if (!sees(c, tok - ctx)) s[c] = -CUDART_INF_F;
+        }
+        bool raise = first;
+        if (!first) {
+          float over = -CUDART_INF_F;
+#pragma unroll
+          for (int c = 0; c < N; ++c) over = fmaxf(over, s[c] + tail->neg[c]);
+          raise = any_of_128(1, over > kRaise + kShift);
+        }
+        if (raise) {
+          reduce_columns<N>(s, tail->red[wq], lane, MaxOf());
+          sync();
+          if (st < N) {
+            const float before = first ? -CUDART_INF_F : tail->top[st];
+            const float now = fmaxf(before, fmaxf(fmaxf(tail->red[0][st], tail->red[1][st]),
+                                                  fmaxf(tail->red[2][st], tail->red[3][st])));
+            tail->top[st] = now;
+            tail->neg[st] = (now == -CUDART_INF_F ? 0.f : -now) + kShift;
+            tail->by[st] = before == -CUDART_INF_F ? 0.f : ex2_approx(before - now);
+          }
+          sync();
+          if (first) {
+#pragma unroll
+            for (int c = 0; c < N; ++c) l[c] = 0.f;
+          } else {
+#pragma unroll
+            for (int c = 0; c < N; ++c) l[c] *= tail->by[c];
+            // O (complete up to the tile before; this one's product waits for its weights)
+            if (!wait_product(t - 1)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < S::VT * N; c0 += 16) {
+              float o[16];
+              tmem_ld16(ocol + quarter + c0, o);
+              uint32_t w[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                w[c] = __float_as_uint(o[c] * tail->by[(c0 & (N - 1)) + c]);
+              tmem_st16_nowait(ocol + quarter + c0, w);
+            }
+            tmem_wait_st();
+          }
+        }
+        // weights: to shared memory as rows of 64 columns, N-major, in storage-type terms
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+          f2_unpack(f2_add(f2_pack(s[c], s[c + 1]), f2_pack(tail->neg[c], tail->neg[c + 1])), s[c],
+                    s[c + 1]);
+          s[c] = ex2_approx(s[c]);
+          s[c + 1] = ex2_approx(s[c + 1]);
+          l[c] += s[c];
+          l[c + 1] += s[c + 1];
+        }
+        if (has_row) {
+          constexpr int PGS = S::SHARED ? S::GS : 1024;
+          uint8_t* prow = (S::SHARED ? smem + (u % R) * S::UNIT + (S::QS - 1) * 1024
+                                     : smem + S::kPOff + (t & 1) * S::PBYTES) +
+                          (row >> 3) * PGS + (row & 7) * 128;
+#pragma unroll
+          for (int c = 0; c < N; c += 8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = s[c + 2 * e], y = s[c + 2 * e + 1];
+              if (S::TERMS == 1) {
+                hi[e] = pack2<DT>(x, y);
+              } else if (DT == PA_BFLOAT16) {
+                // the top 16 bits of a weight, then of what they leave
+                const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+                hi[e] = __byte_perm(ux, uy, 0x7632);
+                lo[e] = __byte_perm(__float_as_uint(x - __uint_as_float(ux & 0xFFFF0000u)),
+                                    __float_as_uint(y - __uint_as_float(uy & 0xFFFF0000u)), 0x7632);
+              } else {
+                hi[e] = pack2<DT>(x, y);
+                const float2 f = widen2<DT>(hi[e]);
+                lo[e] = pack2<DT>(x - f.x, y - f.y);
+              }
+            }
+            const int chunk = c >> 3;
+            *reinterpret_cast<uint4*>(prow + ((chunk ^ (row & 7)) << 4)) =
+                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (S::TERMS == 2) {
+              uint8_t* to = N > 32 ? prow + TOK * 128 + ((chunk ^ (row & 7)) << 4)
+                                   : prow + (((chunk + 4) ^ (row & 7)) << 4);
+              *reinterpret_cast<uint4*>(to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
+        }
+        // V of tokens behind the end, and of new tokens that not every column sees
+        const bool ends = (j + 1) * TOK > g.L;
+        const bool fresh = g.n > 1 && (j + 1) * TOK > ctx;
+        bool apart = false;
+        if (ends || fresh) {
+          if (!wait_all(&tail->full[u % R], (u / R) & 1)) { ok = false; break; }
+          uint8_t* vrow = smem + (u % R) * S::UNIT + (row >> 3) * S::VGS + (row & 7) * 128;
+          bool zero = has_row && tok >= g.L;
+          if (fresh) {
+            bool odd = false;
+            if (has_row && tok >= ctx && tok < g.L) {
+#pragma unroll 4
+              for (int x = 0; x < 8 * S::VS; ++x) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 +
+                                                                (x & 7) * 16);
+                odd = odd || odd2<DT>(w.x) || odd2<DT>(w.y) || odd2<DT>(w.z) || odd2<DT>(w.w);
+              }
+            }
+            zero = zero || odd;
+            const uint32_t rows = __ballot_sync(kAll, odd);
+            if (lane == 0) tail->odd[wq] = rows;
+            apart = any_of_128(1, odd);
+          }
+          if (zero) {
+#pragma unroll 4
+            for (int x = 0; x < 8 * S::VS; ++x)
+              *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + (x & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->p_full[t & 1]);
+        if (apart) {
+          // o += p v for each such row, where the column sees it
+          if (!wait_product(t)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {
+            uint32_t rows = tail->odd[w];
+            while (rows) {
+              const int x = __ffs(rows) - 1;
+              rows &= rows - 1;
+              const int at = j * TOK + (TOK == 128 ? w * 32 + x : w * 16 + x);
+              if (wq == w && lane == x) {
+#pragma unroll
+                for (int c = 0; c < N; ++c) tail->share[c] = sees(c, at - ctx) ? s[c] : -1.f;
+              }
+              sync();
+              const int id = a.tables[(int64_t)g.b * a.max_blocks + (at >> a.bs_shift)];
+              const int64_t slot = ((int64_t)id << a.bs_shift) + (at & ((1 << a.bs_shift) - 1));
+              const uint16_t* vsrc =                     // in the pool: a bad block's are zeros
+                  static_cast<const uint16_t*>(a.v_src) +
+                  (S::SHARED ? slot * (64 * S::QS) : (slot * a.H + g.h) * S::DV);
+#pragma unroll 1
+              for (int v = 0; v < S::VT; ++v) {
+                const int dim = v * S::VM + (S::VM == 128 ? wq * 32 + lane : wq * 16 + (lane & 15));
+                const float val = widen2<DT>(vsrc[dim]).x;
+#pragma unroll 1
+                for (int c0 = 0; c0 < N; c0 += 16) {
+                  float o[16];
+                  tmem_ld16(ocol + quarter + v * N + c0, o);
+                  uint32_t ow[16];
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) {
+                    const float p = tail->share[c0 + c];
+                    ow[c] = __float_as_uint(p == -1.f ? o[c] : fmaf(p, val, o[c]));
+                  }
+                  tmem_st16_nowait(ocol + quarter + v * N + c0, ow);
+                  tmem_wait_st();
+                }
+              }
+              sync();
+            }
+          }
+          tc_fence_before();
+        }
+        if (!last) continue;
+
+        // ------------------------------------------------------- the segment's end --
+        const bool whole = g.j0 == 0 && g.j1 == g.nt;
+        const int64_t part = 2 * (int64_t)blockIdx.x + g.part;
+        reduce_columns<N>(l, tail->red[wq], lane, SumOf());
+        sync();
+        if (st < N) {
+          const float sum = (tail->red[0][st] + tail->red[1][st]) +
+                            (tail->red[2][st] + tail->red[3][st]);
+          tail->by[st] = sum == 0.f ? 0.f : 1.f / sum;
+          if (!whole) {
+            a.ws_m[part * N + st] = tail->top[st];
+            a.ws_l[part * N + st] = sum;
+          }
+        }
+        if (!wait_product(t)) { ok = false; break; }
+        sync();
+        tc_fence_after();
+        const bool has_dim = S::VM == 128 || lane < 16;
+#pragma unroll 1
+        for (int v = 0; v < S::VT; ++v) {
+          const int dim = v * S::VM + (S::VM == 128 ? wq * 32 + lane : wq * 16 + (lane & 15));
+#pragma unroll 1
+          for (int c0 = 0; c0 < N; c0 += 16) {
+            float o[16];
+            tmem_ld16(ocol + quarter + v * N + c0, o);
+            if (whole) {
+              // two lanes exchange halves of two columns: a store of two dims of one column
+#pragma unroll
+              for (int c = 0; c < 16; c += 2) {
+                const float by0 = tail->by[c0 + c], by1 = tail->by[c0 + c + 1];
+                const float y0 = by0 == 0.f ? 0.f : o[c] * by0;
+                const float y1 = by1 == 0.f ? 0.f : o[c + 1] * by1;
+                const float other = __shfl_xor_sync(kAll, lane & 1 ? y0 : y1, 1);
+                const int64_t to = tail->out_at[c0 + c + (lane & 1)];
+                if (has_dim && to >= 0)
+                  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to + (dim & ~1)) =
+                      lane & 1 ? pack2<DT>(other, y1) : pack2<DT>(y0, other);
+              }
+            } else if (has_dim) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (tail->query[c0 + c] >= 0)
+                  a.ws_acc[(part * N + c0 + c) * S::DV + dim] = o[c];
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->o_free);
+      }
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) report(a.status_dev, PA_ERR_TIMEOUT);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kCols);
+  }
+}
+
+// Joins the partials of items that window boundaries cut: CTA (c, r, z) looks at the boundary
+// where window c + 1 begins, and joins columns [z, z + 1) * cols of column group r of its item,
+// if that boundary is the item's first.  The parts: the segment of window c that ends there,
+// then the first segments of the windows behind, as long as they begin inside the item.
+// A thread takes four dims of a column and every PS-th part.
+constexpr int kJoinThreads = 512;
+
+template <class S, int DT, int PS>
+__global__ void __launch_bounds__(kJoinThreads)
+join_kernel(const Args a, int sets, int cols) {
+  constexpr int N = S::N, DV = S::DV, LANES = DV / 4;
+  constexpr int COLS = kJoinThreads / LANES / PS;          // columns at once
+  __shared__ float s_w[COLS][kMaxCtas + 1];
+  __shared__ bool s_none[COLS];                            // no weight at all: zeros
+  __shared__ float4 s_sum[PS > 1 ? PS : 1][PS > 1 ? COLS * LANES : 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = (int)blockIdx.x + 1, r = (int)blockIdx.y;
+  allow_next_grid();
+  wait_prior_grid();
+  const Window at = a.info[c], before = a.info[c - 1];
+  bool same;
+  if (!first_cut(at, before, &same)) return;
+  bool in = false;
+  if (c + 1 + tid < sets) {
+    const Window w = a.info[c + 1 + tid];
+    in = w.b == at.b && w.item == at.item && w.j > 0 && w.tiles > 0;
+  }
+  const int parts = 2 + __syncthreads_count(in);
+  bool bad;
+  const Seq s = seq_of<S>(a, at.b, &bad);
+  const int pairs = s.items / a.H, h = at.item / pairs;
+  const int col0 = ((at.item - h * pairs) * a.gs + r) * N;
+  const int n = min(N, s.n * a.G - col0);
+  // row of part k in ws_m and ws_l
+  auto row = [&](int k) -> int64_t {
+    const int cta = (c - 1 + k) * a.gs + r;
+    return (2 * (int64_t)cta + (k == 0 && !same ? 1 : 0)) * N;
+  };
+  const int x = tid % (COLS * LANES), ps = tid / (COLS * LANES);
+  const int col = x / LANES, d = (x % LANES) * 4;
+  const int end = min(n, ((int)blockIdx.z + 1) * cols);
+  for (int c0 = (int)blockIdx.z * cols; c0 < end; c0 += COLS) {
+    for (int w = warp; w < COLS; w += kJoinThreads / 32) {
+      if (c0 + w >= end) break;
+      float top = -CUDART_INF_F;
+      for (int k = lane; k < parts; k += 32) {
+        const float m = a.ws_m[row(k) + c0 + w];
+        s_w[w][k] = m;
+        top = fmaxf(top, m);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+      float l = 0.f;
+      for (int k = lane; k < parts; k += 32) {
+        const float y = top == -CUDART_INF_F ? 0.f : ex2_approx(s_w[w][k] - top);
+        s_w[w][k] = y;
+        l = fmaf(y, a.ws_l[row(k) + c0 + w], l);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      for (int k = lane; k < parts; k += 32) s_w[w][k] *= inv;
+      if (lane == 0) s_none[w] = l == 0.f;
+    }
+    __syncthreads();
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c0 + col < end) {
+#pragma unroll 8
+      for (int k = ps; k < parts; k += PS) {
+        const float y = s_w[col][k];
+        const float4 v =
+            *reinterpret_cast<const float4*>(a.ws_acc + (row(k) + c0 + col) * DV + d);
+        sum.x = fmaf(y, v.x, sum.x);
+        sum.y = fmaf(y, v.y, sum.y);
+        sum.z = fmaf(y, v.z, sum.z);
+        sum.w = fmaf(y, v.w, sum.w);
+      }
+    }
+    if (PS > 1) {
+      s_sum[PS > 1 ? ps : 0][PS > 1 ? x : 0] = sum;
+      __syncthreads();
+      if (ps == 0) {
+#pragma unroll
+        for (int i = 1; i < PS; ++i) {
+          const float4 v = s_sum[i][PS > 1 ? x : 0];
+          sum.x += v.x;
+          sum.y += v.y;
+          sum.z += v.z;
+          sum.w += v.w;
+        }
+      }
+    }
+    if (ps == 0 && c0 + col < end) {
+      if (s_none[col]) sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int u = col0 + c0 + col, i = u / a.G;
+      const int64_t to = ((int64_t)(s.qs + i) * a.Hq + h * a.G + (u - i * a.G)) * DV + d;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
+          make_uint2(pack2<DT>(sum.x, sum.y), pack2<DT>(sum.z, sum.w));
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ host side --
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                         cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// A pool [num_blocks, bs, heads, 64 slabs] as [heads][8-token groups][slabs][8 tokens][64]; a
+// box is one block of one head.  `heads` 0: of rows without heads.
+inline bool encode_blocks(CUtensorMap* map, const void* pool, int dtype, int64_t num_blocks, int bs,
+                          int heads, int slabs) {
+  const cuuint64_t row = (cuuint64_t)(heads ? heads : 1) * slabs * 128;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)slabs, (cuuint64_t)(num_blocks * bs / 8),
+                              (cuuint64_t)heads};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)slabs * 128};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)slabs, (cuuint32_t)(bs / 8), 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return encode_fn()(map,
+                     dtype == PA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                     heads ? 5 : 4, const_cast<void*>(pool), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Columns of a product for the most (new token, query head) pairs that an item can have, and
+// CTAs of a set.
+struct Columns {
+  int n, gs;
+};
+
+inline Columns columns_for(int64_t most) {
+  if (most <= 16) return {16, 1};
+  if (most <= 32) return {32, 1};
+  return {64, most <= 64 ? 1 : 2};
+}
+
+struct Layout {
+  size_t m_off, l_off, acc_off, total;
+};
+
+inline Layout layout_of(int n, int dv) {
+  auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  Layout y;
+  const size_t rows = (size_t)2 * kMaxCtas * n;
+  y.m_off = align(kMaxCtas * sizeof(Window));
+  y.l_off = y.m_off + align(rows * sizeof(float));
+  y.acc_off = y.l_off + align(rows * sizeof(float));
+  y.total = y.acc_off + align(rows * dv * sizeof(float));
+  return y;
+}
+
+template <class S, int DT>
+cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, int ctas,
+                   int64_t items, bool cut, int device, cudaStream_t stream) {
+  static std::mutex lock;
+  static uint64_t done = 0;                    // devices whose attribute is set
+  {
+    std::lock_guard<std::mutex> hold(lock);
+    if (device >= 64 || !(done >> device & 1)) {
+      const cudaError_t e = taken(cudaFuncSetAttribute(
+          multi_kernel<S, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+      if (e != cudaSuccess) return e;
+      if (device < 64) done |= 1ull << device;
+    }
+  }
+  cudaError_t e = launch_pdl(multi_kernel<S, DT>, dim3((unsigned)ctas), kThreads, S::kSmem, stream,
+                             k, v, a);
+  const int sets = ctas / a.gs;
+  if (e != cudaSuccess || !cut || sets < 2) return e;
+  // few items of many parts: the parts of a few columns to a CTA, else many columns
+  if (items * 8 <= sets) {
+    constexpr int cols = kJoinThreads / (S::DV / 4) / 4;
+    return launch_pdl(join_kernel<S, DT, 4>,
+                      dim3((unsigned)(sets - 1), (unsigned)a.gs,
+                           (unsigned)((S::N + cols - 1) / cols)),
+                      kJoinThreads, 0, stream, a, sets, cols);
+  }
+  constexpr int cols = S::N / 2;
+  return launch_pdl(join_kernel<S, DT, 1>, dim3((unsigned)(sets - 1), (unsigned)a.gs, 2),
+                    kJoinThreads, 0, stream, a, sets, cols);
+}
+
+// The shape of N columns.
+template <template <int> class Of, int DT>
+cudaError_t launch_columns(int n, const CUtensorMap& k, const CUtensorMap& v, const Args& a,
+                           int ctas, int64_t items, bool cut, int device, cudaStream_t stream) {
+  if (n == 16) return launch<Of<16>, DT>(k, v, a, ctas, items, cut, device, stream);
+  if (n == 32) return launch<Of<32>, DT>(k, v, a, ctas, items, cut, device, stream);
+  return launch<Of<64>, DT>(k, v, a, ctas, items, cut, device, stream);
+}
+
+// What a call asks for, checked but for the sizes of its own cache.
+struct Call {
+  void* out;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  const int32_t* tables;
+  const int32_t* lens;
+  const int32_t* q_start;
+  const int32_t* mask;
+  int B, total_q, Hq, H, bs, max_blocks, num_blocks, max_q, words, max_len;
+  float scale;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* status_dev;
+  cudaStream_t stream;
+};
+
+// Host checks; PA_OK and *work false: nothing to do.
+inline pa_status check(const Call& c, size_t workspace_needed, bool* work) {
+  *work = false;
+  if (c.B < 0 || c.total_q < 0 || c.max_blocks <= 0 || c.num_blocks <= 0 || c.max_len < 0 ||
+      c.max_len >= (1 << 30) || !isfinite(c.scale) || (!c.q_start && c.total_q != c.B) ||
+      (c.mask && (c.words <= 0 || (int64_t)c.words * 32 < c.max_q)) ||
+      (int64_t)c.num_blocks * c.bs >= (1ll << 31) || (int64_t)c.total_q * c.Hq >= (1ll << 31))
+    return PA_ERR_INVALID_ARG;
+  if ((c.bs != 8 && c.bs != 16 && c.bs != 32 && c.bs != 64) ||
+      (c.dtype != PA_FLOAT16 && c.dtype != PA_BFLOAT16))
+    return PA_ERR_UNSUPPORTED;
+  if (c.B == 0 || c.total_q == 0) return PA_OK;
+  if (!c.out || !c.q || !c.k_pool || !c.v_pool || !c.tables || !c.lens) return PA_ERR_INVALID_ARG;
+  if ((((uintptr_t)c.out | (uintptr_t)c.q | (uintptr_t)c.k_pool | (uintptr_t)c.v_pool) & 15u) != 0)
+    return PA_ERR_INVALID_ARG;
+  if (!c.workspace || ((uintptr_t)c.workspace & 255u) || c.workspace_bytes < workspace_needed)
+    return PA_ERR_WORKSPACE;
+  *work = true;
+  return PA_OK;
+}
+
+// Launches a checked call.  Launch: f(columns, maps, args, CTAs, items, cut, device).
+template <class F>
+pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f) {
+  const int max_q = c.q_start ? c.max_q : 1, G = c.Hq / c.H;
+  const Columns cols = columns_for((int64_t)max_q * G);
+  const int64_t groups = ((int64_t)max_q * G + cols.n * cols.gs - 1) / (cols.n * cols.gs);
+  const int64_t nt = ((int64_t)c.max_len + tok - 1) / tok;
+  const int64_t items = (int64_t)c.B * c.H * groups;
+  int device = 0, sms = 0;
+  if (!encode_fn() || taken(cudaGetDevice(&device)) != cudaSuccess ||
+      taken(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  int64_t sets = (sms < kMaxCtas ? sms : kMaxCtas) / cols.gs;
+  if (items > (1ll << 31) || (items * nt) / sets >= (1ll << 30)) return PA_ERR_INVALID_ARG;
+  if (items * nt < sets) sets = items * nt > 0 ? items * nt : 1;
+  CUtensorMap k, v;
+  if (!encode_blocks(&k, c.k_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||
+      !encode_blocks(&v, c.v_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs))
+    return PA_ERR_INVALID_ARG;
+  const Layout y = layout_of(cols.n, dv);
+  char* ws = static_cast<char*>(c.workspace);
+  Args a;
+  a.out = c.out;
+  a.q = c.q;
+  a.v_src = c.v_pool;
+  a.tables = c.tables;
+  a.lens = c.lens;
+  a.q_start = c.q_start;
+  a.mask = c.mask;
+  a.B = c.B;
+  a.total_q = c.total_q;
+  a.Hq = c.Hq;
+  a.H = c.H;
+  a.G = G;
+  a.bs_shift = c.bs == 8 ? 3 : (c.bs == 16 ? 4 : (c.bs == 32 ? 5 : 6));
+  a.max_blocks = c.max_blocks;
+  a.num_blocks = c.num_blocks;
+  a.max_q = max_q;
+  a.words = c.words;
+  a.max_len = c.max_len;
+  a.gs = cols.gs;
+  a.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
+  a.info = reinterpret_cast<Window*>(ws);
+  a.ws_m = reinterpret_cast<float*>(ws + y.m_off);
+  a.ws_l = reinterpret_cast<float*>(ws + y.l_off);
+  a.ws_acc = reinterpret_cast<float*>(ws + y.acc_off);
+  a.status_dev = c.status_dev;
+  // an item of one tile is never cut
+  const cudaError_t e = f(cols.n, k, v, a, (int)(sets * cols.gs), items, nt > 1, device);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace multi
+}  // namespace pa
