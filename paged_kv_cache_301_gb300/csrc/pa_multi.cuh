@@ -9,10 +9,10 @@
 // The cache rows are the M side of both products and the columns are (new token, query head)
 // pairs of one KV head, so that a tile of the cache is read once for up to 64 of them:
 //   S^T[TOK x N] = K_tile . Q^T            O^T[Dv x N] += V_tile^T . P^T
-// A thread of the softmax owns a token (a row of S^T): sums over tokens stay in its registers
-// until the item ends.  The running maximum of a column is raised only where a tile exceeds it
-// by more than 2^8, which one vote a tile finds out; only then, and in an item's first tile,
-// the column maxima are reduced over the tokens and O is rescaled.
+// A thread of the softmax has a few columns in a few rows (tokens): sums over tokens stay in
+// its registers until the item ends.  The running maximum of a column is raised only where a
+// tile exceeds it by more than 2^8, which one vote a tile finds out; only then, and in an item's
+// first tile, the column maxima are reduced over the tokens and O is rescaled.
 //
 // A tile stands in shared memory as the TMA unit writes it, [8-token group][64-element slab]
 // [8 tokens][128 bytes] with the 128-byte swizzle, one copy to a block of any size.  The same
@@ -29,8 +29,8 @@
 // 0 times those is no zero: such a row is zeroed too, and what it gives to the columns that
 // see it is added by the softmax warps (rare, and as slow as it may be).
 //
-// Roles (224 threads): warp 0 block ids and TMA; warp 1 TMEM and MMA issue; warp 2 loads q;
-// warps 3-6 softmax, one thread per token, then one per row of O^T.  Every wait is bounded; one
+// Roles: warp 0 block ids and TMA; warp 1 TMEM and MMA issue; warp 2 loads q; the others, one or
+// two groups of four with columns of their own, softmax and output.  Every wait is bounded; one
 // that runs out sets an abort flag, copies and MMAs in flight are drained, TMEM is freed and
 // PA_ERR_TIMEOUT is reported through status_dev.
 #pragma once
@@ -50,7 +50,6 @@ namespace multi {
 
 using namespace sm100;
 
-constexpr int kThreads = 224;
 constexpr int kMaxCtas = 160;                  // CTAs at most (one per SM; GB300: 152)
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -87,6 +86,10 @@ struct Shape {
   static constexpr int VT = DV / VM;
   static constexpr int GS = QS * 1024;                   // bytes between 8-token groups
   static constexpr int VGS = SHARED ? GS : VS * 1024;
+  // softmax warpgroups, each with columns of its own
+  static constexpr int GROUPS = N >= 32 ? 2 : 1;
+  static constexpr int NC = N / GROUPS;
+  static constexpr int kThreads = 96 + 128 * GROUPS;
   static constexpr int UNIT = TOK / 8 * GS;              // a tile of K (and V)
   static_assert(SHARED || VS == QS, "K and V tiles of one size share a ring");
   static constexpr int QBYTES = N * QS * 128;
@@ -117,16 +120,15 @@ struct Tail {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_free, drain;
   int64_t lin[2];
-  int64_t sums[kThreads / 32][2];
+  int64_t sums[S::kThreads / 32][2];
   Place start;
   int64_t out_at[S::N];          // element of out where a column's row begins, -1: none
   int query[S::N];               // the column's new token, -1: none
-  float top[S::N];               // running maximum
-  float neg[S::N];               // what is added to a score before its power of two
   float by[S::N];                // 2^(maximum before - now), then 1 / the weights' sum
-  float red[4][S::N];
+  float red[4][S::N];            // per warp: columns' maxima
+  float sum[4][S::N];            // per warp: columns' sums of weights
   float share[S::N];             // weights of a row whose values are added apart, -1: unseen
-  uint32_t odd[4];               // such rows of a tile, a word of a warp
+  uint32_t odd[S::GROUPS][4];    // such rows of a tile, a word of a warp
   uint32_t tmem;
   int abort_flag;
 };
@@ -229,70 +231,53 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
                : "memory");
 }
 
-// Is any of 128 threads' predicates true?
-__device__ __forceinline__ bool any_of_128(int id, bool x) {
+// Is any of `count` threads' predicates true?
+__device__ __forceinline__ bool any_of(int id, int count, bool x) {
   uint32_t y;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(y)
-      : "r"(id), "r"((uint32_t)x)
+      : "r"(id), "r"(count), "r"((uint32_t)x)
       : "memory");
   return y != 0;
 }
 
-template <int N>
-__device__ __forceinline__ void load_scores(uint32_t t, float (&v)[N]) {
-  if constexpr (N == 64) tmem_ld64(t, v);
-  else if constexpr (N == 32) tmem_ld32(t, v);
-  else tmem_ld16(t, v);
+// 16 lanes x NC columns of tensor memory over a warp: of every eight columns lane l gets
+// columns 2 (l % 4) and the next one of row l / 4, then of row l / 4 + 8.
+template <int NC>
+__device__ __forceinline__ void load_scores(uint32_t t, float (&v)[NC / 8][4]) {
+  uint32_t r[NC / 2];
+  if constexpr (NC == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+  } else {
+    static_assert(NC == 16, "columns of a softmax group");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(t)
+        : "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < NC / 2; ++i) v[i / 4][i % 4] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-
-struct MaxOf {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-struct SumOf {
-  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-
-// Sixteen values of every lane, reduced over the lanes: each step hands the other half of the
-// columns to the lane's partner, so that sixteen shuffles do.  Lanes 2 c and 2 c + 1 end with
-// one column, stored by the first.
-template <class F>
-__device__ __forceinline__ void reduce16(float (&v)[16], float* to, int lane, const F& f) {
-  int col = 0;
-#pragma unroll
-  for (int o = 16, n = 8; o > 1; o >>= 1, n >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float mine = up ? v[i + n] : v[i], other = up ? v[i] : v[i + n];
-      v[i] = f(mine, __shfl_xor_sync(kAll, other, o));
-    }
-    col += up ? n : 0;
-  }
-  v[0] = f(v[0], __shfl_xor_sync(kAll, v[0], 1));
-  if (!(lane & 1)) to[col] = v[0];
-}
-
-template <int N, class F>
-__device__ __forceinline__ void reduce_columns(const float (&x)[N], float* to, int lane,
-                                               const F& f) {
-#pragma unroll
-  for (int c0 = 0; c0 < N; c0 += 16) {
-    float v[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) v[c] = x[c0 + c];
-    reduce16(v, to + c0, lane, f);
-  }
 }
 
 // Of two storage-type values in a word: is one infinite or NaN?
@@ -303,10 +288,10 @@ __device__ __forceinline__ bool odd2(uint32_t w) {
 }
 
 template <class S, int DT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(S::kThreads, 1)
 multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
              const Args a) {
-  constexpr int N = S::N, R = S::RING, QB = S::QBUFS, TOK = S::TOK;
+  constexpr int N = S::N, R = S::RING, QB = S::QBUFS, TOK = S::TOK, kThreads = S::kThreads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -327,10 +312,10 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
       mbar_init(&tail->q_full[i], 1);
       mbar_init(&tail->q_empty[i], 1);
       mbar_init(&tail->s_full[i], 1);
-      mbar_init(&tail->p_full[i], 4);
+      mbar_init(&tail->p_full[i], 4 * S::GROUPS);
       mbar_init(&tail->o_done[i], 1);
     }
-    mbar_init(&tail->o_free, 4);
+    mbar_init(&tail->o_free, 4 * S::GROUPS);
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
     fence_mbar_init();
@@ -601,34 +586,51 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     }
   } else {
     // ------------------------------------------------ softmax and output rows --
+    // A group of four warps has NC columns of every tile.  A thread holds, of every eight of
+    // them, two in the rows (tokens) lane / 4 + 8 i of its warp: what belongs to a column stays
+    // in registers.
+    constexpr int NC = S::NC, HALVES = TOK / 64, K = NC / 4;
     const int wq = warp & 3;                     // TMEM lane quarter of this warp
-    const int st = tid - 96;                     // 0 .. 127
+    const int grp = (warp - 3) >> 2, c_lo = grp * NC;
+    const int st = (tid - 96) & 127;             // thread of the group
     const uint32_t quarter = (uint32_t)(wq * 32) << 16;
-    // S^T of 64 tokens: sixteen lanes of each quarter hold a row
-    const bool has_row = TOK == 128 || lane < 16;
-    const int row = TOK == 128 ? wq * 32 + lane : wq * 16 + (lane & 15);
+    const int row0 = wq * (TOK / 4) + (lane >> 2);
+    const int pair = 2 * (lane & 3);
+    // row of element (half, q) and column of element (i, q), k = 2 i + (q & 1)
+    auto row_of = [&](int half, int q) { return row0 + 16 * half + 8 * (q >> 1); };
+    auto col_of = [&](int k) { return c_lo + 8 * (k >> 1) + pair + (k & 1); };
     const float sl2 = a.scale_log2;
     // fp16 weights stand 2^7 higher: below 2^-14 they would lose bits.  A weight is at most
     // 2^kRaise times that.
     constexpr float kShift = DT == PA_BFLOAT16 ? 0.f : 7.f;
-    float l[N];
+    // of the thread's columns: running maximum, what is added to a score before its power of
+    // two, sum of the weights of the thread's rows
+    float top[K], neg[K], l[K];
     int t = 0;
     auto wait_all = [&](uint64_t* bar, int parity) -> bool {
       return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kLimitNs));
     };
     // V . p of tile i; whoever has S of tile i + 1 or i knows that of tile i - 2 to be done
     auto wait_product = [&](int i) -> bool { return wait_all(&tail->o_done[i & 1], (i >> 1) & 1); };
-    auto sync = [&]() { named_barrier(1, 128); };
+    auto sync = [&]() { named_barrier(1 + grp, 128); };
+    // a column's value in all rows of the warp, from its lanes'
+    auto over_rows = [&](float x, auto&& f) -> float {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) x = f(x, __shfl_xor_sync(kAll, x, o));
+      return x;
+    };
+    auto larger = [](float x, float y) { return fmaxf(x, y); };
+    auto plus = [](float x, float y) { return x + y; };
     while (ok && walk.next(a, r, &g)) {
       if (!g.active) continue;
       const int ctx = g.L - g.n;
       // the columns of this item (those of the one before have been read)
       sync();
-      if (st < N) {
-        const int u = g.col0 + st, i = u / a.G;
+      if (st < NC) {
+        const int c = c_lo + st, u = g.col0 + c, i = u / a.G;
         const bool live = u < g.n * a.G;
-        tail->query[st] = live ? i : -1;
-        tail->out_at[st] =
+        tail->query[c] = live ? i : -1;
+        tail->out_at[c] =
             live ? ((int64_t)(g.qs + i) * a.Hq + g.h * a.G + (u - i * a.G)) * S::DV : -1;
       }
       sync();
@@ -643,135 +645,170 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         const int u = S::SHARED ? t : 2 * t + 1;              // the tile of V
         if (!wait_all(&tail->s_full[t & 1], (t >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
-        float s[N];
-        load_scores<N>(tmem + quarter + (t & 1) * N, s);
+        float s[HALVES][NC / 8][4];
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf)
+          load_scores<NC>(tmem + quarter + ((uint32_t)(16 * hf) << 16) + (t & 1) * N + c_lo, s[hf]);
         const uint64_t scale2 = f2_pack(sl2, sl2);
 #pragma unroll
-        for (int c = 0; c < N; c += 2)
-          f2_unpack(mul2(f2_pack(s[c], s[c + 1]), scale2), s[c], s[c + 1]);
-        const int tok = j * TOK + row;
-        if (!has_row || tok >= g.L) {
+        for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-          for (int c = 0; c < N; ++c) s[c] = -CUDART_INF_F;
-        } else if (tok >= ctx) {
+          for (int i = 0; i < NC / 8; ++i)
 #pragma unroll
-          for (int c = 0; c < N; ++c)
-            if (!sees(c, tok - ctx)) s[c] = -CUDART_INF_F;
+            for (int q = 0; q < 4; q += 2)
+              f2_unpack(mul2(f2_pack(s[hf][i][q], s[hf][i][q + 1]), scale2), s[hf][i][q],
+                        s[hf][i][q + 1]);
+        if ((j + 1) * TOK > ctx) {
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+            for (int i = 0; i < NC / 8; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int tok = j * TOK + row_of(hf, q);
+                if (tok >= ctx && (tok >= g.L || !sees(col_of(2 * i + (q & 1)), tok - ctx)))
+                  s[hf][i][q] = -CUDART_INF_F;
+              }
+        }
+        // the largest of a column in the thread's rows
+        float most[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          float m = fmaxf(s[0][k >> 1][k & 1], s[0][k >> 1][2 + (k & 1)]);
+          if (HALVES == 2)
+            m = fmax3(m, s[HALVES - 1][k >> 1][k & 1], s[HALVES - 1][k >> 1][2 + (k & 1)]);
+          most[k] = m;
         }
         bool raise = first;
         if (!first) {
-          float over = -CUDART_INF_F;
+          bool over = false;
 #pragma unroll
-          for (int c = 0; c < N; ++c) over = fmaxf(over, s[c] + tail->neg[c]);
-          raise = any_of_128(1, over > kRaise + kShift);
+          for (int k = 0; k < K; ++k) over = over || most[k] + neg[k] > kRaise + kShift;
+          raise = any_of(1 + grp, 128, over);
         }
         if (raise) {
-          reduce_columns<N>(s, tail->red[wq], lane, MaxOf());
-          sync();
-          if (st < N) {
-            const float before = first ? -CUDART_INF_F : tail->top[st];
-            const float now = fmaxf(before, fmaxf(fmaxf(tail->red[0][st], tail->red[1][st]),
-                                                  fmaxf(tail->red[2][st], tail->red[3][st])));
-            tail->top[st] = now;
-            tail->neg[st] = (now == -CUDART_INF_F ? 0.f : -now) + kShift;
-            tail->by[st] = before == -CUDART_INF_F ? 0.f : ex2_approx(before - now);
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const float m = over_rows(most[k], larger);
+            if (lane < 4) tail->red[wq][col_of(k)] = m;
           }
           sync();
-          if (first) {
+          float by[K];
 #pragma unroll
-            for (int c = 0; c < N; ++c) l[c] = 0.f;
-          } else {
+          for (int k = 0; k < K; ++k) {
+            const int c = col_of(k);
+            const float before = first ? -CUDART_INF_F : top[k];
+            top[k] = fmaxf(before, fmaxf(fmaxf(tail->red[0][c], tail->red[1][c]),
+                                         fmaxf(tail->red[2][c], tail->red[3][c])));
+            neg[k] = (top[k] == -CUDART_INF_F ? 0.f : -top[k]) + kShift;
+            by[k] = before == -CUDART_INF_F ? 0.f : ex2_approx(before - top[k]);
+            l[k] = first ? 0.f : l[k] * by[k];
+          }
+          if (!first) {
+            if (wq == 0 && lane < 4) {
 #pragma unroll
-            for (int c = 0; c < N; ++c) l[c] *= tail->by[c];
+              for (int k = 0; k < K; ++k) tail->by[col_of(k)] = by[k];
+            }
+            sync();
             // O (complete up to the tile before; this one's product waits for its weights)
             if (!wait_product(t - 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < S::VT * N; c0 += 16) {
-              float o[16];
-              tmem_ld16(ocol + quarter + c0, o);
-              uint32_t w[16];
+            for (int v = 0; v < S::VT; ++v)
+#pragma unroll 1
+              for (int c0 = c_lo; c0 < c_lo + NC; c0 += 16) {
+                float o[16];
+                tmem_ld16(ocol + quarter + v * N + c0, o);
+                uint32_t w[16];
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                w[c] = __float_as_uint(o[c] * tail->by[(c0 & (N - 1)) + c]);
-              tmem_st16_nowait(ocol + quarter + c0, w);
-            }
+                for (int c = 0; c < 16; ++c) w[c] = __float_as_uint(o[c] * tail->by[c0 + c]);
+                tmem_st16_nowait(ocol + quarter + v * N + c0, w);
+              }
             tmem_wait_st();
           }
         }
         // weights: to shared memory as rows of 64 columns, N-major, in storage-type terms
+        constexpr int PGS = S::SHARED ? S::GS : 1024;
+        uint8_t* weights = S::SHARED ? smem + (u % R) * S::UNIT + (S::QS - 1) * 1024
+                                     : smem + S::kPOff + (t & 1) * S::PBYTES;
 #pragma unroll
-        for (int c = 0; c < N; c += 2) {
-          f2_unpack(f2_add(f2_pack(s[c], s[c + 1]), f2_pack(tail->neg[c], tail->neg[c + 1])), s[c],
-                    s[c + 1]);
-          s[c] = ex2_approx(s[c]);
-          s[c + 1] = ex2_approx(s[c + 1]);
-          l[c] += s[c];
-          l[c + 1] += s[c + 1];
-        }
-        if (has_row) {
-          constexpr int PGS = S::SHARED ? S::GS : 1024;
-          uint8_t* prow = (S::SHARED ? smem + (u % R) * S::UNIT + (S::QS - 1) * 1024
-                                     : smem + S::kPOff + (t & 1) * S::PBYTES) +
-                          (row >> 3) * PGS + (row & 7) * 128;
+        for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-          for (int c = 0; c < N; c += 8) {
-            uint32_t hi[4], lo[4];
+          for (int q = 0; q < 4; q += 2) {
+            const int row = row_of(hf, q);
+            uint8_t* prow = weights + (row >> 3) * PGS + (row & 7) * 128 + (lane & 3) * 4;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = s[c + 2 * e], y = s[c + 2 * e + 1];
+            for (int i = 0; i < NC / 8; ++i) {
+              float x, y;
+              f2_unpack(f2_add(f2_pack(s[hf][i][q], s[hf][i][q + 1]),
+                               f2_pack(neg[2 * i], neg[2 * i + 1])), x, y);
+              x = ex2_approx(x);
+              y = ex2_approx(y);
+              l[2 * i] += x;
+              l[2 * i + 1] += y;
+              s[hf][i][q] = x;
+              s[hf][i][q + 1] = y;
+              const int chunk = (c_lo >> 3) + i;
+              uint32_t* hi = reinterpret_cast<uint32_t*>(prow + ((chunk ^ (row & 7)) << 4));
               if (S::TERMS == 1) {
-                hi[e] = pack2<DT>(x, y);
-              } else if (DT == PA_BFLOAT16) {
-                // the top 16 bits of a weight, then of what they leave
-                const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
-                hi[e] = __byte_perm(ux, uy, 0x7632);
-                lo[e] = __byte_perm(__float_as_uint(x - __uint_as_float(ux & 0xFFFF0000u)),
-                                    __float_as_uint(y - __uint_as_float(uy & 0xFFFF0000u)), 0x7632);
+                *hi = pack2<DT>(x, y);
               } else {
-                hi[e] = pack2<DT>(x, y);
-                const float2 f = widen2<DT>(hi[e]);
-                lo[e] = pack2<DT>(x - f.x, y - f.y);
+                uint32_t* lo = reinterpret_cast<uint32_t*>(
+                    N > 32 ? prow + TOK * 128 + ((chunk ^ (row & 7)) << 4)
+                           : prow + (((chunk + 4) ^ (row & 7)) << 4));
+                if (DT == PA_BFLOAT16) {
+                  // the top 16 bits of a weight, then of what they leave
+                  const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+                  *hi = __byte_perm(ux, uy, 0x7632);
+                  *lo = __byte_perm(__float_as_uint(x - __uint_as_float(ux & 0xFFFF0000u)),
+                                    __float_as_uint(y - __uint_as_float(uy & 0xFFFF0000u)),
+                                    0x7632);
+                } else {
+                  const uint32_t w = pack2<DT>(x, y);
+                  const float2 f = widen2<DT>(w);
+                  *hi = w;
+                  *lo = pack2<DT>(x - f.x, y - f.y);
+                }
               }
             }
-            const int chunk = c >> 3;
-            *reinterpret_cast<uint4*>(prow + ((chunk ^ (row & 7)) << 4)) =
-                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (S::TERMS == 2) {
-              uint8_t* to = N > 32 ? prow + TOK * 128 + ((chunk ^ (row & 7)) << 4)
-                                   : prow + (((chunk + 4) ^ (row & 7)) << 4);
-              *reinterpret_cast<uint4*>(to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
           }
-        }
-        // V of tokens behind the end, and of new tokens that not every column sees
+        // V of tokens behind the end, and of new tokens that not every column sees.  A row's
+        // slabs are shared out to the threads that look at it.
         const bool ends = (j + 1) * TOK > g.L;
         const bool fresh = g.n > 1 && (j + 1) * TOK > ctx;
         bool apart = false;
         if (ends || fresh) {
           if (!wait_all(&tail->full[u % R], (u / R) & 1)) { ok = false; break; }
+          constexpr int SIDES = TOK == 64 ? 2 : 1, PARTS = SIDES * S::GROUPS;
+          const int row = TOK == 64 ? wq * 16 + (lane & 15) : wq * 32 + lane;
+          const int mine = grp * SIDES + (TOK == 64 ? lane >> 4 : 0), tok = j * TOK + row;
           uint8_t* vrow = smem + (u % R) * S::UNIT + (row >> 3) * S::VGS + (row & 7) * 128;
-          bool zero = has_row && tok >= g.L;
+          auto at = [&](int x) { return vrow + (x >> 3) * 1024 + (x & 7) * 16; };
+          bool zero = tok >= g.L;
           if (fresh) {
             bool odd = false;
-            if (has_row && tok >= ctx && tok < g.L) {
+            if (tok >= ctx && tok < g.L) {
 #pragma unroll 4
-              for (int x = 0; x < 8 * S::VS; ++x) {
-                const uint4 w = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 +
-                                                                (x & 7) * 16);
+              for (int x = mine; x < 8 * S::VS; x += PARTS) {
+                const uint4 w = *reinterpret_cast<const uint4*>(at(x));
                 odd = odd || odd2<DT>(w.x) || odd2<DT>(w.y) || odd2<DT>(w.z) || odd2<DT>(w.w);
               }
             }
-            zero = zero || odd;
             const uint32_t rows = __ballot_sync(kAll, odd);
-            if (lane == 0) tail->odd[wq] = rows;
-            apart = any_of_128(1, odd);
+            if (lane == 0) tail->odd[grp][wq] = rows;
+            apart = any_of(3, 128 * S::GROUPS, odd);
+            if (apart) {
+              uint32_t both = 0;
+#pragma unroll
+              for (int i = 0; i < S::GROUPS; ++i) both |= tail->odd[i][wq];
+              if (TOK == 64) both |= both >> 16;
+              zero = zero || (both >> (row & (TOK / 4 - 1)) & 1);
+            }
           }
           if (zero) {
 #pragma unroll 4
-            for (int x = 0; x < 8 * S::VS; ++x)
-              *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + (x & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
+            for (int x = mine; x < 8 * S::VS; x += PARTS)
+              *reinterpret_cast<uint4*>(at(x)) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_async_smem();
@@ -784,15 +821,23 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           tc_fence_after();
 #pragma unroll 1
           for (int w = 0; w < 4; ++w) {
-            uint32_t rows = tail->odd[w];
-            while (rows) {
-              const int x = __ffs(rows) - 1;
-              rows &= rows - 1;
-              const int at = j * TOK + (TOK == 128 ? w * 32 + x : w * 16 + x);
-              if (wq == w && lane == x) {
+            uint32_t rows = 0;
 #pragma unroll
-                for (int c = 0; c < N; ++c) tail->share[c] = sees(c, at - ctx) ? s[c] : -1.f;
-              }
+            for (int i = 0; i < S::GROUPS; ++i) rows |= tail->odd[i][w];
+            if (TOK == 64) rows = (rows | rows >> 16) & 0xFFFFu;
+            while (rows) {
+              const int x = w * (TOK / 4) + __ffs(rows) - 1, at = j * TOK + x;
+              rows &= rows - 1;
+#pragma unroll
+              for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+                for (int i = 0; i < NC / 8; ++i)
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    if (row_of(hf, q) == x) {
+                      const int c = col_of(2 * i + (q & 1));
+                      tail->share[c] = sees(c, at - ctx) ? s[hf][i][q] : -1.f;
+                    }
               sync();
               const int id = a.tables[(int64_t)g.b * a.max_blocks + (at >> a.bs_shift)];
               const int64_t slot = ((int64_t)id << a.bs_shift) + (at & ((1 << a.bs_shift) - 1));
@@ -804,7 +849,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
                 const int dim = v * S::VM + (S::VM == 128 ? wq * 32 + lane : wq * 16 + (lane & 15));
                 const float val = widen2<DT>(vsrc[dim]).x;
 #pragma unroll 1
-                for (int c0 = 0; c0 < N; c0 += 16) {
+                for (int c0 = c_lo; c0 < c_lo + NC; c0 += 16) {
                   float o[16];
                   tmem_ld16(ocol + quarter + v * N + c0, o);
                   uint32_t ow[16];
@@ -821,22 +866,29 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
             }
           }
           tc_fence_before();
+          named_barrier(3, 128 * S::GROUPS);     // every thread has read the rows' words
         }
         if (!last) continue;
 
         // ------------------------------------------------------- the segment's end --
         const bool whole = g.j0 == 0 && g.j1 == g.nt;
         const int64_t part = 2 * (int64_t)blockIdx.x + g.part;
-        reduce_columns<N>(l, tail->red[wq], lane, SumOf());
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const float sum = over_rows(l[k], plus);
+          if (lane < 4) tail->sum[wq][col_of(k)] = sum;
+        }
+        if (!whole && wq == 0 && lane < 4) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) a.ws_m[part * N + col_of(k)] = top[k];
+        }
         sync();
-        if (st < N) {
-          const float sum = (tail->red[0][st] + tail->red[1][st]) +
-                            (tail->red[2][st] + tail->red[3][st]);
-          tail->by[st] = sum == 0.f ? 0.f : 1.f / sum;
-          if (!whole) {
-            a.ws_m[part * N + st] = tail->top[st];
-            a.ws_l[part * N + st] = sum;
-          }
+        if (st < NC) {
+          const int c = c_lo + st;
+          const float sum = (tail->sum[0][c] + tail->sum[1][c]) +
+                            (tail->sum[2][c] + tail->sum[3][c]);
+          tail->by[c] = sum == 0.f ? 0.f : 1.f / sum;
+          if (!whole) a.ws_l[part * N + c] = sum;
         }
         if (!wait_product(t)) { ok = false; break; }
         sync();
@@ -846,7 +898,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         for (int v = 0; v < S::VT; ++v) {
           const int dim = v * S::VM + (S::VM == 128 ? wq * 32 + lane : wq * 16 + (lane & 15));
 #pragma unroll 1
-          for (int c0 = 0; c0 < N; c0 += 16) {
+          for (int c0 = c_lo; c0 < c_lo + NC; c0 += 16) {
             float o[16];
             tmem_ld16(ocol + quarter + v * N + c0, o);
             if (whole) {
@@ -1073,7 +1125,7 @@ cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, in
       if (device < 64) done |= 1ull << device;
     }
   }
-  cudaError_t e = launch_pdl(multi_kernel<S, DT>, dim3((unsigned)ctas), kThreads, S::kSmem, stream,
+  cudaError_t e = launch_pdl(multi_kernel<S, DT>, dim3((unsigned)ctas), S::kThreads, S::kSmem, stream,
                              k, v, a);
   const int sets = ctas / a.gs;
   if (e != cudaSuccess || !cut || sets < 2) return e;
