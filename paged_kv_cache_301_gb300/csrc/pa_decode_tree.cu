@@ -31,8 +31,9 @@ static pa_status check_tree(int num_q_heads, int num_kv_heads, int head_dim, int
 extern "C" size_t pa_decode_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim,
                                                  int max_q_len) {
   if (check_tree(num_q_heads, num_kv_heads, head_dim, max_q_len) != PA_OK) return 0;
-  const int64_t most = (int64_t)(max_q_len > 1 ? max_q_len : 1) * (num_q_heads / num_kv_heads);
-  return multi::layout_of(multi::columns_for(most).n, head_dim).total;
+  return multi::layout_of(
+             multi::columns_for(max_q_len > 1 ? max_q_len : 1, num_q_heads / num_kv_heads).n,
+             head_dim).total;
 }
 
 extern "C" pa_status pa_decode_tree(void* out, const void* q, const void* k_pool,

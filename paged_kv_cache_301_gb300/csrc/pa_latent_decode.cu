@@ -31,8 +31,8 @@ static pa_status check_latent(int num_q_heads, int latent_dim, int rope_dim, int
 extern "C" size_t pa_latent_decode_workspace_bytes(int num_q_heads, int latent_dim, int rope_dim,
                                                    int max_q_len) {
   if (check_latent(num_q_heads, latent_dim, rope_dim, max_q_len) != PA_OK) return 0;
-  const int64_t most = (int64_t)(max_q_len > 1 ? max_q_len : 1) * num_q_heads;
-  return multi::layout_of(multi::columns_for(most).n, latent_dim).total;
+  return multi::layout_of(multi::columns_for(max_q_len > 1 ? max_q_len : 1, num_q_heads).n,
+                          latent_dim).total;
 }
 
 extern "C" pa_status pa_latent_decode(void* out, const void* q, const void* pool,

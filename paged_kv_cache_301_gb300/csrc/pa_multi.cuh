@@ -29,7 +29,7 @@
 // 0 times those is no zero: such a row is zeroed too, and what it gives to the columns that
 // see it is added by the softmax warps (rare, and as slow as it may be).
 //
-// Roles: warp 0 block ids and TMA; warp 1 TMEM and MMA issue; warp 2 loads q; the others, one or
+// Roles: warp 0 block ids and TMA; warp 1 TMEM and MMA issue; warp 2 q; the others, one or
 // two groups of four with columns of their own, softmax and output.  Every wait is bounded; one
 // that runs out sets an abort flag, copies and MMAs in flight are drained, TMEM is freed and
 // PA_ERR_TIMEOUT is reported through status_dev.
@@ -65,6 +65,8 @@ struct Args {
   const int32_t* q_start;
   const int32_t* mask;
   int B, total_q, Hq, H, G, bs_shift, max_blocks, num_blocks, max_q, words, max_len;
+  // columns of a group: gh heads of gn new tokens each; a KV head's heads are `chunks` of gh
+  int gh, gn, chunks;
   int gs;                        // CTAs of a set: column groups of an item
   float scale_log2;
   Window* info;                  // [sets]
@@ -124,6 +126,7 @@ struct Tail {
   Place start;
   int64_t out_at[S::N];          // element of out where a column's row begins, -1: none
   int query[S::N];               // the column's new token, -1: none
+  uint32_t seen[S::N][S::TOK / 32];        // what it sees of a tile, a bit of a token
   float by[S::N];                // 2^(maximum before - now), then 1 / the weights' sum
   float red[4][S::N];            // per warp: columns' maxima
   float sum[4][S::N];            // per warp: columns' sums of weights
@@ -136,6 +139,11 @@ struct Tail {
 struct Seq {
   int L, n, qs, nt, items;
 };
+
+// Column groups of n new tokens.
+__device__ __forceinline__ int groups_of(const Args& a, int n) {
+  return (n + a.gn - 1) / a.gn * a.chunks;
+}
 
 // A sequence's lengths and work; nt 0: none.  *bad: it is skipped and reported.
 template <class S>
@@ -152,14 +160,13 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, bool* bad) {
          (int64_t)s.L > ((int64_t)a.max_blocks << a.bs_shift) || s.qs < 0 || s.n < 0 ||
          s.n > a.max_q || s.n > a.total_q - s.qs || (a.q_start && s.n > s.L);
   s.nt = *bad || s.n == 0 ? 0 : (s.L + S::TOK - 1) / S::TOK;
-  const int wide = S::N * a.gs;
-  s.items = s.nt == 0 ? 0 : a.H * ((s.n * a.G + wide - 1) / wide);
+  s.items = s.nt == 0 ? 0 : a.H * ((groups_of(a, s.n) + a.gs - 1) / a.gs);
   return s;
 }
 
 // Walks the segments of a window: its part of one item after another.
 struct Segment {
-  int b, h, col0, j0, j1, nt, L, n, qs;
+  int b, h, i0, g0, j0, j1, nt, L, n, qs;       // i0, g0: the group's first token and head
   int part;                      // 0: the window's first segment, else 1
   bool active;                   // the CTA's column group has a column
 };
@@ -188,8 +195,10 @@ struct Walk {
     const int pairs = s.items / a.H;
     g->b = b;
     g->h = item / pairs;
-    g->col0 = ((item - g->h * pairs) * a.gs + r) * S::N;
-    g->active = g->col0 < s.n * a.G;
+    const int group = (item - g->h * pairs) * a.gs + r, i = group / a.chunks;
+    g->i0 = i * a.gn;
+    g->g0 = (group - i * a.chunks) * a.gh;
+    g->active = g->i0 < s.n;
     g->j0 = j;
     g->j1 = s.nt - j <= left ? s.nt : j + left;
     g->nt = s.nt;
@@ -225,10 +234,28 @@ __device__ __forceinline__ void tma_block_head(void* dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 16 : 0)
-               : "memory");
+// One slab of q: [new tokens][heads][64].
+__device__ __forceinline__ void tma_q(void* dst, const CUtensorMap* map, uint64_t* bar, int head,
+                                      int row, int slab) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(head), "r"(row),
+      "r"(slab)
+      : "memory");
+}
+
+// Has the phase of this parity completed?  Does not wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Is any of `count` threads' predicates true?
@@ -290,7 +317,7 @@ __device__ __forceinline__ bool odd2(uint32_t w) {
 template <class S, int DT>
 __global__ void __launch_bounds__(S::kThreads, 1)
 multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-             const Args a) {
+             const __grid_constant__ CUtensorMap map_q, const Args a) {
   constexpr int N = S::N, R = S::RING, QB = S::QBUFS, TOK = S::TOK, kThreads = S::kThreads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -323,10 +350,17 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&map_k);
     if (!S::SHARED) tma_prefetch_desc(&map_v);
+    tma_prefetch_desc(&map_q);
   }
   if (warp == 1) {
     tmem_alloc(&tail->tmem, S::kCols);
     tmem_relinquish();
+  }
+  // rows of q that no copy writes
+  if (a.gh * a.gn < N) {
+    for (int i = tid; i < QB * S::QBYTES / 16; i += kThreads)
+      reinterpret_cast<uint4*>(smem + S::kQOff)[i] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
   }
   wait_prior_grid();
 
@@ -461,12 +495,15 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issue --
-    // K . q of tile t, then V . p of tile t - 1: the softmax of a tile runs while the tensor
-    // cores have the next tile's scores.  Where an item begins, q may still be on its way, so
-    // V . p goes first.
+    // V . p of tile t - 1 goes before or behind K . q of tile t, whichever can begin first: the
+    // softmax of a tile runs while the tensor cores have the next one's scores, and where the
+    // next tile is still on its way, the product frees the ring for the one behind it.
+    // One thread issues every product, so descriptors are built once a tile and stepped by
+    // constants (the start-address field holds address / 16).
     constexpr uint32_t ab = DT == PA_BFLOAT16 ? 1u : 0u;
     constexpr uint32_t idesc_s = idesc_f16(ab, 0, 0, TOK, N);
     constexpr uint32_t idesc_o = idesc_f16(ab, 1, 1, S::VM, N);
+    constexpr int PGS = S::SHARED ? S::GS : 1024;
     if (lane == 0) {
       int t = 0, seg = 0;
       bool prev_first = false;
@@ -482,20 +519,24 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           return false;
         tc_fence_after();
         const uint32_t va = ring + (u % R) * S::UNIT;
-        const uint32_t pw = S::SHARED ? va + (S::QS - 1) * 1024
-                                      : smem_addr(smem + S::kPOff + slot * S::PBYTES);
-        constexpr int PGS = S::SHARED ? S::GS : 1024;
+        const uint64_t vd = smem_desc_sw128(va, 1024, S::VGS);
+        const uint64_t pd = smem_desc_sw128(S::SHARED ? va + (S::QS - 1) * 1024
+                                                      : smem_addr(smem + S::kPOff) +
+                                                            slot * S::PBYTES,
+                                            1024, PGS);
+        uint32_t more = !prev_first;
 #pragma unroll
-        for (int v = 0; v < S::VT; ++v)
+        for (int k = 0; k < TOK / 16; ++k)
 #pragma unroll
-          for (int k = 0; k < TOK / 16; ++k)
+          for (int term = 0; term < S::TERMS; ++term) {
 #pragma unroll
-            for (int term = 0; term < S::TERMS; ++term)
+            for (int v = 0; v < S::VT; ++v)
               mma_f16(ocol + v * N,
-                      smem_desc_sw128(va + v * (S::VM / 64) * 1024 + k * 2 * S::VGS, 1024, S::VGS),
-                      smem_desc_sw128(pw + k * 2 * PGS + term * (N > 32 ? TOK * 128 : 64), 1024,
-                                      PGS),
-                      idesc_o, !prev_first || (k | term) != 0);
+                      vd + (uint64_t)((v * (S::VM / 64) * 1024 + k * 2 * S::VGS) >> 4),
+                      pd + (uint64_t)((k * 2 * PGS + term * (N > 32 ? TOK * 128 : 64)) >> 4),
+                      idesc_o, more);
+            more = 1;
+          }
         mma_commit(&tail->empty[u % R]);
         mma_commit(&tail->o_done[slot]);
         return true;
@@ -506,22 +547,33 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         for (int j = g.j0; j < g.j1 && ok; ++j) {
           const int u = S::SHARED ? t : 2 * t;
           const bool first = j == g.j0;
-          if (first && t > 0) ok = issue_pv(t - 1);
-          ok = ok && (!first || mbar_wait(&tail->q_full[qs], (seg / QB) & 1, abort_flag, kLimitNs)) &&
-               mbar_wait(&tail->full[u % R], (u / R) & 1, abort_flag, kLimitNs);
+          bool left = t > 0;                     // the product of tile t - 1 is not issued
+          uint64_t* bars[2] = {&tail->full[u % R], &tail->q_full[qs]};
+          const uint32_t parity[2] = {(uint32_t)((u / R) & 1), (uint32_t)((seg / QB) & 1)};
+          for (int i = 0; i < (first ? 2 : 1) && ok; ++i) {
+            while (left && !mbar_test(bars[i], parity[i])) {
+              if (mbar_test(&tail->p_full[(t - 1) & 1], ((t - 1) >> 1) & 1)) {
+                ok = issue_pv(t - 1);
+                left = false;
+              } else if (*abort_flag) {
+                break;
+              }
+            }
+            ok = ok && mbar_wait(bars[i], parity[i], abort_flag, kLimitNs);
+          }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ka = ring + (u % R) * S::UNIT, qa = qb + qs * S::QBYTES;
+          const uint64_t kd = smem_desc_sw128(ring + (u % R) * S::UNIT, 16, S::GS);
+          const uint64_t qd = smem_desc_sw128(qb + qs * S::QBYTES, 16, 1024);
+          const uint32_t scol = tmem + (t & 1) * N;
 #pragma unroll
           for (int k = 0; k < 4 * S::QS; ++k)
-            mma_f16(tmem + (t & 1) * N,
-                    smem_desc_sw128(ka + (k >> 2) * 1024 + (k & 3) * 32, 16, S::GS),
-                    smem_desc_sw128(qa + (k >> 2) * (N * 128) + (k & 3) * 32, 16, 1024), idesc_s,
-                    k > 0);
+            mma_f16(scol, kd + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                    qd + (uint64_t)(((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_s, k > 0);
           if (!S::SHARED) mma_commit(&tail->empty[u % R]);
           mma_commit(&tail->s_full[t & 1]);
           if (j + 1 == g.j1) mma_commit(&tail->q_empty[qs]);
-          if (!first) ok = issue_pv(t - 1);
+          if (left) ok = issue_pv(t - 1);
           prev_first = first;
           prev_seg = seg;
           ++t;
@@ -551,27 +603,22 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         ok = __all_sync(kAll, ok);
         if (!ok) break;
       }
-      const int cols = g.n * a.G;
-      for (int c = 0; c < N; ++c) {
-        const int u = g.col0 + c;
-        const bool live = u < cols;
-        const int i = live ? u / a.G : 0, head = g.h * a.G + (live ? u - i * a.G : 0);
-        const uint8_t* row = static_cast<const uint8_t*>(a.q) +
-                             ((int64_t)(g.qs + i) * a.Hq + head) * (S::QS * 128);
-        for (int x = lane; x < 8 * S::QS; x += 32)
-          cp_async16(qb + slot * S::QBYTES + (x >> 3) * (N * 128) + c * 128 +
-                         (((x & 7) ^ (c & 7)) << 4),
-                     row + x * 16, live);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&tail->q_full[slot], (uint32_t)(S::QS * a.gh * a.gn * 128));
+        for (int x = 0; x < S::QS; ++x)
+          tma_q(smem + S::kQOff + slot * S::QBYTES + x * (N * 128), &map_q, &tail->q_full[slot],
+                g.h * a.G + g.g0, g.qs + g.i0, x);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->q_full[slot]);
       ++seg;
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
       report(a.status_dev, PA_ERR_TIMEOUT);
+    }
+    if (*abort_flag && lane == 0) {             // copies in flight land before the CTA ends
+      for (int i = max(0, seg - QB); i < seg; ++i)
+        mbar_wait_drain(&tail->q_full[i % QB], (i / QB) & 1, kLimitNs);
     }
     // sequences without work: empty ones of a step without q_start, and bad ones
     for (int b = (int)blockIdx.x; b < a.B; b += (int)gridDim.x) {
@@ -607,8 +654,10 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     // two, sum of the weights of the thread's rows
     float top[K], neg[K], l[K];
     int t = 0;
+    // These waits end by time alone, not by the abort flag: the warps of a group wait for the
+    // same barriers, so they give up together and none is left at a barrier of theirs.
     auto wait_all = [&](uint64_t* bar, int parity) -> bool {
-      return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kLimitNs));
+      return __all_sync(kAll, mbar_try_wait(bar, parity) || mbar_wait_drain(bar, parity, kLimitNs));
     };
     // V . p of tile i; whoever has S of tile i + 1 or i knows that of tile i - 2 to be done
     auto wait_product = [&](int i) -> bool { return wait_all(&tail->o_done[i & 1], (i >> 1) & 1); };
@@ -627,24 +676,44 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
       // the columns of this item (those of the one before have been read)
       sync();
       if (st < NC) {
-        const int c = c_lo + st, u = g.col0 + c, i = u / a.G;
-        const bool live = u < g.n * a.G;
+        const int c = c_lo + st, x = c / a.gh, i = g.i0 + x, head = g.g0 + c - x * a.gh;
+        const bool live = x < a.gn && i < g.n && head < a.G;
         tail->query[c] = live ? i : -1;
-        tail->out_at[c] =
-            live ? ((int64_t)(g.qs + i) * a.Hq + g.h * a.G + (u - i * a.G)) * S::DV : -1;
+        tail->out_at[c] = live ? ((int64_t)(g.qs + i) * a.Hq + g.h * a.G + head) * S::DV : -1;
       }
       sync();
-      auto sees = [&](int c, int jj) -> bool {
-        const int i = tail->query[c];
-        if (i < 0) return false;
-        return a.mask ? (a.mask[(int64_t)(g.qs + i) * a.words + (jj >> 5)] >> (jj & 31)) & 1
-                      : jj <= i;
-      };
       for (int j = g.j0; j < g.j1; ++j, ++t) {
         const bool first = j == g.j0, last = j + 1 == g.j1;
         const int u = S::SHARED ? t : 2 * t + 1;              // the tile of V
+        const bool edge = (j + 1) * TOK > ctx;               // new tokens, or behind the end
+        if (edge && st < NC) {
+          // what a column sees of this tile: of each 32 tokens the older ones, the new ones of
+          // its set, none behind the end
+          const int i = tail->query[c_lo + st];
+          const int32_t* set = a.mask + (int64_t)(g.qs + max(i, 0)) * a.words;
+#pragma unroll
+          for (int w = 0; w < TOK / 32; ++w) {
+            const int lo = j * TOK + 32 * w - ctx;           // the new token of bit 0
+            const int ends_at = g.L - j * TOK - 32 * w;
+            uint32_t bits;
+            if (a.mask) {
+              // words x and x + 1 of the set, from bit lo - 32 x on
+              const int x = lo >> 5;
+              const uint32_t w0 = x < 0 ? kAll : (x < a.words ? (uint32_t)set[x] : 0u);
+              const uint32_t w1 = x + 1 < 0 ? kAll : (x + 1 < a.words ? (uint32_t)set[x + 1] : 0u);
+              bits = __funnelshift_r(w0, w1, lo & 31);
+            } else {
+              const int n = i + 1 - lo;                      // a chain: new tokens up to i
+              bits = n <= 0 ? 0u : (n >= 32 ? kAll : (1u << n) - 1);
+            }
+            if (lo < 0) bits |= lo <= -32 ? kAll : (1u << -lo) - 1;
+            if (ends_at < 32) bits &= ends_at <= 0 ? 0u : (1u << ends_at) - 1;
+            tail->seen[c_lo + st][w] = bits;
+          }
+        }
         if (!wait_all(&tail->s_full[t & 1], (t >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
+        if (edge) sync();
         float s[HALVES][NC / 8][4];
 #pragma unroll
         for (int hf = 0; hf < HALVES; ++hf)
@@ -658,17 +727,17 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
             for (int q = 0; q < 4; q += 2)
               f2_unpack(mul2(f2_pack(s[hf][i][q], s[hf][i][q + 1]), scale2), s[hf][i][q],
                         s[hf][i][q + 1]);
-        if ((j + 1) * TOK > ctx) {
+        if (edge) {
 #pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf)
+          for (int k = 0; k < K; ++k) {
+            // the thread's rows stand in one word
+            const uint32_t bits = tail->seen[col_of(k)][row0 >> 5] >> (row0 & 31);
 #pragma unroll
-            for (int i = 0; i < NC / 8; ++i)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int tok = j * TOK + row_of(hf, q);
-                if (tok >= ctx && (tok >= g.L || !sees(col_of(2 * i + (q & 1)), tok - ctx)))
-                  s[hf][i][q] = -CUDART_INF_F;
-              }
+            for (int hf = 0; hf < HALVES; ++hf) {
+              if (!(bits >> (16 * hf) & 1)) s[hf][k >> 1][k & 1] = -CUDART_INF_F;
+              if (!(bits >> (16 * hf + 8) & 1)) s[hf][k >> 1][2 + (k & 1)] = -CUDART_INF_F;
+            }
+          }
         }
         // the largest of a column in the thread's rows
         float most[K];
@@ -836,7 +905,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
                   for (int q = 0; q < 4; ++q)
                     if (row_of(hf, q) == x) {
                       const int c = col_of(2 * i + (q & 1));
-                      tail->share[c] = sees(c, at - ctx) ? s[hf][i][q] : -1.f;
+                      tail->share[c] = tail->seen[c][x >> 5] >> (x & 31) & 1 ? s[hf][i][q] : -1.f;
                     }
               sync();
               const int id = a.tables[(int64_t)g.b * a.max_blocks + (at >> a.bs_shift)];
@@ -972,8 +1041,9 @@ join_kernel(const Args a, int sets, int cols) {
   bool bad;
   const Seq s = seq_of<S>(a, at.b, &bad);
   const int pairs = s.items / a.H, h = at.item / pairs;
-  const int col0 = ((at.item - h * pairs) * a.gs + r) * N;
-  const int n = min(N, s.n * a.G - col0);
+  const int group = (at.item - h * pairs) * a.gs + r, i0 = group / a.chunks * a.gn;
+  const int g0 = group % a.chunks * a.gh;
+  const int n = a.gh * min(a.gn, s.n - i0);              // none, for a group without columns
   // row of part k in ws_m and ws_l
   auto row = [&](int k) -> int64_t {
     const int cta = (c - 1 + k) * a.gs + r;
@@ -1035,10 +1105,11 @@ join_kernel(const Args a, int sets, int cols) {
     }
     if (ps == 0 && c0 + col < end) {
       if (s_none[col]) sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int u = col0 + c0 + col, i = u / a.G;
-      const int64_t to = ((int64_t)(s.qs + i) * a.Hq + h * a.G + (u - i * a.G)) * DV + d;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
-          make_uint2(pack2<DT>(sum.x, sum.y), pack2<DT>(sum.z, sum.w));
+      const int x = (c0 + col) / a.gh, head = g0 + c0 + col - x * a.gh;
+      const int64_t to = ((int64_t)(s.qs + i0 + x) * a.Hq + h * a.G + head) * DV + d;
+      if (head < a.G)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
+            make_uint2(pack2<DT>(sum.x, sum.y), pack2<DT>(sum.z, sum.w));
     }
     __syncthreads();
   }
@@ -1084,16 +1155,38 @@ inline bool encode_blocks(CUtensorMap* map, const void* pool, int dtype, int64_t
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Columns of a product for the most (new token, query head) pairs that an item can have, and
-// CTAs of a set.
+// Queries [T, heads, 64 slabs] as [slabs][T][heads][64]; a box is a group of columns.
+inline bool encode_q(CUtensorMap* map, const void* q, int dtype, int64_t rows, int heads, int slabs,
+                     int gh, int gn) {
+  const cuuint64_t row = (cuuint64_t)slabs * 128;
+  const cuuint64_t dims[4] = {64, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)slabs};
+  const cuuint64_t strides[3] = {row, row * heads, 128};
+  const cuuint32_t box[4] = {64, (cuuint32_t)gh, (cuuint32_t)gn, 1}, ones[4] = {1, 1, 1, 1};
+  return encode_fn()(map,
+                     dtype == PA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                     4, const_cast<void*>(q), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How the (new token, query head) pairs of a KV head become columns, by the most new tokens of
+// a sequence and the query heads of a KV head: n columns of a product, of gh heads of gn new
+// tokens; gs CTAs to a set.
 struct Columns {
-  int n, gs;
+  int n, gh, gn, chunks, gs;
 };
 
-inline Columns columns_for(int64_t most) {
-  if (most <= 16) return {16, 1};
-  if (most <= 32) return {32, 1};
-  return {64, most <= 64 ? 1 : 2};
+inline Columns columns_for(int most, int G) {
+  Columns c;
+  const int64_t all = (int64_t)most * G;
+  c.n = all <= 16 ? 16 : (all <= 32 ? 32 : 64);
+  c.chunks = (G + c.n - 1) / c.n;
+  c.gh = (G + c.chunks - 1) / c.chunks;
+  c.gn = c.n / c.gh;
+  c.gs = most > c.gn || c.chunks > 1 ? 2 : 1;
+  return c;
 }
 
 struct Layout {
@@ -1112,8 +1205,8 @@ inline Layout layout_of(int n, int dv) {
 }
 
 template <class S, int DT>
-cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, int ctas,
-                   int64_t items, bool cut, int device, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap (&maps)[3], const Args& a, int ctas, int64_t items, bool cut,
+                   int device, cudaStream_t stream) {
   static std::mutex lock;
   static uint64_t done = 0;                    // devices whose attribute is set
   {
@@ -1126,7 +1219,7 @@ cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, in
     }
   }
   cudaError_t e = launch_pdl(multi_kernel<S, DT>, dim3((unsigned)ctas), S::kThreads, S::kSmem, stream,
-                             k, v, a);
+                             maps[0], maps[1], maps[2], a);
   const int sets = ctas / a.gs;
   if (e != cudaSuccess || !cut || sets < 2) return e;
   // few items of many parts: the parts of a few columns to a CTA, else many columns
@@ -1144,11 +1237,11 @@ cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, in
 
 // The shape of N columns.
 template <template <int> class Of, int DT>
-cudaError_t launch_columns(int n, const CUtensorMap& k, const CUtensorMap& v, const Args& a,
-                           int ctas, int64_t items, bool cut, int device, cudaStream_t stream) {
-  if (n == 16) return launch<Of<16>, DT>(k, v, a, ctas, items, cut, device, stream);
-  if (n == 32) return launch<Of<32>, DT>(k, v, a, ctas, items, cut, device, stream);
-  return launch<Of<64>, DT>(k, v, a, ctas, items, cut, device, stream);
+cudaError_t launch_columns(int n, const CUtensorMap (&maps)[3], const Args& a, int ctas,
+                           int64_t items, bool cut, int device, cudaStream_t stream) {
+  if (n == 16) return launch<Of<16>, DT>(maps, a, ctas, items, cut, device, stream);
+  if (n == 32) return launch<Of<32>, DT>(maps, a, ctas, items, cut, device, stream);
+  return launch<Of<64>, DT>(maps, a, ctas, items, cut, device, stream);
 }
 
 // What a call asks for, checked but for the sizes of its own cache.
@@ -1195,8 +1288,9 @@ inline pa_status check(const Call& c, size_t workspace_needed, bool* work) {
 template <class F>
 pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f) {
   const int max_q = c.q_start ? c.max_q : 1, G = c.Hq / c.H;
-  const Columns cols = columns_for((int64_t)max_q * G);
-  const int64_t groups = ((int64_t)max_q * G + cols.n * cols.gs - 1) / (cols.n * cols.gs);
+  const Columns cols = columns_for(max_q, G);
+  const int64_t groups =                       // pairs of column groups
+      (((int64_t)max_q + cols.gn - 1) / cols.gn * cols.chunks + cols.gs - 1) / cols.gs;
   const int64_t nt = ((int64_t)c.max_len + tok - 1) / tok;
   const int64_t items = (int64_t)c.B * c.H * groups;
   int device = 0, sms = 0;
@@ -1206,9 +1300,10 @@ pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f)
   int64_t sets = (sms < kMaxCtas ? sms : kMaxCtas) / cols.gs;
   if (items > (1ll << 31) || (items * nt) / sets >= (1ll << 30)) return PA_ERR_INVALID_ARG;
   if (items * nt < sets) sets = items * nt > 0 ? items * nt : 1;
-  CUtensorMap k, v;
-  if (!encode_blocks(&k, c.k_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||
-      !encode_blocks(&v, c.v_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs))
+  CUtensorMap maps[3];
+  if (!encode_blocks(&maps[0], c.k_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||
+      !encode_blocks(&maps[1], c.v_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||
+      !encode_q(&maps[2], c.q, c.dtype, c.total_q, c.Hq, slabs, cols.gh, cols.gn))
     return PA_ERR_INVALID_ARG;
   const Layout y = layout_of(cols.n, dv);
   char* ws = static_cast<char*>(c.workspace);
@@ -1231,6 +1326,9 @@ pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f)
   a.max_q = max_q;
   a.words = c.words;
   a.max_len = c.max_len;
+  a.gh = cols.gh;
+  a.gn = cols.gn;
+  a.chunks = cols.chunks;
   a.gs = cols.gs;
   a.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
   a.info = reinterpret_cast<Window*>(ws);
@@ -1239,7 +1337,7 @@ pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f)
   a.ws_acc = reinterpret_cast<float*>(ws + y.acc_off);
   a.status_dev = c.status_dev;
   // an item of one tile is never cut
-  const cudaError_t e = f(cols.n, k, v, a, (int)(sets * cols.gs), items, nt > 1, device);
+  const cudaError_t e = f(cols.n, maps, a, (int)(sets * cols.gs), items, nt > 1, device);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
