@@ -245,6 +245,30 @@ __device__ __forceinline__ void tma_q(void* dst, const CUtensorMap* map, uint64_
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem] by one lane of a whole warp.  With warp-uniform descriptors a
+// product is issued in 21 cycles, from a branch of one lane in 44 or more; a product takes 24
+// (64 rows, 16 columns) to 49 (128 rows, 64 columns).
+__device__ __forceinline__ void mma_by_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The lane that issues the products arrives on `bar` once all of them have completed.
+__device__ __forceinline__ void commit_by_one(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+
 // Has the phase of this parity completed?  Does not wait.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -325,7 +349,8 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
   static_assert(sizeof(Tail<S>) <= S::kTailBytes, "barrier block");
   Tail<S>* tail = reinterpret_cast<Tail<S>*>(smem + S::kTailOff);
   volatile int* abort_flag = &tail->abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kAll, tid >> 5, 0);           // uniform, and known to be
   const int set = (int)blockIdx.x / a.gs, r = (int)blockIdx.x - set * a.gs;
   const int sets = (int)gridDim.x / a.gs;
 
@@ -498,24 +523,25 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     // V . p of tile t - 1 goes before or behind K . q of tile t, whichever can begin first: the
     // softmax of a tile runs while the tensor cores have the next one's scores, and where the
     // next tile is still on its way, the product frees the ring for the one behind it.
-    // One thread issues every product, so descriptors are built once a tile and stepped by
-    // constants (the start-address field holds address / 16).
+    // Descriptors are built once a tile and stepped by constants (the start-address field holds
+    // address / 16), and the whole warp runs along, so that they stay uniform.
     constexpr uint32_t ab = DT == PA_BFLOAT16 ? 1u : 0u;
     constexpr uint32_t idesc_s = idesc_f16(ab, 0, 0, TOK, N);
     constexpr uint32_t idesc_o = idesc_f16(ab, 1, 1, S::VM, N);
     constexpr int PGS = S::SHARED ? S::GS : 1024;
-    if (lane == 0) {
+    {
       int t = 0, seg = 0;
       bool prev_first = false;
       int prev_seg = 0;
+      auto wait = [&](uint64_t* bar, int parity) -> bool {
+        return __all_sync(kAll, mbar_wait(bar, parity, abort_flag, kLimitNs));
+      };
       auto issue_pv = [&](int p) -> bool {
         const int u = S::SHARED ? p : 2 * p + 1, slot = p & 1;
         // the weights are there, and with them: S of tile p is read
-        if ((!S::SHARED &&
-             !mbar_wait(&tail->full[u % R], (u / R) & 1, abort_flag, kLimitNs)) ||
-            !mbar_wait(&tail->p_full[slot], (p >> 1) & 1, abort_flag, kLimitNs) ||
-            (prev_first && prev_seg > 0 &&
-             !mbar_wait(&tail->o_free, (prev_seg - 1) & 1, abort_flag, kLimitNs)))
+        if ((!S::SHARED && !wait(&tail->full[u % R], (u / R) & 1)) ||
+            !wait(&tail->p_full[slot], (p >> 1) & 1) ||
+            (prev_first && prev_seg > 0 && !wait(&tail->o_free, (prev_seg - 1) & 1)))
           return false;
         tc_fence_after();
         const uint32_t va = ring + (u % R) * S::UNIT;
@@ -531,14 +557,14 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           for (int term = 0; term < S::TERMS; ++term) {
 #pragma unroll
             for (int v = 0; v < S::VT; ++v)
-              mma_f16(ocol + v * N,
+              mma_by_one(ocol + v * N,
                       vd + (uint64_t)((v * (S::VM / 64) * 1024 + k * 2 * S::VGS) >> 4),
                       pd + (uint64_t)((k * 2 * PGS + term * (N > 32 ? TOK * 128 : 64)) >> 4),
                       idesc_o, more);
             more = 1;
           }
-        mma_commit(&tail->empty[u % R]);
-        mma_commit(&tail->o_done[slot]);
+        commit_by_one(&tail->empty[u % R]);
+        commit_by_one(&tail->o_done[slot]);
         return true;
       };
       while (ok && walk.next(a, r, &g)) {
@@ -551,15 +577,15 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           uint64_t* bars[2] = {&tail->full[u % R], &tail->q_full[qs]};
           const uint32_t parity[2] = {(uint32_t)((u / R) & 1), (uint32_t)((seg / QB) & 1)};
           for (int i = 0; i < (first ? 2 : 1) && ok; ++i) {
-            while (left && !mbar_test(bars[i], parity[i])) {
-              if (mbar_test(&tail->p_full[(t - 1) & 1], ((t - 1) >> 1) & 1)) {
+            while (left && !__all_sync(kAll, mbar_test(bars[i], parity[i]))) {
+              if (__all_sync(kAll, mbar_test(&tail->p_full[(t - 1) & 1], ((t - 1) >> 1) & 1))) {
                 ok = issue_pv(t - 1);
                 left = false;
-              } else if (*abort_flag) {
+              } else if (__any_sync(kAll, *abort_flag)) {
                 break;
               }
             }
-            ok = ok && mbar_wait(bars[i], parity[i], abort_flag, kLimitNs);
+            ok = ok && wait(bars[i], parity[i]);
           }
           if (!ok) break;
           tc_fence_after();
@@ -568,11 +594,11 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           const uint32_t scol = tmem + (t & 1) * N;
 #pragma unroll
           for (int k = 0; k < 4 * S::QS; ++k)
-            mma_f16(scol, kd + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4),
+            mma_by_one(scol, kd + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4),
                     qd + (uint64_t)(((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_s, k > 0);
-          if (!S::SHARED) mma_commit(&tail->empty[u % R]);
-          mma_commit(&tail->s_full[t & 1]);
-          if (j + 1 == g.j1) mma_commit(&tail->q_empty[qs]);
+          if (!S::SHARED) commit_by_one(&tail->empty[u % R]);
+          commit_by_one(&tail->s_full[t & 1]);
+          if (j + 1 == g.j1) commit_by_one(&tail->q_empty[qs]);
           if (left) ok = issue_pv(t - 1);
           prev_first = first;
           prev_seg = seg;
@@ -581,13 +607,13 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         ++seg;
       }
       if (ok && t > 0) ok = issue_pv(t - 1);
-      if (!ok) {
+      if (!ok && lane == 0) {
         *abort_flag = 1;
         report(a.status_dev, PA_ERR_TIMEOUT);
       }
       // every product and commit issued here ends before TMEM is freed
       if (t > 0) {
-        mma_commit(&tail->drain);
+        commit_by_one(&tail->drain);
         mbar_wait_drain(&tail->drain, 0, kLimitNs);
       }
     }
