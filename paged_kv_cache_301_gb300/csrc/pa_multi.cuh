@@ -53,7 +53,7 @@ using namespace sm100;
 constexpr int kMaxCtas = 160;                  // CTAs at most (one per SM; GB300: 152)
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kEnds = 4;                       // cost of an item's ends, in quarters of a tile
+constexpr int kEnds = 8;                       // cost of an item's ends, in quarters of a tile
 constexpr float kRaise = 8.f;                  // log2 by which a tile may exceed the maximum
 
 struct Args {
@@ -67,7 +67,8 @@ struct Args {
   int B, total_q, Hq, H, G, bs_shift, max_blocks, num_blocks, max_q, words, max_len;
   // columns of a group: gh heads of gn new tokens each; a KV head's heads are `chunks` of gh
   int gh, gn, chunks;
-  int gs;                        // CTAs of a set: column groups of an item
+  int gs;                        // CTAs of a set, 1 or 2: column groups of an item
+  int narrow;                    // costs fit 32 bits
   float scale_log2;
   Window* info;                  // [sets]
   float* ws_m;                   // [2 CTAs, N]
@@ -121,13 +122,13 @@ template <class S>
 struct Tail {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_free, drain;
-  int64_t lin[2];
+  int64_t lin[2];                // the window's first tile, and the next one's
   int64_t sums[S::kThreads / 32][2];
-  Place start;
-  int64_t out_at[S::N];          // element of out where a column's row begins, -1: none
-  int query[S::N];               // the column's new token, -1: none
+  Window start;
+  alignas(16) int out_row[S::N]; // a column's row of out, -1: none
+  int query[S::N];               // its new token, -1: none
   uint32_t seen[S::N][S::TOK / 32];        // what it sees of a tile, a bit of a token
-  float by[S::N];                // 2^(maximum before - now), then 1 / the weights' sum
+  alignas(16) float by[S::N];    // 2^(maximum before - now), then 1 / the weights' sum
   float red[4][S::N];            // per warp: columns' maxima
   float sum[4][S::N];            // per warp: columns' sums of weights
   float share[S::N];             // weights of a row whose values are added apart, -1: unseen
@@ -160,8 +161,77 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, bool* bad) {
          (int64_t)s.L > ((int64_t)a.max_blocks << a.bs_shift) || s.qs < 0 || s.n < 0 ||
          s.n > a.max_q || s.n > a.total_q - s.qs || (a.q_start && s.n > s.L);
   s.nt = *bad || s.n == 0 ? 0 : (s.L + S::TOK - 1) / S::TOK;
-  s.items = s.nt == 0 ? 0 : a.H * ((groups_of(a, s.n) + a.gs - 1) / a.gs);
+  s.items = s.nt == 0 ? 0 : a.H * ((groups_of(a, s.n) + a.gs - 1) >> (a.gs - 1));
   return s;
+}
+
+// The window of a set, by the whole CTA: tail->start and tail->lin.
+template <class S, class I>
+__device__ __forceinline__ void find_window(const Args& a, Tail<S>* tail, int set, int sets) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (a.B + S::kThreads - 1) / S::kThreads;
+  Share<I> share;
+  share.b0 = min(a.B, tid * per);
+  share.b1 = min(a.B, share.b0 + per);
+  share.tiles = share.items = 0;
+  auto work_of = [&](int b) {
+    bool bad;
+    const Seq s = seq_of<S>(a, b, &bad);
+    return Work{s.nt, s.items};
+  };
+  for (int b = share.b0; b < share.b1; ++b) {
+    const Work w = work_of(b);
+    share.tiles += (I)w.nt * w.items;
+    share.items += w.items;
+  }
+  share.tiles_to = share.tiles;
+  share.items_to = share.items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const I t = __shfl_up_sync(kAll, share.tiles_to, o);
+    const I n = __shfl_up_sync(kAll, share.items_to, o);
+    if (lane >= o) {
+      share.tiles_to += t;
+      share.items_to += n;
+    }
+  }
+  I (*sums)[2] = reinterpret_cast<I (*)[2]>(tail->sums);
+  if (lane == 31) {
+    sums[warp][0] = share.tiles_to;
+    sums[warp][1] = share.items_to;
+  }
+  share.tiles_to -= share.tiles;
+  share.items_to -= share.items;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  I tiles = 0, items = 0;
+#pragma unroll
+  for (int w = 0; w < S::kThreads / 32; ++w) {
+    if (w < warp) {
+      share.tiles_to += sums[w][0];
+      share.items_to += sums[w][1];
+    }
+    tiles += sums[w][0];
+    items += sums[w][1];
+  }
+  const Cut<I> cut = cut_of(tiles, items, sets, kEnds);
+  if (set < cut.windows) {
+    Place<I> p;
+    if (place_of(cut, share, a.B, bound_of(cut, set), work_of, &p)) {
+      tail->start = Window{p.b, p.item, p.j, 0};
+      tail->lin[0] = p.lin;
+    }
+    if (set + 1 == cut.windows) {
+      if (tid == 0) tail->lin[1] = cut.tiles;
+    } else if (place_of(cut, share, a.B, bound_of(cut, set + 1), work_of, &p)) {
+      tail->lin[1] = p.lin;
+    }
+  } else if (tid == 0) {
+    tail->start = Window{0, -1, -1, 0};
+    tail->lin[0] = tail->lin[1] = 0;
+  }
+  __syncthreads();
 }
 
 // Walks the segments of a window: its part of one item after another.
@@ -381,6 +451,12 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     tmem_alloc(&tail->tmem, S::kCols);
     tmem_relinquish();
   }
+  // block ids stand at the end of a chain of loads: into L2 while the window is found
+  for (int64_t i = ((int64_t)blockIdx.x * kThreads + tid) * 32; i < (int64_t)a.B * a.max_blocks;
+       i += (int64_t)gridDim.x * kThreads * 32) {
+    prefetch_l2(a.tables + i);
+    if (i > (1 << 22)) break;
+  }
   // rows of q that no copy writes
   if (a.gh * a.gn < N) {
     for (int i = tid; i < QB * S::QBYTES / 16; i += kThreads)
@@ -390,68 +466,8 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
   wait_prior_grid();
 
   // this set's window
-  const int per = (a.B + kThreads - 1) / kThreads;
-  Share share;
-  share.b0 = min(a.B, tid * per);
-  share.b1 = min(a.B, share.b0 + per);
-  share.tiles = share.items = 0;
-  auto work_of = [&](int b) {
-    bool bad;
-    const Seq s = seq_of<S>(a, b, &bad);
-    return Work{s.nt, s.items};
-  };
-  for (int b = share.b0; b < share.b1; ++b) {
-    const Work w = work_of(b);
-    share.tiles += (int64_t)w.nt * w.items;
-    share.items += w.items;
-  }
-  share.tiles_to = share.tiles;
-  share.items_to = share.items;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t t = __shfl_up_sync(kAll, share.tiles_to, o);
-    const int64_t n = __shfl_up_sync(kAll, share.items_to, o);
-    if (lane >= o) {
-      share.tiles_to += t;
-      share.items_to += n;
-    }
-  }
-  if (lane == 31) {
-    tail->sums[warp][0] = share.tiles_to;
-    tail->sums[warp][1] = share.items_to;
-  }
-  share.tiles_to -= share.tiles;
-  share.items_to -= share.items;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  int64_t tiles = 0, items = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) {
-      share.tiles_to += tail->sums[w][0];
-      share.items_to += tail->sums[w][1];
-    }
-    tiles += tail->sums[w][0];
-    items += tail->sums[w][1];
-  }
-  const Cut cut = cut_of(tiles, items, sets, kEnds);
-  if (set < cut.windows) {
-    Place p;
-    if (place_of(cut, share, a.B, bound_of(cut, set), work_of, &p)) {
-      tail->start = p;
-      tail->lin[0] = p.lin;
-    }
-    if (set + 1 == cut.windows) {
-      if (tid == 0) tail->lin[1] = cut.tiles;
-    } else if (place_of(cut, share, a.B, bound_of(cut, set + 1), work_of, &p)) {
-      tail->lin[1] = p.lin;
-    }
-  } else if (tid == 0) {
-    tail->start = Place{0, -1, -1, 0};
-    tail->lin[0] = tail->lin[1] = 0;
-  }
-  __syncthreads();
+  if (a.narrow) find_window<S, int>(a, tail, set, sets);
+  else find_window<S, int64_t>(a, tail, set, sets);
   Walk<S> walk;
   walk.b = tail->start.b;
   walk.item = tail->start.item;
@@ -520,9 +536,9 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issue --
-    // V . p of tile t - 1 goes before or behind K . q of tile t, whichever can begin first: the
-    // softmax of a tile runs while the tensor cores have the next one's scores, and where the
-    // next tile is still on its way, the product frees the ring for the one behind it.
+    // K . q of tile t, then V . p of tile t - 1, so that the softmax of a tile runs while the
+    // tensor cores have the next one's scores; but where the next tile is still on its way, the
+    // product goes first and frees the ring for the one behind it.
     // Descriptors are built once a tile and stepped by constants (the start-address field holds
     // address / 16), and the whole warp runs along, so that they stay uniform.
     constexpr uint32_t ab = DT == PA_BFLOAT16 ? 1u : 0u;
@@ -574,19 +590,16 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           const int u = S::SHARED ? t : 2 * t;
           const bool first = j == g.j0;
           bool left = t > 0;                     // the product of tile t - 1 is not issued
-          uint64_t* bars[2] = {&tail->full[u % R], &tail->q_full[qs]};
-          const uint32_t parity[2] = {(uint32_t)((u / R) & 1), (uint32_t)((seg / QB) & 1)};
-          for (int i = 0; i < (first ? 2 : 1) && ok; ++i) {
-            while (left && !__all_sync(kAll, mbar_test(bars[i], parity[i]))) {
-              if (__all_sync(kAll, mbar_test(&tail->p_full[(t - 1) & 1], ((t - 1) >> 1) & 1))) {
-                ok = issue_pv(t - 1);
-                left = false;
-              } else if (__any_sync(kAll, *abort_flag)) {
-                break;
-              }
-            }
-            ok = ok && wait(bars[i], parity[i]);
+          // Scores of tile t go first only if the tile and q are there by now: they take
+          // longer than the softmax that the product of tile t - 1 waits for.
+          if (left && !(__all_sync(kAll, mbar_test(&tail->full[u % R], (u / R) & 1)) &&
+                        (!first ||
+                         __all_sync(kAll, mbar_test(&tail->q_full[qs], (seg / QB) & 1))))) {
+            ok = issue_pv(t - 1);
+            left = false;
           }
+          ok = ok && wait(&tail->full[u % R], (u / R) & 1) &&
+               (!first || wait(&tail->q_full[qs], (seg / QB) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint64_t kd = smem_desc_sw128(ring + (u % R) * S::UNIT, 16, S::GS);
@@ -705,7 +718,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         const int c = c_lo + st, x = c / a.gh, i = g.i0 + x, head = g.g0 + c - x * a.gh;
         const bool live = x < a.gn && i < g.n && head < a.G;
         tail->query[c] = live ? i : -1;
-        tail->out_at[c] = live ? ((int64_t)(g.qs + i) * a.Hq + g.h * a.G + head) * S::DV : -1;
+        tail->out_row[c] = live ? (g.qs + i) * a.Hq + g.h * a.G + head : -1;
       }
       sync();
       for (int j = g.j0; j < g.j1; ++j, ++t) {
@@ -989,32 +1002,34 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         sync();
         tc_fence_after();
         const bool has_dim = S::VM == 128 || lane < 16;
+        const int dim0 = S::VM == 128 ? wq * 32 + lane : wq * 16 + (lane & 15);
+        constexpr int CS = NC < 32 ? NC : 32;
 #pragma unroll 1
         for (int v = 0; v < S::VT; ++v) {
-          const int dim = v * S::VM + (S::VM == 128 ? wq * 32 + lane : wq * 16 + (lane & 15));
-#pragma unroll 1
-          for (int c0 = c_lo; c0 < c_lo + NC; c0 += 16) {
-            float o[16];
-            tmem_ld16(ocol + quarter + v * N + c0, o);
-            if (whole) {
-              // two lanes exchange halves of two columns: a store of two dims of one column
+          const int dim = v * S::VM + dim0;
+          float o[CS];
+          if constexpr (CS == 32) tmem_ld32(ocol + quarter + v * N + c_lo, o);
+          else tmem_ld16(ocol + quarter + v * N + c_lo, o);
+          if (whole) {
+            // two lanes exchange halves of two columns: a store of two dims of one column
+            uint16_t* to = static_cast<uint16_t*>(a.out) + (dim & ~1);
 #pragma unroll
-              for (int c = 0; c < 16; c += 2) {
-                const float by0 = tail->by[c0 + c], by1 = tail->by[c0 + c + 1];
-                const float y0 = by0 == 0.f ? 0.f : o[c] * by0;
-                const float y1 = by1 == 0.f ? 0.f : o[c + 1] * by1;
-                const float other = __shfl_xor_sync(kAll, lane & 1 ? y0 : y1, 1);
-                const int64_t to = tail->out_at[c0 + c + (lane & 1)];
-                if (has_dim && to >= 0)
-                  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to + (dim & ~1)) =
-                      lane & 1 ? pack2<DT>(other, y1) : pack2<DT>(y0, other);
-              }
-            } else if (has_dim) {
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if (tail->query[c0 + c] >= 0)
-                  a.ws_acc[(part * N + c0 + c) * S::DV + dim] = o[c];
+            for (int c = 0; c < CS; c += 2) {
+              const float2 by = *reinterpret_cast<const float2*>(&tail->by[c_lo + c]);
+              const int2 rows = *reinterpret_cast<const int2*>(&tail->out_row[c_lo + c]);
+              const float y0 = by.x == 0.f ? 0.f : o[c] * by.x;
+              const float y1 = by.y == 0.f ? 0.f : o[c + 1] * by.y;
+              const float other = __shfl_xor_sync(kAll, lane & 1 ? y0 : y1, 1);
+              const int row = lane & 1 ? rows.y : rows.x;
+              const uint32_t two = lane & 1 ? pack2<DT>(other, y1) : pack2<DT>(y0, other);
+              if (has_dim && row >= 0)
+                *reinterpret_cast<uint32_t*>(to + (int64_t)row * S::DV) = two;
             }
+          } else if (has_dim) {
+            float* to = a.ws_acc + (part * N + c_lo) * S::DV + dim;
+#pragma unroll
+            for (int c = 0; c < CS; ++c)
+              if (c_lo + c < a.gh * a.gn) to[c * S::DV] = o[c];
           }
         }
         tc_fence_before();
@@ -1037,17 +1052,26 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
 }
 
 // Joins the partials of items that window boundaries cut: CTA (c, r, z) looks at the boundary
-// where window c + 1 begins, and joins columns [z, z + 1) * cols of column group r of its item,
+// where window c + 1 begins, and joins its share z of the columns of column group r of its item,
 // if that boundary is the item's first.  The parts: the segment of window c that ends there,
 // then the first segments of the windows behind, as long as they begin inside the item.
 // A thread takes four dims of a column and every PS-th part.
 constexpr int kJoinThreads = 512;
 
+template <class S, int PS>
+struct Join {
+  static constexpr int LANES = S::DV / 4;                          // threads of a column
+  static constexpr int AT_ONCE = kJoinThreads / LANES / PS;        // columns at once
+  // columns of a CTA: with few parts half of them, all asked for at once
+  static constexpr int COLS = PS > 1 ? AT_ONCE : S::N / 2;
+  static constexpr int ROUNDS = COLS > AT_ONCE ? COLS / AT_ONCE : 1;
+};
+
 template <class S, int DT, int PS>
 __global__ void __launch_bounds__(kJoinThreads)
-join_kernel(const Args a, int sets, int cols) {
-  constexpr int N = S::N, DV = S::DV, LANES = DV / 4;
-  constexpr int COLS = kJoinThreads / LANES / PS;          // columns at once
+join_kernel(const Args a, int sets) {
+  using J = Join<S, PS>;
+  constexpr int N = S::N, DV = S::DV, LANES = J::LANES, COLS = J::COLS, ROUNDS = J::ROUNDS;
   __shared__ float s_w[COLS][kMaxCtas + 1];
   __shared__ bool s_none[COLS];                            // no weight at all: zeros
   __shared__ float4 s_sum[PS > 1 ? PS : 1][PS > 1 ? COLS * LANES : 1];
@@ -1068,76 +1092,83 @@ join_kernel(const Args a, int sets, int cols) {
   const Seq s = seq_of<S>(a, at.b, &bad);
   const int pairs = s.items / a.H, h = at.item / pairs;
   const int group = (at.item - h * pairs) * a.gs + r, i0 = group / a.chunks * a.gn;
-  const int g0 = group % a.chunks * a.gh;
-  const int n = a.gh * min(a.gn, s.n - i0);              // none, for a group without columns
+  const int g0 = group % a.chunks * a.gh, c0 = (int)blockIdx.z * COLS;
+  // columns of this CTA: none, for a group without columns
+  const int n = min(COLS, a.gh * min(a.gn, s.n - i0) - c0);
+  if (n <= 0) return;
   // row of part k in ws_m and ws_l
   auto row = [&](int k) -> int64_t {
     const int cta = (c - 1 + k) * a.gs + r;
-    return (2 * (int64_t)cta + (k == 0 && !same ? 1 : 0)) * N;
+    return (2 * (int64_t)cta + (k == 0 && !same ? 1 : 0)) * N + c0;
   };
-  const int x = tid % (COLS * LANES), ps = tid / (COLS * LANES);
+  for (int w = warp; w < n; w += kJoinThreads / 32) {
+    float top = -CUDART_INF_F, l = 0.f;
+    float m0 = -CUDART_INF_F, l0 = 0.f;                    // of the lane's first part
+    if (lane < parts) {
+      m0 = a.ws_m[row(lane) + w];
+      l0 = a.ws_l[row(lane) + w];
+      top = m0;
+    }
+    for (int k = lane + 32; k < parts; k += 32) top = fmaxf(top, a.ws_m[row(k) + w]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    for (int k = lane; k < parts; k += 32) {
+      const float m = k < 32 ? m0 : a.ws_m[row(k) + w];
+      const float y = top == -CUDART_INF_F ? 0.f : ex2_approx(m - top);
+      s_w[w][k] = y;
+      l = fmaf(y, k < 32 ? l0 : a.ws_l[row(k) + w], l);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int k = lane; k < parts; k += 32) s_w[w][k] *= inv;
+    if (lane == 0) s_none[w] = l == 0.f;
+  }
+  __syncthreads();
+  const int x = tid % (J::AT_ONCE * LANES), ps = tid / (J::AT_ONCE * LANES);
   const int col = x / LANES, d = (x % LANES) * 4;
-  const int end = min(n, ((int)blockIdx.z + 1) * cols);
-  for (int c0 = (int)blockIdx.z * cols; c0 < end; c0 += COLS) {
-    for (int w = warp; w < COLS; w += kJoinThreads / 32) {
-      if (c0 + w >= end) break;
-      float top = -CUDART_INF_F;
-      for (int k = lane; k < parts; k += 32) {
-        const float m = a.ws_m[row(k) + c0 + w];
-        s_w[w][k] = m;
-        top = fmaxf(top, m);
-      }
+  float4 sum[ROUNDS];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      float l = 0.f;
-      for (int k = lane; k < parts; k += 32) {
-        const float y = top == -CUDART_INF_F ? 0.f : ex2_approx(s_w[w][k] - top);
-        s_w[w][k] = y;
-        l = fmaf(y, a.ws_l[row(k) + c0 + w], l);
-      }
+  for (int i = 0; i < ROUNDS; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(ROUNDS > 2 ? 2 : 8)
+  for (int k = ps; k < parts; k += PS) {
+    const float* acc = a.ws_acc + (row(k) + col) * DV + d;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      for (int k = lane; k < parts; k += 32) s_w[w][k] *= inv;
-      if (lane == 0) s_none[w] = l == 0.f;
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int w = col + i * J::AT_ONCE;
+      if (w < n) {
+        const float y = s_w[w][k];
+        const float4 v = *reinterpret_cast<const float4*>(acc + i * J::AT_ONCE * DV);
+        sum[i].x = fmaf(y, v.x, sum[i].x);
+        sum[i].y = fmaf(y, v.y, sum[i].y);
+        sum[i].z = fmaf(y, v.z, sum[i].z);
+        sum[i].w = fmaf(y, v.w, sum[i].w);
+      }
     }
+  }
+  if (PS > 1) {
+    s_sum[PS > 1 ? ps : 0][PS > 1 ? x : 0] = sum[0];
     __syncthreads();
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c0 + col < end) {
-#pragma unroll 8
-      for (int k = ps; k < parts; k += PS) {
-        const float y = s_w[col][k];
-        const float4 v =
-            *reinterpret_cast<const float4*>(a.ws_acc + (row(k) + c0 + col) * DV + d);
-        sum.x = fmaf(y, v.x, sum.x);
-        sum.y = fmaf(y, v.y, sum.y);
-        sum.z = fmaf(y, v.z, sum.z);
-        sum.w = fmaf(y, v.w, sum.w);
-      }
-    }
-    if (PS > 1) {
-      s_sum[PS > 1 ? ps : 0][PS > 1 ? x : 0] = sum;
-      __syncthreads();
-      if (ps == 0) {
+    if (ps > 0) return;
 #pragma unroll
-        for (int i = 1; i < PS; ++i) {
-          const float4 v = s_sum[i][PS > 1 ? x : 0];
-          sum.x += v.x;
-          sum.y += v.y;
-          sum.z += v.z;
-          sum.w += v.w;
-        }
-      }
+    for (int i = 1; i < PS; ++i) {
+      const float4 v = s_sum[i][PS > 1 ? x : 0];
+      sum[0].x += v.x;
+      sum[0].y += v.y;
+      sum[0].z += v.z;
+      sum[0].w += v.w;
     }
-    if (ps == 0 && c0 + col < end) {
-      if (s_none[col]) sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int x = (c0 + col) / a.gh, head = g0 + c0 + col - x * a.gh;
-      const int64_t to = ((int64_t)(s.qs + i0 + x) * a.Hq + h * a.G + head) * DV + d;
-      if (head < a.G)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
-            make_uint2(pack2<DT>(sum.x, sum.y), pack2<DT>(sum.z, sum.w));
-    }
-    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int w = col + i * J::AT_ONCE;
+    if (w >= n) break;
+    const int x0 = (c0 + w) / a.gh, head = g0 + c0 + w - x0 * a.gh;
+    const int64_t to = ((int64_t)(s.qs + i0 + x0) * a.Hq + h * a.G + head) * DV + d;
+    const float4 y = s_none[w] ? make_float4(0.f, 0.f, 0.f, 0.f) : sum[i];
+    if (head < a.G)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
+          make_uint2(pack2<DT>(y.x, y.y), pack2<DT>(y.z, y.w));
   }
 }
 
@@ -1248,17 +1279,12 @@ cudaError_t launch(const CUtensorMap (&maps)[3], const Args& a, int ctas, int64_
                              maps[0], maps[1], maps[2], a);
   const int sets = ctas / a.gs;
   if (e != cudaSuccess || !cut || sets < 2) return e;
-  // few items of many parts: the parts of a few columns to a CTA, else many columns
-  if (items * 8 <= sets) {
-    constexpr int cols = kJoinThreads / (S::DV / 4) / 4;
-    return launch_pdl(join_kernel<S, DT, 4>,
-                      dim3((unsigned)(sets - 1), (unsigned)a.gs,
-                           (unsigned)((S::N + cols - 1) / cols)),
-                      kJoinThreads, 0, stream, a, sets, cols);
-  }
-  constexpr int cols = S::N / 2;
-  return launch_pdl(join_kernel<S, DT, 1>, dim3((unsigned)(sets - 1), (unsigned)a.gs, 2),
-                    kJoinThreads, 0, stream, a, sets, cols);
+  // few items of many parts: the parts of a few columns to a CTA, else half the columns
+  const bool deep = items * 8 <= sets;
+  const int cols = deep ? Join<S, 4>::COLS : Join<S, 1>::COLS;
+  const dim3 grid((unsigned)(sets - 1), (unsigned)a.gs, (unsigned)((S::N + cols - 1) / cols));
+  return launch_pdl(deep ? join_kernel<S, DT, 4> : join_kernel<S, DT, 1>, grid, kJoinThreads, 0,
+                    stream, a, sets);
 }
 
 // The shape of N columns.
@@ -1356,6 +1382,7 @@ pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f)
   a.gn = cols.gn;
   a.chunks = cols.chunks;
   a.gs = cols.gs;
+  a.narrow = items * (4 * nt + kEnds) < (1ll << 31);
   a.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
   a.info = reinterpret_cast<Window*>(ws);
   a.ws_m = reinterpret_cast<float*>(ws + y.m_off);

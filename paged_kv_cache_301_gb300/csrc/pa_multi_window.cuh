@@ -24,66 +24,72 @@ struct Work {
   int nt, items;
 };
 
+// Costs and tile numbers are of type I: int, or int64_t where they do not fit.
+template <class I>
 struct Cut {
-  int64_t tiles, total;        // of all items: tiles, cost
+  I tiles, total;              // of all items: tiles, cost
   int windows, ends;           // windows that hold any; what an item's ends cost
 };
 
-PA_MULTI_HD Cut cut_of(int64_t tiles, int64_t items, int sets, int ends) {
-  Cut c;
+template <class I>
+PA_MULTI_HD Cut<I> cut_of(I tiles, I items, int sets, int ends) {
+  Cut<I> c;
   c.tiles = tiles;
   c.windows = tiles < sets ? (int)tiles : sets;
   // two tiles begin 4 + ends apart at most: the ends count only where windows are longer, so
   // that every window holds a tile
   c.ends = ends;
   c.total = 4 * tiles + ends * items;
-  if (c.total < (int64_t)c.windows * (4 + ends)) {
+  if (c.total < (I)c.windows * (4 + ends)) {
     c.ends = 0;
     c.total = 4 * tiles;
   }
   return c;
 }
 
-PA_MULTI_HD int64_t bound_of(const Cut& c, int window) {
-  return c.total / c.windows * window + c.total % c.windows * window / c.windows;
+// total * window / windows, without the product that might not fit.
+template <class I>
+PA_MULTI_HD I bound_of(const Cut<I>& c, int window) {
+  const I each = c.total / c.windows;
+  return each * window + (int)(c.total - each * c.windows) * window / c.windows;
 }
 
 // Sequences [b0, b1) and what stands before them: tiles and items.
+template <class I>
 struct Share {
   int b0, b1;
-  int64_t tiles_to, items_to, tiles, items;
+  I tiles_to, items_to, tiles, items;
 };
 
 // A window's first tile: its number among all, sequence, item of it, tile of that.
+template <class I>
 struct Place {
-  int64_t lin;
+  I lin;
   int b, item, j;
 };
 
 // The first tile that begins at cost w or behind it, if w (< total) lies in this share.
 // work_of(b): sequence b's; B sequences in all.
-template <class F>
-PA_MULTI_HD bool place_of(const Cut& cut, const Share& s, int B, int64_t w, const F& work_of,
-                          Place* p) {
-  int64_t cost = 4 * s.tiles_to + cut.ends * s.items_to;
+template <class I, class F>
+PA_MULTI_HD bool place_of(const Cut<I>& cut, const Share<I>& s, int B, I w, const F& work_of,
+                          Place<I>* p) {
+  I cost = 4 * s.tiles_to + cut.ends * s.items_to;
   if (w < cost || w >= cost + 4 * s.tiles + cut.ends * s.items) return false;
-  int64_t tiles = s.tiles_to;
+  I tiles = s.tiles_to;
   int b = s.b0;
   Work k = work_of(b);
   for (;;) {
-    const int64_t c = k.nt ? (int64_t)k.items * (4 * (int64_t)k.nt + cut.ends) : 0;
+    const I c = k.nt ? (I)k.items * (4 * (I)k.nt + cut.ends) : 0;
     if (w < cost + c || b + 1 >= s.b1) break;
     cost += c;
-    tiles += k.nt ? (int64_t)k.items * k.nt : 0;
+    tiles += k.nt ? (I)k.items * k.nt : 0;
     k = work_of(++b);
   }
-  const int64_t at = w - cost, each = 4 * (int64_t)k.nt + cut.ends;
-  // 64-bit division is slow; most batches fit 32 bits
-  int item = at < (1ll << 32) && each < (1ll << 32) ? (int)((uint32_t)at / (uint32_t)each)
-                                                   : (int)(at / each);
-  const int64_t r = at - item * each, up = (r - cut.ends + 3) >> 2;
-  int64_t j = r == 0 ? 0 : (up > 1 ? up : 1);
-  p->lin = tiles + (int64_t)item * k.nt + j;
+  const I at = w - cost, each = 4 * (I)k.nt + cut.ends;
+  int item = (int)(at / each);
+  const I r = at - item * each, up = (r - cut.ends + 3) >> 2;
+  I j = r == 0 ? 0 : (up > 1 ? up : 1);
+  p->lin = tiles + (I)item * k.nt + j;
   if (j >= k.nt) {                             // the next item, maybe of a later sequence
     j = 0;
     if (++item == k.items) {
