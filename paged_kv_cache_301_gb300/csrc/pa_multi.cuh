@@ -304,6 +304,14 @@ __device__ __forceinline__ void tma_block_head(void* dst, const CUtensorMap* map
       : "memory");
 }
 
+// The same block to L2 only.
+__device__ __forceinline__ void prefetch_block(const CUtensorMap* map, int group, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.prefetch.tensor.4d.L2.global.tile.L2::cache_hint [%0, {%1, %2, %3, %4}], "
+      "%5;" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(0), "r"(group), "l"(policy)
+      : "memory");
+}
+
 // One slab of q: [new tokens][heads][64].
 __device__ __forceinline__ void tma_q(void* dst, const CUtensorMap* map, uint64_t* bar, int head,
                                       int row, int slab) {
@@ -524,6 +532,12 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           }
           ++u;
         }
+        // With two tiles of shared memory a copy's time is in the way: the next tile's blocks are
+        // brought to L2, from where they come in half the time (the first two tiles are asked for
+        // at once).
+        if (S::SHARED && j > g.j0 && id >= 0 && id < a.num_blocks &&
+            (a.gs == 1 || (lane & 1) == r) && j + 1 < g.j1)
+          prefetch_block(&map_k, id << a.bs_shift >> 3, policy);
       }
     }
     if (!ok && lane == 0) {
