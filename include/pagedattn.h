@@ -672,7 +672,8 @@ pa_status pa_latent_decode(void* out, const void* q, const void* pool,
  * total_kv) is skipped (rows untouched; reported in checked mode).  Infinities and NaN of
  * tokens that a row does not see have no part in it.  fp32 sums and statistics; the
  * softmax weights enter the product rounded to the storage type.
- * Supported: fp16 / bf16, nope_dim 128, rope_dim 64, value_dim 128.  No workspace.
+ * Supported: fp16 / bf16, nope_dim 128, rope_dim 64, value_dim 128; scale > 0.  No
+ * workspace.
  */
 pa_status pa_latent_prefill(void* out, const void* q, const void* kv, const void* key_rope,
                             const int32_t* q_start, const int32_t* kv_start, int num_seqs,
