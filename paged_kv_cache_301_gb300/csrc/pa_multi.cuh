@@ -53,7 +53,7 @@ using namespace sm100;
 constexpr int kMaxCtas = 160;                  // CTAs at most (one per SM; GB300: 152)
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kEnds = 8;                       // cost of an item's ends, in quarters of a tile
+constexpr int kEnds = 12;                       // cost of an item's ends, in quarters of a tile
 constexpr float kRaise = 8.f;                  // log2 by which a tile may exceed the maximum
 
 struct Args {
@@ -121,7 +121,7 @@ struct Shape {
 template <class S>
 struct Tail {
   uint64_t full[8], empty[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_free, drain;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_free, drain;
   int64_t lin[2];                // the window's first tile, and the next one's
   int64_t sums[S::kThreads / 32][2];
   Window start;
@@ -409,6 +409,27 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// Four values of each of four lanes: lane i's value j to lane j's value i.
+__device__ __forceinline__ void transpose4(float& a, float& b, float& c, float& d, int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+  const float x = __shfl_xor_sync(kAll, odd ? a : b, 1), y = __shfl_xor_sync(kAll, odd ? c : d, 1);
+  if (odd) {
+    a = x;
+    c = y;
+  } else {
+    b = x;
+    d = y;
+  }
+  const float u = __shfl_xor_sync(kAll, high ? a : c, 2), v = __shfl_xor_sync(kAll, high ? b : d, 2);
+  if (high) {
+    a = u;
+    b = v;
+  } else {
+    c = u;
+    d = v;
+  }
+}
+
 // Of two storage-type values in a word: is one infinite or NaN?
 template <int DT>
 __device__ __forceinline__ bool odd2(uint32_t w) {
@@ -443,7 +464,6 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
       mbar_init(&tail->q_empty[i], 1);
       mbar_init(&tail->s_full[i], 1);
       mbar_init(&tail->p_full[i], 4 * S::GROUPS);
-      mbar_init(&tail->o_done[i], 1);
     }
     mbar_init(&tail->o_free, 4 * S::GROUPS);
     mbar_init(&tail->drain, 1);
@@ -594,7 +614,6 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
             more = 1;
           }
         commit_by_one(&tail->empty[u % R]);
-        commit_by_one(&tail->o_done[slot]);
         return true;
       };
       while (ok && walk.next(a, r, &g)) {
@@ -712,8 +731,11 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     auto wait_all = [&](uint64_t* bar, int parity) -> bool {
       return __all_sync(kAll, mbar_try_wait(bar, parity) || mbar_wait_drain(bar, parity, kLimitNs));
     };
-    // V . p of tile i; whoever has S of tile i + 1 or i knows that of tile i - 2 to be done
-    auto wait_product = [&](int i) -> bool { return wait_all(&tail->o_done[i & 1], (i >> 1) & 1); };
+    // V . p of tile i, which frees its V
+    auto wait_product = [&](int i) -> bool {
+      const int u = S::SHARED ? i : 2 * i + 1;
+      return wait_all(&tail->empty[u % R], (u / R) & 1);
+    };
     auto sync = [&]() { named_barrier(1 + grp, 128); };
     // a column's value in all rows of the warp, from its lanes'
     auto over_rows = [&](float x, auto&& f) -> float {
@@ -1017,33 +1039,52 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         tc_fence_after();
         const bool has_dim = S::VM == 128 || lane < 16;
         const int dim0 = S::VM == 128 ? wq * 32 + lane : wq * 16 + (lane & 15);
-        constexpr int CS = NC < 32 ? NC : 32;
+        constexpr int CS = 16;
 #pragma unroll 1
-        for (int v = 0; v < S::VT; ++v) {
-          const int dim = v * S::VM + dim0;
-          float o[CS];
-          if constexpr (CS == 32) tmem_ld32(ocol + quarter + v * N + c_lo, o);
-          else tmem_ld16(ocol + quarter + v * N + c_lo, o);
+        for (int c0 = c_lo; c0 < c_lo + NC; c0 += CS) {
           if (whole) {
             // two lanes exchange halves of two columns: a store of two dims of one column
-            uint16_t* to = static_cast<uint16_t*>(a.out) + (dim & ~1);
+            float by[CS];
+            uint16_t* to[CS / 2];
+            bool none = false;                   // a column without weights: zeros
+#pragma unroll
+            for (int c = 0; c < CS; ++c) by[c] = tail->by[c0 + c];
 #pragma unroll
             for (int c = 0; c < CS; c += 2) {
-              const float2 by = *reinterpret_cast<const float2*>(&tail->by[c_lo + c]);
-              const int2 rows = *reinterpret_cast<const int2*>(&tail->out_row[c_lo + c]);
-              const float y0 = by.x == 0.f ? 0.f : o[c] * by.x;
-              const float y1 = by.y == 0.f ? 0.f : o[c + 1] * by.y;
-              const float other = __shfl_xor_sync(kAll, lane & 1 ? y0 : y1, 1);
-              const int row = lane & 1 ? rows.y : rows.x;
-              const uint32_t two = lane & 1 ? pack2<DT>(other, y1) : pack2<DT>(y0, other);
-              if (has_dim && row >= 0)
-                *reinterpret_cast<uint32_t*>(to + (int64_t)row * S::DV) = two;
+              const int row = tail->out_row[c0 + c + (lane & 1)];
+              to[c / 2] = row >= 0 && has_dim ? static_cast<uint16_t*>(a.out) +
+                                                    (int64_t)row * S::DV + (dim0 & ~1)
+                                              : nullptr;
+              none = none || by[c] == 0.f || by[c + 1] == 0.f;
             }
-          } else if (has_dim) {
-            float* to = a.ws_acc + (part * N + c_lo) * S::DV + dim;
+#pragma unroll 1
+            for (int v = 0; v < S::VT; ++v) {
+              float o[CS];
+              tmem_ld16(ocol + quarter + v * N + c0, o);
 #pragma unroll
-            for (int c = 0; c < CS; ++c)
-              if (c_lo + c < a.gh * a.gn) to[c * S::DV] = o[c];
+              for (int c = 0; c < CS; ++c) o[c] *= by[c];
+              if (none) {
+#pragma unroll
+                for (int c = 0; c < CS; ++c) o[c] = by[c] == 0.f ? 0.f : o[c];
+              }
+#pragma unroll
+              for (int c = 0; c < CS; c += 2) {
+                const float other = __shfl_xor_sync(kAll, lane & 1 ? o[c] : o[c + 1], 1);
+                const uint32_t two =
+                    pack2<DT>(lane & 1 ? other : o[c], lane & 1 ? o[c + 1] : other);
+                if (to[c / 2]) *reinterpret_cast<uint32_t*>(to[c / 2] + v * S::VM) = two;
+              }
+            }
+          } else {
+            float* to = a.ws_acc + (part * N + c0) * S::DV + dim0;
+#pragma unroll 1
+            for (int v = 0; v < S::VT; ++v) {
+              float o[CS];
+              tmem_ld16(ocol + quarter + v * N + c0, o);
+#pragma unroll
+              for (int c = 0; c < CS; ++c)
+                if (has_dim && c0 + c < a.gh * a.gn) to[c * S::DV + v * S::VM] = o[c];
+            }
           }
         }
         tc_fence_before();
@@ -1083,18 +1124,33 @@ struct Join {
 
 template <class S, int DT, int PS>
 __global__ void __launch_bounds__(kJoinThreads)
-join_kernel(const Args a, int sets) {
+join_kernel(const Args a, int sets, int items) {
   using J = Join<S, PS>;
   constexpr int N = S::N, DV = S::DV, LANES = J::LANES, COLS = J::COLS, ROUNDS = J::ROUNDS;
   __shared__ float s_w[COLS][kMaxCtas + 1];
   __shared__ bool s_none[COLS];                            // no weight at all: zeros
   __shared__ float4 s_sum[PS > 1 ? PS : 1][PS > 1 ? COLS * LANES : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = (int)blockIdx.x + 1, r = (int)blockIdx.y;
+  const int r = (int)blockIdx.y;
   allow_next_grid();
   wait_prior_grid();
-  const Window at = a.info[c], before = a.info[c - 1];
+  int c = (int)blockIdx.x + 1;
   bool same;
+  if (PS > 1) {                                // the first boundary in item x, if any
+    __shared__ int s_c;
+    if (tid == 0) s_c = 0;
+    __syncthreads();
+    if (tid > 0 && tid < sets) {
+      const Window w = a.info[tid];
+      if (w.b == (int)blockIdx.x / items && w.item == (int)blockIdx.x % items &&
+          first_cut(w, a.info[tid - 1], &same))
+        s_c = tid;
+    }
+    __syncthreads();
+    c = s_c;
+    if (c == 0) return;
+  }
+  const Window at = a.info[c], before = a.info[c - 1];
   if (!first_cut(at, before, &same)) return;
   bool in = false;
   if (c + 1 + tid < sets) {
@@ -1296,9 +1352,10 @@ cudaError_t launch(const CUtensorMap (&maps)[3], const Args& a, int ctas, int64_
   // few items of many parts: the parts of a few columns to a CTA, else half the columns
   const bool deep = items * 8 <= sets;
   const int cols = deep ? Join<S, 4>::COLS : Join<S, 1>::COLS;
-  const dim3 grid((unsigned)(sets - 1), (unsigned)a.gs, (unsigned)((S::N + cols - 1) / cols));
+  const dim3 grid((unsigned)(deep ? items : sets - 1), (unsigned)a.gs,
+                  (unsigned)((S::N + cols - 1) / cols));
   return launch_pdl(deep ? join_kernel<S, DT, 4> : join_kernel<S, DT, 1>, grid, kJoinThreads, 0,
-                    stream, a, sets);
+                    stream, a, sets, (int)(items / a.B));
 }
 
 // The shape of N columns.
