@@ -550,7 +550,10 @@ pa_status pa_expand_blocks_q8(void* k_pool, void* v_pool, const void* k_pool8, c
  * in checked mode); a bad block id's rows read as zeros (reported).  Rows behind the
  * last sequence are left alone.
  * Scores, softmax statistics and sums are fp32.  The softmax weights enter the product
- * with V as two terms of the storage type (15 bits or more).
+ * with V as two terms of the storage type (15 bits or more) where a KV head has at most 32
+ * columns (max_q_len * num_q_heads / num_kv_heads), else rounded to it once (bf16 2^-8 of
+ * the weight at most, fp16 2^-11): with more columns the second term is no longer hidden
+ * behind the cache's bytes.
  * workspace: at least pa_decode_tree_workspace_bytes(...) bytes (0 for invalid
  * arguments), 256-byte aligned, contents arbitrary, not shared by calls that overlap on
  * the GPU.
@@ -634,10 +637,7 @@ pa_status pa_latent_gather(void* out, const void* pool, const int32_t* block_tab
  * over the t that the row sees: one new token per sequence (q_start NULL) or several, a
  * chain or a tree, all as in pa_decode_tree, with its rules for bad data and rows that
  * see nothing.
- * The softmax weights enter the product as two terms of the storage type where a call
- * has at most 32 columns (max_q_len * num_q_heads), else rounded to it once (bf16 2^-8
- * of the weight at most, fp16 2^-11): with more columns the second term is no longer
- * hidden behind the cache's bytes.
+ * The softmax weights are rounded as in pa_decode_tree (columns: max_q_len * num_q_heads).
  * Supported: fp16 / bf16, latent_dim 256 or 512, rope_dim 64, block_size 8/16/32/64,
  * any num_q_heads; max_q_len * num_q_heads <= 65536, max_seq_len < 2^30, a pool of less
  * than 2^31 rows.

@@ -7,12 +7,13 @@
 namespace pa {
 namespace {
 
-// The second term of the weights is free: the cache's bytes and the softmax take longer than
-// both products.
+// Up to 32 columns the second term of the weights costs nothing: the cache's bytes take longer.
+// With 64 it would cost 10% (16-token trees of 64 sequences, 125 us for 113) to 27% (a 60-token
+// tree over 50,001 tokens, 188 us for 148), its rows shared memory that tiles are on their way to.
 template <int N>
-using Tree128 = multi::Shape<128, 2, 2, false, N, 2>;
+using Tree128 = multi::Shape<128, 2, 2, false, N, N <= 32 ? 2 : 1>;
 template <int N>
-using Tree64 = multi::Shape<128, 1, 1, false, N, 2>;
+using Tree64 = multi::Shape<128, 1, 1, false, N, N <= 32 ? 2 : 1>;
 
 }  // namespace
 }  // namespace pa
@@ -55,7 +56,8 @@ extern "C" pa_status pa_decode_tree(void* out, const void* q, const void* k_pool
   st = multi::check(c, pa_decode_tree_workspace_bytes(num_q_heads, num_kv_heads, head_dim,
                                                       max_q_len), &work);
   if (st != PA_OK || !work) return st;
-  return multi::run(c, 128, head_dim, head_dim / 64, true, [&](int n, auto&&... x) {
+  return multi::run(c, Tree128<16>::TOK, head_dim, head_dim / 64, true,
+                    [&](int n, auto&&... x) {
     if (head_dim == 128)
       return dtype == PA_BFLOAT16
                  ? multi::launch_columns<Tree128, PA_BFLOAT16>(n, x..., stream)

@@ -104,7 +104,7 @@ struct Shape {
   static constexpr int units_with(int qbufs) {
     return (kBudget - qbufs * QBYTES - 2 * PBYTES) / UNIT;
   }
-  static constexpr int QBUFS = units_with(2) >= (SHARED ? 2 : 4) ? 2 : 1;
+  static constexpr int QBUFS = units_with(2) >= (SHARED ? 2 : 5) ? 2 : 1;
   static constexpr int RING = units_with(QBUFS) > 8 ? 8 : units_with(QBUFS);
   static_assert(RING >= (SHARED ? 2 : 3), "ring too shallow");
   static constexpr int kQOff = RING * UNIT;
@@ -1117,8 +1117,8 @@ template <class S, int PS>
 struct Join {
   static constexpr int LANES = S::DV / 4;                          // threads of a column
   static constexpr int AT_ONCE = kJoinThreads / LANES / PS;        // columns at once
-  // columns of a CTA: with few parts half of them, all asked for at once
-  static constexpr int COLS = PS > 1 ? AT_ONCE : S::N / 2;
+  // columns of a CTA: with few parts half of them or a quarter, all asked for at once
+  static constexpr int COLS = PS > 1 ? AT_ONCE : (S::DV > 256 ? S::N / 4 : S::N / 2);
   static constexpr int ROUNDS = COLS > AT_ONCE ? COLS / AT_ONCE : 1;
 };
 
