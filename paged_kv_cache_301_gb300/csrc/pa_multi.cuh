@@ -479,12 +479,6 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     tmem_alloc(&tail->tmem, S::kCols);
     tmem_relinquish();
   }
-  // block ids stand at the end of a chain of loads: into L2 while the window is found
-  for (int64_t i = ((int64_t)blockIdx.x * kThreads + tid) * 32; i < (int64_t)a.B * a.max_blocks;
-       i += (int64_t)gridDim.x * kThreads * 32) {
-    prefetch_l2(a.tables + i);
-    if (i > (1 << 22)) break;
-  }
   // rows of q that no copy writes
   if (a.gh * a.gn < N) {
     for (int i = tid; i < QB * S::QBYTES / 16; i += kThreads)
@@ -927,7 +921,8 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           const int row = TOK == 64 ? wq * 16 + (lane & 15) : wq * 32 + lane;
           const int mine = grp * SIDES + (TOK == 64 ? lane >> 4 : 0), tok = j * TOK + row;
           uint8_t* vrow = smem + (u % R) * S::UNIT + (row >> 3) * S::VGS + (row & 7) * 128;
-          auto at = [&](int x) { return vrow + (x >> 3) * 1024 + (x & 7) * 16; };
+          // lanes side by side over the banks
+          auto at = [&](int x) { return vrow + (x >> 3) * 1024 + ((x ^ row) & 7) * 16; };
           bool zero = tok >= g.L;
           if (fresh) {
             bool odd = false;
