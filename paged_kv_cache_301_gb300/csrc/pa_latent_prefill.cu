@@ -20,9 +20,14 @@
 // Weights are rounded to the storage type once (half a step: bf16 2^-8, fp16 2^-11 of each):
 // a second term would cost another product, as much as the first.
 //
-// Bound: the tensor cores and the exponentials, 2,600 cycles of either for 256 rows and 128
-// keys.  CTAs of one sequence and head stand side by side in the grid, so that their keys and
-// values come from L2.
+// Bound: for 256 rows and 128 keys the tensor cores take 2,600 cycles and the exponentials
+// 2,050; a query tile's own chain (scores, softmax, product, and the waits between them) takes
+// 4,000 and two tiles overlap in part.
+//
+// Measured (GB300; cuBLAS 1,880 TFLOP/s): four prompts of 960 to 3,648 tokens, 32 heads, bf16
+// 269 us, 960 TFLOP/s; six chunks of 500 tokens over prefixes of up to 8,000, 16 heads, fp16
+// 125 us: the longest prefix's 64 tiles of keys are one CTA's chain.  Tried: values asked for in
+// halves (287 us for the prompts).
 //
 // Values that a row does not see have no part in it: those behind the sequence's end are
 // zeroed in shared memory, and in the tiles that cut the diagonal so are rows that hold
@@ -76,7 +81,7 @@ struct Args {
 };
 
 struct Tail {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full;
+  uint64_t k_full[2], k_empty[2], v_full, v_empty, q_full;
   uint64_t s_full[2], p_full[2], pv_done[2];     // of the query tiles
   uint64_t odd_full[2], drain;
   uint32_t odd[2][4];            // rows of V that are added apart, in A's tiles on the diagonal
@@ -149,7 +154,6 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_kv,
-                      const __grid_constant__ CUtensorMap map_v,
                       const __grid_constant__ CUtensorMap map_r, const Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -160,8 +164,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0);
   allow_next_grid();
   wait_prior_grid();
-  // the pairs of query tiles of one sequence and head side by side, the longest first
-  const int bh = blockIdx.x / a.pairs, pair = a.pairs - 1 - (int)(blockIdx.x - bh * a.pairs);
+  // the pairs of query tiles with the longest causal work first, so that the last CTAs to run
+  // are short (four prompts of 32 heads: 269 us; pairs of one sequence and head side by side,
+  // whose keys and values stay in L2: 287)
+  const int bhs = gridDim.x / a.pairs, bh = blockIdx.x % bhs;
+  const int pair = a.pairs - 1 - (int)(blockIdx.x / bhs);
   const int b = bh / a.H, h = bh - b * a.H;
   const int qs = a.q_start[b], n = a.q_start[b + 1] - qs;
   const int ks = a.kv_start[b], L = a.kv_start[b + 1] - ks;
@@ -183,14 +190,14 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tl->k_full[i], 1);
       mbar_init(&tl->k_empty[i], 1);
-      mbar_init(&tl->v_full[i], 1);
-      mbar_init(&tl->v_empty[i], 1);
       mbar_init(&tl->s_full[i], 1);
       mbar_init(&tl->p_full[i], 4);
       mbar_init(&tl->pv_done[i], 1);
       mbar_init(&tl->odd_full[i], 4);
       tl->keep[i] = 0;
     }
+    mbar_init(&tl->v_full, 1);
+    mbar_init(&tl->v_empty, 1);
     mbar_init(&tl->q_full, 1);
     mbar_init(&tl->drain, 1);
     tl->abort_flag = 0;
@@ -235,24 +242,18 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
         tma_slab(kt + kSlab, &map_kv, &tl->k_full[s], 64, h, row);
         tma_slab(kt + 2 * kSlab, &map_r, &tl->k_full[s], 0, 0, row);
         ++k_used;
-        // values by halves of the keys: the first comes while the last product reads the second
-        for (int half = 0; half < 2 && ok; ++half) {
-          ok = mbar_wait(&tl->v_empty[half], (t & 1) ^ 1, abort_flag, kLimitNs);
-          if (!ok) break;
-          uint8_t* vt = smem + kVOff + half * (kSlab / 2);
-          mbar_arrive_expect_tx(&tl->v_full[half], kVTile / 2);
-          for (int x = 0; x < kVSlabs; ++x)
-            tma_slab(vt + x * kSlab, &map_v, &tl->v_full[half], kDk - kRope + 64 * x, h,
-                     row + half * (kKeys / 2));
-          ++v_used;
-        }
+        ok = mbar_wait(&tl->v_empty, (t & 1) ^ 1, abort_flag, kLimitNs);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&tl->v_full, kVTile);
+        tma_slab(smem + kVOff, &map_kv, &tl->v_full, kDk - kRope, h, row);
+        tma_slab(smem + kVOff + kSlab, &map_kv, &tl->v_full, kDk - kRope + 64, h, row);
+        ++v_used;
       }
       if (!ok) set_abort();
       if (*abort_flag) {                       // copies in flight land before the CTA ends
         for (int t = max(0, k_used - 2); t < k_used; ++t)
           mbar_wait_drain(&tl->k_full[t & 1], (t >> 1) & 1, kLimitNs);
-        for (int v = max(0, v_used - 2); v < v_used; ++v)
-          mbar_wait_drain(&tl->v_full[v & 1], (v >> 1) & 1, kLimitNs);
+        if (v_used) mbar_wait_drain(&tl->v_full, (v_used - 1) & 1, kLimitNs);
         mbar_wait_drain(&tl->q_full, 0, kLimitNs);
       }
     }
@@ -279,20 +280,13 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       commit_by_one(&tl->s_full[k]);
       issued = true;
     };
-    // `last`: no other product reads this tile's values
-    auto issue_pv = [&](int k, int t, bool last) -> bool {
+    auto issue_pv = [&](int k, int t) {
       const uint32_t keep = t > 0 || *const_cast<volatile int*>(&tl->keep[k]);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!wait(&tl->v_full[half], t & 1)) return false;
-#pragma unroll
-        for (int x = half * (kKeys / 32); x < (half + 1) * (kKeys / 32); ++x)
-          mma_ts_by_one(tmem + 256 + k * kDv, tmem + k * kKeys + x * 8,
-                        v_desc + (uint64_t)(x * 16 * 128 >> 4), idesc_o, x > 0 ? 1u : keep);
-        if (last) commit_by_one(&tl->v_empty[half]);
-      }
+      for (int x = 0; x < kKeys / 16; ++x)
+        mma_ts_by_one(tmem + 256 + k * kDv, tmem + k * kKeys + x * 8,
+                      v_desc + (uint64_t)(x * 16 * 128 >> 4), idesc_o, x > 0 ? 1u : keep);
       commit_by_one(&tl->pv_done[k]);
-      return true;
     };
     ok = wait(&tl->q_full, 0) && wait(&tl->k_full[0], 0);
     if (ok) {
@@ -302,6 +296,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       commit_by_one(&tl->k_empty[0]);
     }
     for (int t = 0; t <= last_all && ok; ++t) {
+      ok = wait(&tl->v_full, t & 1);
       bool next_k = false;
       for (int k = 0; k < 2 && ok; ++k) {
         const int last = k ? last_b : last_a;
@@ -309,8 +304,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
         ok = wait(&tl->p_full[k], t & 1);
         if (!ok) break;
         tc_fence_after();
-        ok = issue_pv(k, t, k == 1 || t > last_b);
-        if (!ok) break;
+        issue_pv(k, t);
+        if (k == 1 || t > last_b) commit_by_one(&tl->v_empty);    // its last product
         if (t + 1 <= last) {
           // S of the next keys goes over P: once the product has read it
           ok = (next_k || wait(&tl->k_full[(t + 1) & 1], ((t + 1) >> 1) & 1)) &&
@@ -421,10 +416,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       const bool ends = kc + kKeys > L && (k == 0 || t > last_a);
       uint32_t* words = on_a ? tl->odd[(t - cut_a) & 1] : tl->odd_b;
       if (ends || mine) {
-        if (!wait_all(&tl->v_full[0], t & 1) || !wait_all(&tl->v_full[1], t & 1)) {
-          ok = false;
-          break;
-        }
+        if (!wait_all(&tl->v_full, t & 1)) { ok = false; break; }
         // 16 bytes of the row at a time, lanes side by side over the banks
         auto part = [&](int x) {
           return smem + kVOff + (x >> 3) * kSlab + r * 128 + ((x ^ r) & 7) * 16;
@@ -567,13 +559,12 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [rows, heads, width], rows `stride` elements apart; a box is `box_rows` rows of 64 elements of
-// a head.
+// [rows, heads, width], rows `stride` elements apart; a box is 128 rows of 64 elements of a head.
 bool encode_rows(CUtensorMap* map, const void* x, int dtype, int64_t rows, int heads, int width,
-                 int64_t stride, int box_rows) {
+                 int64_t stride) {
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, ones[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, 128}, ones[3] = {1, 1, 1};
   return encode_fn()(map,
                      dtype == PA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
@@ -584,7 +575,7 @@ bool encode_rows(CUtensorMap* map, const void* x, int dtype, int64_t rows, int h
 }
 
 template <int DT>
-cudaError_t launch(const CUtensorMap (&m)[4], const Args& a, int ctas, int device,
+cudaError_t launch(const CUtensorMap (&m)[3], const Args& a, int ctas, int device,
                    cudaStream_t stream) {
   static std::mutex lock;
   static uint64_t done = 0;                    // devices whose attribute is set
@@ -598,7 +589,7 @@ cudaError_t launch(const CUtensorMap (&m)[4], const Args& a, int ctas, int devic
     }
   }
   return launch_pdl(latent_prefill_kernel<DT>, dim3((unsigned)ctas), kThreads, kSmem, stream, m[0],
-                    m[1], m[2], m[3], a);
+                    m[1], m[2], a);
 }
 
 }  // namespace
@@ -635,14 +626,11 @@ extern "C" pa_status pa_latent_prefill(void* out, const void* q, const void* kv,
   if (!encode_fn() || taken(cudaGetDevice(&device)) != cudaSuccess) return PA_ERR_CUDA;
   // without a token every sequence is bad or empty: the maps are not read
   const int64_t rows = total_kv > 0 ? total_kv : 1;
-  const void* kvs = total_kv > 0 ? kv : q;
-  const int64_t kv_row = (int64_t)num_heads * kKv;
-  CUtensorMap m[4];
-  if (!encode_rows(&m[0], q, dtype, total_q, num_heads, kDk, (int64_t)num_heads * kDk, kRows) ||
-      !encode_rows(&m[1], kvs, dtype, rows, num_heads, kKv, kv_row, kKeys) ||
-      !encode_rows(&m[2], kvs, dtype, rows, num_heads, kKv, kv_row, kKeys / 2) ||
-      !encode_rows(&m[3], total_kv > 0 ? key_rope : q, dtype, rows, 1, kRope, key_token_stride,
-                   kKeys))
+  CUtensorMap m[3];
+  if (!encode_rows(&m[0], q, dtype, total_q, num_heads, kDk, (int64_t)num_heads * kDk) ||
+      !encode_rows(&m[1], total_kv > 0 ? kv : q, dtype, rows, num_heads, kKv,
+                   (int64_t)num_heads * kKv) ||
+      !encode_rows(&m[2], total_kv > 0 ? key_rope : q, dtype, rows, 1, kRope, key_token_stride))
     return PA_ERR_INVALID_ARG;
   Args a;
   a.out = out;
