@@ -33,6 +33,19 @@
 // two groups of four with columns of their own, softmax and output.  Every wait is bounded; one
 // that runs out sets an abort flag, copies and MMAs in flight are drained, TMEM is freed and
 // PA_ERR_TIMEOUT is reported through status_dev.
+//
+// Measured (GB300, bf16; of a plain copy's 6.8 TB/s):
+//   pa_decode_tree, 64 sequences of 128..4,096, 16 drafted, 32/8 heads of 128: 107 us, 5.35
+//     TB/s, 0.79; one of 50,001, 60 drafted, 40/8: 148-152 us; 4 short ones of 4 heads: 8.0 us
+//   pa_latent_decode, 64 sequences of 128..4,096, 128 heads: 78-80 us; 8 of 32,768..131,072, 16
+//     heads, 3 drafted: 139 us, 5.4 TB/s, 0.80; 4 short ones of 16 heads, latent 256: 7.6 us
+// About 14,000 cycles pass from a CTA's start to its first tile, 6,000 from its last product to
+// its last store, and 10 us in the join of many parts; in between trees and long latent
+// sequences run at the memory's rate, 128 heads at 3,300 cycles a tile (the operands' reads from
+// shared memory: 2,000).
+// Tried: tiles of 64 tokens for head_dim 128 (tree 138 us, was 125), a latent tile in halves (82,
+// was 80), the second product always first (218, was 190), polls of tile and weights at once
+// (they take the softmax's issue slots).
 #pragma once
 
 #include <math.h>
@@ -53,7 +66,9 @@ using namespace sm100;
 constexpr int kMaxCtas = 160;                  // CTAs at most (one per SM; GB300: 152)
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kEnds = 12;                       // cost of an item's ends, in quarters of a tile
+// cost of an item's ends, in quarters of a tile (16-token trees of 64 sequences: with 4 139 us,
+// 8 129, 12 127, 16 126)
+constexpr int kEnds = 12;
 constexpr float kRaise = 8.f;                  // log2 by which a tile may exceed the maximum
 
 struct Args {
@@ -407,27 +422,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-
-// Four values of each of four lanes: lane i's value j to lane j's value i.
-__device__ __forceinline__ void transpose4(float& a, float& b, float& c, float& d, int lane) {
-  const bool odd = lane & 1, high = lane & 2;
-  const float x = __shfl_xor_sync(kAll, odd ? a : b, 1), y = __shfl_xor_sync(kAll, odd ? c : d, 1);
-  if (odd) {
-    a = x;
-    c = y;
-  } else {
-    b = x;
-    d = y;
-  }
-  const float u = __shfl_xor_sync(kAll, high ? a : c, 2), v = __shfl_xor_sync(kAll, high ? b : d, 2);
-  if (high) {
-    a = u;
-    b = v;
-  } else {
-    c = u;
-    d = v;
-  }
 }
 
 // Of two storage-type values in a word: is one infinite or NaN?
