@@ -9,8 +9,8 @@
 // number alone, so its loads are asked for before that chain begins.
 //
 // Measured (GB300, bf16, latent 512): append of 64 tokens with 16 heads 2.8 us; of 18,432 prompt
-// tokens with 32 heads 38.4 us, 5.1 TB/s, 0.75 of a plain copy; gather of 65,536 rows 26.2 us,
-// 5.8 TB/s, 0.85.
+// tokens with 32 heads 35.2 us, 5.5 TB/s, 0.81 of a plain copy; gather of 65,536 rows 25.2 us,
+// 6.0 TB/s, 0.88.
 #include <math.h>
 
 #include "pa_common.cuh"
@@ -21,10 +21,13 @@ namespace pa {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kWarps = 8;
+// Small CTAs, and little to a warp: 18,432 prompt tokens with eight warps of four groups of heads
+// 38.5 us, eight of two 37.8, four of two 35.7, two of two 35.2, one of two 57 (an SM holds 32
+// CTAs).
+constexpr int kWarps = 2;
 constexpr int kRope = 64;
 constexpr int kHeads = 8;              // query heads that a warp turns at once: four lanes each
-constexpr int kChunks = 4;             // such groups of heads to a warp
+constexpr int kChunks = 2;             // such groups of heads to a warp
 
 struct AppendArgs {
   void* pool;
@@ -255,9 +258,9 @@ struct GatherArgs {
   int32_t* status_dev;
 };
 
-constexpr int kGatherRows = 8;         // rows to a warp
+constexpr int kGatherRows = 4;         // rows to a warp (with eight, 65,536 rows 26.2 us, now 25.2)
 
-// Eight rows of out to a warp, its lanes side by side over all of them: 9 KB asked for at
+// Four rows of out to a warp, its lanes side by side over all of them: 4.6 KB asked for at
 // once at latent_dim 512.
 template <int R>
 __global__ void __launch_bounds__(32 * kWarps) latent_gather_kernel(const GatherArgs a) {
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_gather_kernel(const Gather
   wait_prior_grid();
   if (r0 >= a.total) return;
   const int first = find_seq(a.kv_start, a.B, (int)r0, lane);
-  // lane i < 8: the slot of row r0 + i (-1: zeros, -2: not written)
+  // lane i < kGatherRows: the slot of row r0 + i (-1: zeros, -2: not written)
   int64_t slot = -2;
   const int row = (int)r0 + lane;
   if (lane < kGatherRows && r0 + lane < a.total) {
