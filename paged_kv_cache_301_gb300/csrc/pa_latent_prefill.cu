@@ -472,8 +472,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
               const float2 p2 = widen2<DT>(tmem_ld1(scol + x / 2));
               const bool seen = kc + x <= pos;
               const float p = x & 1 ? p2.y : p2.x;
-              const uint32_t* v = static_cast<const uint32_t*>(a.kv) +
-                                  ((int64_t)(ks + kc + x) * a.H + h) * (kKv / 2) + (kDk - kRope) / 2;
+              const uint32_t* v = static_cast<const uint32_t*>(a.kv) + (kDk - kRope) / 2 +
+                                  ((int64_t)(ks + kc + x) * a.H + h) * (kKv / 2);
 #pragma unroll 1
               for (int c0 = 0; c0 < kDv; c0 += 16) {
                 float o[16];
@@ -523,7 +523,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               dst[c0 / 8 + c] =
-                  make_uint4(pack2<DT>(o[8 * c], o[8 * c + 1]), pack2<DT>(o[8 * c + 2], o[8 * c + 3]),
+                  make_uint4(pack2<DT>(o[8 * c], o[8 * c + 1]),
+                             pack2<DT>(o[8 * c + 2], o[8 * c + 3]),
                              pack2<DT>(o[8 * c + 4], o[8 * c + 5]),
                              pack2<DT>(o[8 * c + 6], o[8 * c + 7]));
           }

@@ -1334,8 +1334,8 @@ cudaError_t launch(const CUtensorMap (&maps)[3], const Args& a, int ctas, int64_
       if (device < 64) done |= 1ull << device;
     }
   }
-  cudaError_t e = launch_pdl(multi_kernel<S, DT>, dim3((unsigned)ctas), S::kThreads, S::kSmem, stream,
-                             maps[0], maps[1], maps[2], a);
+  cudaError_t e = launch_pdl(multi_kernel<S, DT>, dim3((unsigned)ctas), S::kThreads, S::kSmem,
+                             stream, maps[0], maps[1], maps[2], a);
   const int sets = ctas / a.gs;
   if (e != cudaSuccess || !cut || sets < 2) return e;
   // few items of many parts: the parts of a few columns to a CTA, else half the columns

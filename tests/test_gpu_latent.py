@@ -154,6 +154,19 @@ def test_decode_bad_data(pa):
     b.check()
 
 
+@pytest.mark.parametrize("H", [65, 130, 200])
+def test_decode_heads_that_do_not_fill_a_group(pa, H):
+    Batch([200, 7, 300], [2, 1, 3], H, 256, 16, "bf16").run(pa).check(heads=[0, 63, 64, H - 1])
+
+
+def test_decode_a_bound_whose_costs_pass_32_bits(pa):
+    g = np.random.default_rng(8)
+    lens = [int(x) for x in g.integers(0, 900, size=70)]
+    b = Batch(lens, [1] * 70, 128, 512, 16, "bf16", "one")
+    assert 70 * 4 * ((1 << 30) // 64) > 1 << 31
+    b.run(pa, max_seq_len=(1 << 30) - 1).check(heads=[0, 100])
+
+
 def test_decode_graph_replay_and_stream(pa):
     b = Batch([3000, 900, 0], [1] * 3, 128, 512, 16, "bf16", "one")
     s = torch.cuda.Stream()

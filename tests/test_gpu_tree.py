@@ -213,6 +213,22 @@ def test_offsets_past_32_bits(pa):
     b.check()
 
 
+def test_a_bound_whose_costs_pass_32_bits(pa):
+    """max_seq_len may be far more than the lengths are: the shares are then counted in 64 bits."""
+    g = np.random.default_rng(8)
+    lens = [int(x) for x in g.integers(1, 900, size=70)]
+    counts = [int(min(n, x)) for n, x in zip(lens, g.integers(0, 9, size=70))]
+    b = Batch(lens, counts, 16, 8, 128, 16, "bf16")
+    assert 70 * 8 * 4 * ((1 << 30) // 128) > 1 << 31
+    b.run(pa, max_seq_len=(1 << 30) - 1).check()
+
+
+@pytest.mark.parametrize("Hq,H", [(96, 1), (130, 2), (70, 1), (12, 4)])
+def test_heads_that_do_not_fill_a_group(pa, Hq, H):
+    """More query heads to a KV head than columns of a product, and odd shares of them."""
+    Batch([200, 7, 300], [3, 1, 2], Hq, H, 64, 16, "bf16").run(pa).check()
+
+
 def test_the_tree_mask_helper(pa):
     g = np.random.default_rng(3)
     parents = [chain_or_tree(n, "tree", g) for n in (5, 40, 1)]
