@@ -595,8 +595,9 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
  *                of the same rows; any other overlap with an input is rejected.
  *   weight       [latent_dim] storage type, nullable
  *   cos_sin      [max_position, rope_dim] fp32, nullable; positions as in pa_rope_append
- * Strides are multiples of 8 elements, addresses 16-byte aligned.  q_start, bad
- * sequences, positions and block ids as in pa_rope_append.
+ * Strides are multiples of 8 elements, times their count at most 2^40; addresses
+ * are 16-byte aligned.  q_start, bad sequences, positions and block ids as in
+ * pa_rope_append.
  * Supported: fp16 / bf16, latent_dim 256 or 512, rope_dim 64, block_size 8/16/32/64.
  */
 pa_status pa_latent_append(void* pool, const void* latent, const void* key_rope,
@@ -616,7 +617,7 @@ pa_status pa_latent_append(void* pool, const void* latent, const void* key_rope,
  * a cached prefix takes: rows kv_start[b] .. kv_start[b+1]-1 of out are tokens
  * 0 .. n_b - 1 of sequence b.  Bit copies.
  *   out          [total_kv, latent_dim + rope_dim], token stride out_token_stride (0 =
- *                packed; a multiple of 8 elements)
+ *                packed; a multiple of 8 elements, times total_kv at most 2^40)
  *   kv_start     [num_seqs + 1] int32, non-decreasing
  * A sequence with n_b > seq_lens[b], seq_lens[b] past its table, or rows outside [0,
  * total_kv) is skipped (reported in checked mode); a bad block id's rows become zeros

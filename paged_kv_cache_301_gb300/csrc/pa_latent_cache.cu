@@ -320,6 +320,13 @@ bool overlaps(const void* p, int64_t n, const void* q, int64_t m) {
 // Bytes from the first to the last element of rows of `row` elements, `stride` apart.
 int64_t span(int64_t rows, int64_t stride, int64_t row) { return 2 * ((rows - 1) * stride + row); }
 
+// Whether n steps of `stride` elements stay within 2^40 elements, so that byte offsets and their
+// sums fit 64 bits.
+bool within(int64_t n, int64_t stride) {
+  const int64_t most = 1ll << 40;
+  return stride <= most && (n <= 0 || stride <= most / n);
+}
+
 bool known(int latent_dim, int rope_dim, int block_size, int dtype) {
   return (latent_dim == 256 || latent_dim == 512) && rope_dim == kRope &&
          (block_size == 8 || block_size == 16 || block_size == 32 || block_size == 64) &&
@@ -336,12 +343,14 @@ pa_status check_append(const AppendArgs& a, int R) {
     return PA_ERR_INVALID_ARG;
   if (((a.latent_stride | a.key_stride) & 7) || a.latent_stride < R || a.key_stride < kRope)
     return PA_ERR_INVALID_ARG;
-  const int64_t most = 1ll << 40;              // elements between tokens: products fit 64 bits
-  if (a.latent_stride > most || a.key_stride > most) return PA_ERR_INVALID_ARG;
+  if (!within(a.total_q, a.latent_stride) || !within(a.total_q, a.key_stride))
+    return PA_ERR_INVALID_ARG;
   if (!a.q) return PA_OK;
+  if (!within(a.Hq, a.q_head) || !within(a.Hq, a.out_head) || !within(a.total_q, a.q_stride) ||
+      !within(a.total_q, a.out_stride))
+    return PA_ERR_INVALID_ARG;
   if (((a.q_stride | a.q_head | a.out_stride | a.out_head) & 7) || a.q_head < kRope ||
-      a.out_head < kRope || a.q_stride > most || a.out_stride > most ||
-      a.q_stride < (a.Hq - 1) * a.q_head + kRope ||
+      a.out_head < kRope || a.q_stride < (a.Hq - 1) * a.q_head + kRope ||
       a.out_stride < (a.Hq - 1) * a.out_head + kRope)
     return PA_ERR_INVALID_ARG;
   const int64_t T = a.total_q, heads = a.Hq;
@@ -394,9 +403,9 @@ extern "C" pa_status pa_latent_append(
   a.latent_stride = latent_token_stride ? latent_token_stride : latent_dim;
   a.key_stride = key_token_stride ? key_token_stride : rope_dim;
   a.q_head = q_head_stride ? q_head_stride : rope_dim;
-  a.q_stride = q_token_stride ? q_token_stride : num_q_heads * a.q_head;
+  a.q_stride = q_token_stride;
   a.out_head = q_out_head_stride ? q_out_head_stride : rope_dim;
-  a.out_stride = q_out_token_stride ? q_out_token_stride : num_q_heads * a.out_head;
+  a.out_stride = q_out_token_stride;
   a.eps = eps;
   a.max_position = max_position;
   a.interleaved = interleaved;
@@ -408,6 +417,10 @@ extern "C" pa_status pa_latent_append(
   a.num_blocks = num_blocks;
   a.units = 1 + (q_rope ? (num_q_heads + kChunks * kHeads - 1) / (kChunks * kHeads) : 0);
   a.status_dev = status_dev;
+  if (within(num_q_heads, a.q_head) && within(num_q_heads, a.out_head)) {
+    if (a.q_stride == 0) a.q_stride = num_q_heads * a.q_head;
+    if (a.out_stride == 0) a.out_stride = num_q_heads * a.out_head;
+  }
   const pa_status st = check_append(a, latent_dim);
   if (st != PA_OK) return st;
   const int64_t ctas = ((int64_t)total_q * a.units + kWarps - 1) / kWarps;
@@ -432,7 +445,7 @@ extern "C" pa_status pa_latent_gather(void* out, const void* pool, const int32_t
   const int row = latent_dim + rope_dim;
   if (out_token_stride == 0) out_token_stride = row;
   if (num_seqs < 0 || total_kv < 0 || max_blocks <= 0 || num_blocks <= 0 ||
-      out_token_stride < row || (out_token_stride & 7) || out_token_stride > (1ll << 40))
+      out_token_stride < row || (out_token_stride & 7) || !within(total_kv, out_token_stride))
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_kv == 0) return PA_OK;
   if (!out || !pool || !block_tables || !seq_lens || !kv_start ||

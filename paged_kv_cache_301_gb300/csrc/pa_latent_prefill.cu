@@ -621,8 +621,10 @@ extern "C" pa_status pa_latent_prefill(void* out, const void* q, const void* kv,
   if ((((uintptr_t)out | (uintptr_t)q | (uintptr_t)kv | (uintptr_t)key_rope) & 15u) != 0)
     return PA_ERR_INVALID_ARG;
   const int64_t pairs = ((int64_t)max_q_len + 2 * kRows - 1) / (2 * kRows);
-  const int64_t ctas = (int64_t)num_seqs * num_heads * pairs;
-  if (ctas > 0x7FFFFFFF) return PA_ERR_INVALID_ARG;
+  // a factor at a time: the product of all three may pass 64 bits
+  const int64_t most = 0x7FFFFFFF, heads_of_all = (int64_t)num_seqs * num_heads;
+  if (heads_of_all > most || heads_of_all * pairs > most) return PA_ERR_INVALID_ARG;
+  const int64_t ctas = heads_of_all * pairs;
   int device = 0;
   if (!encode_fn() || taken(cudaGetDevice(&device)) != cudaSuccess) return PA_ERR_CUDA;
   // without a token every sequence is bad or empty: the maps are not read

@@ -1404,13 +1404,16 @@ pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f)
   const int64_t groups =                       // pairs of column groups
       (((int64_t)max_q + cols.gn - 1) / cols.gn * cols.chunks + cols.gs - 1) / cols.gs;
   const int64_t nt = ((int64_t)c.max_len + tok - 1) / tok;
-  const int64_t items = (int64_t)c.B * c.H * groups;
+  // a factor at a time: the product of all three may pass 64 bits
+  const int64_t most = 1ll << 31, heads_of_all = (int64_t)c.B * c.H;
+  if (heads_of_all > most || heads_of_all * groups > most) return PA_ERR_INVALID_ARG;
+  const int64_t items = heads_of_all * groups;
   int device = 0, sms = 0;
   if (!encode_fn() || taken(cudaGetDevice(&device)) != cudaSuccess ||
       taken(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
     return PA_ERR_CUDA;
   int64_t sets = (sms < kMaxCtas ? sms : kMaxCtas) / cols.gs;
-  if (items > (1ll << 31) || (items * nt) / sets >= (1ll << 30)) return PA_ERR_INVALID_ARG;
+  if ((items * nt) / sets >= (1ll << 30)) return PA_ERR_INVALID_ARG;
   if (items * nt < sets) sets = items * nt > 0 ? items * nt : 1;
   CUtensorMap maps[3];
   if (!encode_blocks(&maps[0], c.k_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||

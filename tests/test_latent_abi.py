@@ -149,6 +149,28 @@ def test_prefill_refusals(lib):
     assert g(B=0) == 0 and g(T=0) == 0 and g(mq=0) == 0
 
 
+def test_strides_whose_products_pass_64_bits(lib):
+    far, many = 1 << 40, 1 << 30
+    assert _append(lib, qh=1 << 61, qs=far) == 1 and _append(lib, oh=1 << 61, os=far) == 1
+    assert _append(lib, qh=1 << 60, os=far) == 1         # the token stride is then 2^63
+    for s in ("xs", "ks", "qs", "os"):
+        assert _append(lib, T=many, **{s: far}) == 1, s
+    assert _gather(lib, S=many, os=far) == 1
+
+
+@pytest.mark.parametrize("f", [_tree, _latent], ids=["tree", "latent"])
+def test_counts_of_work_that_pass_32_bits(lib, f):
+    kw = dict(mask=None, T=1, mx=1 << 24)
+    assert f(lib, B=1 << 30, mq=4096, **kw) == 1
+    if f is _tree:                                       # 2^30 x 2^24 x 2^9: 64 bits wrap
+        assert f(lib, B=1 << 30, Hq=1 << 24, H=1 << 24, mq=65536, **kw) == 1
+
+
+def test_prefill_work_that_passes_64_bits(lib):
+    assert _prefill(lib, B=1 << 30, T=1, S=1, H=1 << 20, mq=1 << 22) == 1
+    assert _prefill(lib, B=1 << 30, T=1, S=1, H=1 << 20, mq=(1 << 31) - 1) == 1
+
+
 def test_binding_refuses_what_the_library_cannot_see(lib):
     import paged_kv_cache_301_gb300 as pa
     bf = torch.bfloat16
