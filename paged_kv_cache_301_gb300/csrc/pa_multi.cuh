@@ -11,8 +11,10 @@
 //   S^T[TOK x N] = K_tile . Q^T            O^T[Dv x N] += V_tile^T . P^T
 // A thread of the softmax has a few columns in a few rows (tokens): sums over tokens stay in
 // its registers until the item ends.  The running maximum of a column is raised only where a
-// tile exceeds it by more than 2^8, which one vote a tile finds out; only then, and in an item's
-// first tile, the column maxima are reduced over the tokens and O is rescaled.
+// tile exceeds it by more than 2^8, or holds the first score of a column that has none yet (a
+// drafted token need not see anything of the tile that a segment begins with), which one vote a
+// tile finds out; only then, and in a segment's first tile, the column maxima are reduced over
+// the tokens and O is rescaled.
 //
 // A tile stands in shared memory as the TMA unit writes it, [8-token group][64-element slab]
 // [8 tokens][128 bytes] with the 128-byte swizzle, one copy to a block of any size.  The same
@@ -815,7 +817,9 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         if (!first) {
           bool over = false;
 #pragma unroll
-          for (int k = 0; k < K; ++k) over = over || most[k] + neg[k] > kRaise + kShift;
+          for (int k = 0; k < K; ++k)
+            over = over || (top[k] == -CUDART_INF_F ? most[k] > -CUDART_INF_F
+                                                    : most[k] + neg[k] > kRaise + kShift);
           raise = any_of(1 + grp, 128, over);
         }
         if (raise) {
