@@ -911,7 +911,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         // V of tokens behind the end, and of new tokens that not every column sees.  A row's
         // slabs are shared out to the threads that look at it.
         const bool ends = (j + 1) * TOK > g.L;
-        const bool fresh = g.n > 1 && (j + 1) * TOK > ctx;
+        const bool fresh = (g.n > 1 || a.mask) && (j + 1) * TOK > ctx;
         bool apart = false;
         if (ends || fresh) {
           if (!wait_all(&tail->full[u % R], (u / R) & 1)) { ok = false; break; }
