@@ -817,9 +817,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         if (!first) {
           bool over = false;
 #pragma unroll
-          for (int k = 0; k < K; ++k)
-            over = over || (top[k] == -CUDART_INF_F ? most[k] > -CUDART_INF_F
-                                                    : most[k] + neg[k] > kRaise + kShift);
+          for (int k = 0; k < K; ++k) over = over || most[k] > top[k] + kRaise;  // also of -inf
           raise = any_of(1 + grp, 128, over);
         }
         if (raise) {
