@@ -337,15 +337,18 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
     // fp16 weights stand 2^7 higher: below 2^-14 they would lose bits
     constexpr float kShift = DT == PA_BFLOAT16 ? 0.f : 7.f;
     float m_run = -CUDART_INF_F, l_run = 0.f;
-    bool ok = true;
-    // by time alone, not by the abort flag: the warps of a group give up together
-    auto wait_all = [&](uint64_t* bar, int parity) -> bool {
-      return __all_sync(kAll,
-                        mbar_try_wait(bar, parity) || mbar_wait_drain(bar, parity, kLimitNs));
+    // A wait that runs out, or finds that another's has, ends the waiting and nothing else: the
+    // warp goes on through its tiles, so that every thread meets the named barrier (which has no
+    // limit of its own).  Its rows are not stored.
+    const uint32_t flag = smem_addr(&tl->abort_flag);
+    auto wait_all = [&](uint64_t* bar, int parity) {
+      if (!__all_sync(kAll, mbar_try_wait(bar, parity)) &&
+          !__all_sync(kAll, mbar_wait_far<kLimitNs>(smem_addr(bar), parity, flag)))
+        *abort_flag = 1;
     };
     const int my_last = k ? last_b : last_a;
-    for (int t = 0; t <= my_last && ok; ++t) {
-      if (!wait_all(&tl->s_full[k], t & 1)) { ok = false; break; }
+    for (int t = 0; t <= my_last; ++t) {
+      wait_all(&tl->s_full[k], t & 1);
       tc_fence_after();
       const int kc = t * kKeys;
       float sv[kKeys];
@@ -396,7 +399,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       l_run = fmaf(l_run, alpha, (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]));
       // O is complete up to tile t - 1 and P . V of this one not issued yet
       if (__any_sync(kAll, raise)) {
-        if (!wait_all(&tl->pv_done[k], (t - 1) & 1)) { ok = false; break; }
+        wait_all(&tl->pv_done[k], (t - 1) & 1);
         tc_fence_after();
 #pragma unroll 1
         for (int c0 = 0; c0 < kDv; c0 += 32) {
@@ -416,7 +419,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       const bool ends = kc + kKeys > L && (k == 0 || t > last_a);
       uint32_t* words = on_a ? tl->odd[(t - cut_a) & 1] : tl->odd_b;
       if (ends || mine) {
-        if (!wait_all(&tl->v_full, t & 1)) { ok = false; break; }
+        wait_all(&tl->v_full, t & 1);
         // 16 bytes of the row at a time, lanes side by side over the banks
         auto part = [&](int x) {
           return smem + kVOff + (x >> 3) * kSlab + r * 128 + ((x ^ r) & 7) * 16;
@@ -448,16 +451,17 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
           if (lane == 0) mbar_arrive(&tl->odd_full[(t - cut_a) & 1]);
         }
         if (on_a) {                                // once a barrier: t - cut_a is 0 or 1
-          if (!wait_all(&tl->odd_full[(t - cut_a) & 1], 0)) { ok = false; break; }
+          wait_all(&tl->odd_full[(t - cut_a) & 1], 0);
         } else {
           named_barrier(1, 128);                   // B's own warps
         }
-        apart = (words[0] | words[1] | words[2] | words[3]) != 0;
+        // all four are written, unless a wait has run out
+        apart = !__any_sync(kAll, *abort_flag) && (words[0] | words[1] | words[2] | words[3]) != 0;
         if (apart) {
           // O += p v for each such row that this one sees
           tmem_wait_st();
           if (t > 0) {
-            if (!wait_all(&tl->pv_done[k], (t - 1) & 1)) { ok = false; break; }
+            wait_all(&tl->pv_done[k], (t - 1) & 1);
             tc_fence_after();
           } else if (lane == 0 && wq == 0) {
             tl->keep[k] = 1;
@@ -496,7 +500,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       }
       // consume P.V(t-1)'s completion before P(t) is released, so that the barrier cannot run
       // two phases ahead of a waiting warp
-      if (t > 0 && !wait_all(&tl->pv_done[k], (t - 1) & 1)) { ok = false; break; }
+      if (t > 0) wait_all(&tl->pv_done[k], (t - 1) & 1);
       tmem_wait_st();                            // every P word is in tensor memory
       tc_fence_before();
       fence_async_smem();
@@ -504,9 +508,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       if (lane == 0) mbar_arrive(&tl->p_full[k]);
     }
     if (my_last >= 0) {
-      if (ok) ok = wait_all(&tl->pv_done[k], my_last & 1);
-      if (!ok) {
-        if (lane == 0) set_abort();
+      wait_all(&tl->pv_done[k], my_last & 1);
+      if (__any_sync(kAll, *abort_flag)) {
+        if (lane == 0) report(a.status_dev, PA_ERR_TIMEOUT);
       } else {
         tc_fence_after();
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;

@@ -715,16 +715,21 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     // of the thread's columns: running maximum, what is added to a score before its power of
     // two, sum of the weights of the thread's rows
     float top[K], neg[K], l[K];
+    const uint32_t flag = smem_addr(&tail->abort_flag);
     int t = 0;
-    // These waits end by time alone, not by the abort flag: the warps of a group wait for the
-    // same barriers, so they give up together and none is left at a barrier of theirs.
-    auto wait_all = [&](uint64_t* bar, int parity) -> bool {
-      return __all_sync(kAll, mbar_try_wait(bar, parity) || mbar_wait_drain(bar, parity, kLimitNs));
+    // A wait that runs out, or finds that another's has, ends the waiting and nothing else: the
+    // warp goes on through the window, so that every thread meets every barrier of its group (they
+    // have no limit of their own), and the window's tiles bound what follows.  Rows of out that
+    // end behind that are not stored.
+    auto wait_all = [&](uint64_t* bar, int parity) {
+      if (!__all_sync(kAll, mbar_try_wait(bar, parity)) &&
+          !__all_sync(kAll, mbar_wait_far<kLimitNs>(smem_addr(bar), parity, flag)))
+        *abort_flag = 1;
     };
     // V . p of tile i, which frees its V
-    auto wait_product = [&](int i) -> bool {
+    auto wait_product = [&](int i) {
       const int u = S::SHARED ? i : 2 * i + 1;
-      return wait_all(&tail->empty[u % R], (u / R) & 1);
+      wait_all(&tail->empty[u % R], (u / R) & 1);
     };
     auto sync = [&]() { named_barrier(1 + grp, 128); };
     // a column's value in all rows of the warp, from its lanes'
@@ -735,7 +740,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     };
     auto larger = [](float x, float y) { return fmaxf(x, y); };
     auto plus = [](float x, float y) { return x + y; };
-    while (ok && walk.next(a, r, &g)) {
+    while (walk.next(a, r, &g)) {
       if (!g.active) continue;
       const int ctx = g.L - g.n;
       // the columns of this item (those of the one before have been read)
@@ -776,7 +781,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
             tail->seen[c_lo + st][w] = bits;
           }
         }
-        if (!wait_all(&tail->s_full[t & 1], (t >> 1) & 1)) { ok = false; break; }
+        wait_all(&tail->s_full[t & 1], (t >> 1) & 1);
         tc_fence_after();
         if (edge) sync();
         float s[HALVES][NC / 8][4];
@@ -845,7 +850,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
             }
             sync();
             // O (complete up to the tile before; this one's product waits for its weights)
-            if (!wait_product(t - 1)) { ok = false; break; }
+            wait_product(t - 1);
             tc_fence_after();
 #pragma unroll 1
             for (int v = 0; v < S::VT; ++v)
@@ -912,7 +917,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         const bool fresh = (g.n > 1 || a.mask) && (j + 1) * TOK > ctx;
         bool apart = false;
         if (ends || fresh) {
-          if (!wait_all(&tail->full[u % R], (u / R) & 1)) { ok = false; break; }
+          wait_all(&tail->full[u % R], (u / R) & 1);
           constexpr int SIDES = TOK == 64 ? 2 : 1, PARTS = SIDES * S::GROUPS;
           const int row = TOK == 64 ? wq * 16 + (lane & 15) : wq * 32 + lane;
           const int mine = grp * SIDES + (TOK == 64 ? lane >> 4 : 0), tok = j * TOK + row;
@@ -952,7 +957,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         if (lane == 0) mbar_arrive(&tail->p_full[t & 1]);
         if (apart) {
           // o += p v for each such row, where the column sees it
-          if (!wait_product(t)) { ok = false; break; }
+          wait_product(t);
           tc_fence_after();
 #pragma unroll 1
           for (int w = 0; w < 4; ++w) {
@@ -975,8 +980,10 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
                     }
               sync();
               const int id = a.tables[(int64_t)g.b * a.max_blocks + (at >> a.bs_shift)];
-              const int64_t slot = ((int64_t)id << a.bs_shift) + (at & ((1 << a.bs_shift) - 1));
-              const uint16_t* vsrc =                     // in the pool: a bad block's are zeros
+              // in the pool: a bad block's are zeros, unless its copy has not come
+              const int64_t slot = ((int64_t)(id >= 0 && id < a.num_blocks ? id : 0) << a.bs_shift) +
+                                   (at & ((1 << a.bs_shift) - 1));
+              const uint16_t* vsrc =
                   static_cast<const uint16_t*>(a.v_src) +
                   (S::SHARED ? slot * (64 * S::QS) : (slot * a.H + g.h) * S::DV);
 #pragma unroll 1
@@ -1025,10 +1032,11 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           tail->by[c] = sum == 0.f ? 0.f : 1.f / sum;
           if (!whole) a.ws_l[part * N + c] = sum;
         }
-        if (!wait_product(t)) { ok = false; break; }
+        wait_product(t);
         sync();
         tc_fence_after();
         const bool has_dim = S::VM == 128 || lane < 16;
+        const bool stores = has_dim && !*abort_flag;
         const int dim0 = S::VM == 128 ? wq * 32 + lane : wq * 16 + (lane & 15);
         constexpr int CS = 16;
 #pragma unroll 1
@@ -1043,7 +1051,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
 #pragma unroll
             for (int c = 0; c < CS; c += 2) {
               const int row = tail->out_row[c0 + c + (lane & 1)];
-              to[c / 2] = row >= 0 && has_dim ? static_cast<uint16_t*>(a.out) +
+              to[c / 2] = row >= 0 && stores ? static_cast<uint16_t*>(a.out) +
                                                     (int64_t)row * S::DV + (dim0 & ~1)
                                               : nullptr;
               none = none || by[c] == 0.f || by[c + 1] == 0.f;
@@ -1083,10 +1091,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         if (lane == 0) mbar_arrive(&tail->o_free);
       }
     }
-    if (!ok) {
-      *abort_flag = 1;
-      if (lane == 0) report(a.status_dev, PA_ERR_TIMEOUT);
-    }
+    if (*abort_flag && lane == 0) report(a.status_dev, PA_ERR_TIMEOUT);
   }
 
   tc_fence_before();

@@ -75,6 +75,27 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity,
   return true;
 }
 
+// The far part of a wait, behind a first look that found the phase open: until it completes,
+// *abort is set (false) or the limit has passed (false).  A call of its own, with addresses in
+// shared memory, so that a wait costs its kernel few instructions and no registers.
+template <uint64_t LimitNs>
+__device__ __noinline__ bool mbar_wait_far(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
+  const uint64_t t0 = globaltimer();
+  uint32_t done;
+  int gone;
+  do {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%2], %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "ld.volatile.shared.s32 %1, [%4];\n\t}"
+        : "=&r"(done), "=&r"(gone)
+        : "r"(bar), "r"(parity), "r"(abort_flag)
+        : "memory");
+  } while (!done && !gone && globaltimer() - t0 <= LimitNs);
+  return done != 0;
+}
+
 // -------------------------------------------------------------------- TMA --
 
 // Bring the 128-byte line holding p into L2 (no register result, no wait).
