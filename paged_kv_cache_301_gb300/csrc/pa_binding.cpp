@@ -379,14 +379,14 @@ long latent_append(Args a) {
            "q_rope and q_out are [T, Hq, rope], of the pool's dtype");
     Hq = q->size(1);
     a.need(Hq > 0, "no query heads");
-    for (const Tensor* t : {q, out}) {
+    const auto strides = [&](const Tensor* t, int64_t& s, int64_t& h) {
       a.need(t->stride(2) == 1, "the elements of a head must be packed");
-      int64_t& s = t == q ? qs : os;
-      int64_t& h = t == q ? qh : oh;
       h = Hq > 1 ? t->stride(1) : P;
       s = T > 1 ? t->stride(0) : Hq * h;
       a.need(h >= P && s >= (Hq - 1) * h + P, "heads or tokens that share elements");
-    }
+    };
+    strides(q, qs, qh);                        // q_out may be the same object
+    strides(out, os, oh);
   }
   a.need(tables.dim() == 2 && lens.numel() == tables.size(0) && (!pos || pos->numel() == T) &&
              (q_start ? q_start->numel() == tables.size(0) + 1 : T == tables.size(0)),
