@@ -591,8 +591,11 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
  *   q_rope       [total_q, num_q_heads, rope_dim] with token and head strides (0 =
  *                packed), or NULL (num_q_heads is ignored); q_out likewise.  The strides
  *                let both be parts of wider rows, as [.., latent_dim:] of the absorbed
- *                query.  q_out may be q_rope itself (same strides), or other columns
- *                of the same rows; any other overlap with an input is rejected.
+ *                query.  q_out may be q_rope itself (same strides); else it must not
+ *                share a byte with q_rope, latent or key_rope (rejected).  All four may
+ *                be columns of the same rows, as one projection's output; of rows at two
+ *                different strides, and heads at two different distances, it is their
+ *                spans that must not meet.
  *   weight       [latent_dim] storage type, nullable
  *   cos_sin      [max_position, rope_dim] fp32, nullable; positions as in pa_rope_append
  * Strides are multiples of 8 elements, times their count at most 2^40; addresses

@@ -16,6 +16,7 @@
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_q8.cuh"
+#include "pa_share.h"
 
 namespace pa {
 namespace {
@@ -311,12 +312,6 @@ __global__ void __launch_bounds__(32 * kWarps) latent_gather_kernel(const Gather
   }
 }
 
-// Bytes [p, p + n) and [q, q + m).
-bool overlaps(const void* p, int64_t n, const void* q, int64_t m) {
-  const uintptr_t x = (uintptr_t)p, y = (uintptr_t)q;
-  return x < y + (uint64_t)m && y < x + (uint64_t)n;
-}
-
 // Bytes from the first to the last element of rows of `row` elements, `stride` apart.
 int64_t span(int64_t rows, int64_t stride, int64_t row) { return 2 * ((rows - 1) * stride + row); }
 
@@ -354,17 +349,16 @@ pa_status check_append(const AppendArgs& a, int R) {
       a.out_stride < (a.Hq - 1) * a.out_head + kRope)
     return PA_ERR_INVALID_ARG;
   const int64_t T = a.total_q, heads = a.Hq;
-  const int64_t in = span(T, a.q_stride, (heads - 1) * a.q_head + kRope);
-  const int64_t out = span(T, a.out_stride, (heads - 1) * a.out_head + kRope);
-  if (overlaps(a.q_out, out, a.latent, span(T, a.latent_stride, R)) ||
-      overlaps(a.q_out, out, a.key, span(T, a.key_stride, kRope)))
+  const Rows in = rows_of(a.q, T, a.q_stride, heads, a.q_head, kRope);
+  const Rows out = rows_of(a.q_out, T, a.out_stride, heads, a.out_head, kRope);
+  if (share(out, rows_of(a.latent, T, a.latent_stride, 1, 0, R)) ||
+      share(out, rows_of(a.key, T, a.key_stride, 1, 0, kRope)))
     return PA_ERR_INVALID_ARG;
-  if (!overlaps(a.q_out, out, a.q, in)) return PA_OK;
-  // the same rows, in place or other columns of every head
-  if (a.q_stride != a.out_stride || a.q_head != a.out_head || a.q_stride < heads * a.q_head)
-    return PA_ERR_INVALID_ARG;
-  const int64_t by = ((intptr_t)a.q_out - (intptr_t)a.q) / 2, far = by < 0 ? -by : by;
-  return far == 0 || (far >= kRope && far + kRope <= a.q_head) ? PA_OK : PA_ERR_INVALID_ARG;
+  // in place, each element read and written by the same lane; else no byte of both
+  if (a.q_out == a.q && (T == 1 || a.q_stride == a.out_stride) &&
+      (heads == 1 || a.q_head == a.out_head))
+    return PA_OK;
+  return share(out, in) ? PA_ERR_INVALID_ARG : PA_OK;
 }
 
 }  // namespace
