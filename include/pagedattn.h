@@ -595,7 +595,9 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
  *                share a byte with q_rope, latent or key_rope (rejected).  All four may
  *                be columns of the same rows, as one projection's output; of rows at two
  *                different strides, and heads at two different distances, it is their
- *                spans that must not meet.
+ *                spans that must not meet.  Nor may the span of q_out meet weight,
+ *                cos_sin or an index array.
+ *   pool         none of it may be read: no input, nor q_out, lies in it (rejected)
  *   weight       [latent_dim] storage type, nullable
  *   cos_sin      [max_position, rope_dim] fp32, nullable; positions as in pa_rope_append
  * Strides are multiples of 8 elements, times their count at most 2^40; addresses

@@ -340,6 +340,25 @@ pa_status check_append(const AppendArgs& a, int R) {
     return PA_ERR_INVALID_ARG;
   if (!within(a.total_q, a.latent_stride) || !within(a.total_q, a.key_stride))
     return PA_ERR_INVALID_ARG;
+  const int64_t T = a.total_q, heads = a.Hq;
+  const Rows latent = rows_of(a.latent, T, a.latent_stride, 1, 0, R);
+  const Rows key = rows_of(a.key, T, a.key_stride, 1, 0, kRope);
+  const int64_t pool_bytes = 2 * (int64_t)a.num_blocks * a.bs * (R + kRope);
+  // which rows of the pool are written only the GPU knows: none of it may be read
+  auto in_pool = [&](const void* p, int64_t n) { return overlaps(a.pool, pool_bytes, p, n); };
+  const struct {
+    const void* p;
+    int64_t n;
+  } whole[] = {{a.weight, 2 * (int64_t)R},
+               {a.cos_sin, 4 * (int64_t)a.max_position * kRope},
+               {a.positions, 4 * T},
+               {a.tables, 4 * (int64_t)a.B * a.max_blocks},
+               {a.lens, 4 * (int64_t)a.B},
+               {a.q_start, 4 * ((int64_t)a.B + 1)}};
+  if (in_pool(latent.base, latent.span()) || in_pool(key.base, key.span()))
+    return PA_ERR_INVALID_ARG;
+  for (const auto& w : whole)
+    if (w.p && in_pool(w.p, w.n)) return PA_ERR_INVALID_ARG;
   if (!a.q) return PA_OK;
   if (!within(a.Hq, a.q_head) || !within(a.Hq, a.out_head) || !within(a.total_q, a.q_stride) ||
       !within(a.total_q, a.out_stride))
@@ -348,12 +367,12 @@ pa_status check_append(const AppendArgs& a, int R) {
       a.out_head < kRope || a.q_stride < (a.Hq - 1) * a.q_head + kRope ||
       a.out_stride < (a.Hq - 1) * a.out_head + kRope)
     return PA_ERR_INVALID_ARG;
-  const int64_t T = a.total_q, heads = a.Hq;
   const Rows in = rows_of(a.q, T, a.q_stride, heads, a.q_head, kRope);
   const Rows out = rows_of(a.q_out, T, a.out_stride, heads, a.out_head, kRope);
-  if (share(out, rows_of(a.latent, T, a.latent_stride, 1, 0, R)) ||
-      share(out, rows_of(a.key, T, a.key_stride, 1, 0, kRope)))
-    return PA_ERR_INVALID_ARG;
+  if (in_pool(in.base, in.span()) || in_pool(out.base, out.span())) return PA_ERR_INVALID_ARG;
+  for (const auto& w : whole)
+    if (w.p && overlaps(out.base, out.span(), w.p, w.n)) return PA_ERR_INVALID_ARG;
+  if (share(out, latent) || share(out, key)) return PA_ERR_INVALID_ARG;
   // in place, each element read and written by the same lane; else no byte of both
   if (a.q_out == a.q && (T == 1 || a.q_stride == a.out_stride) &&
       (heads == 1 || a.q_head == a.out_head))

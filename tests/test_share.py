@@ -87,3 +87,21 @@ def test_append_refuses_shared_bytes(lib):                 # noqa: F811
     assert g(q_out=q + 2 * 96, Hq=1, qs=128, os=128) == 1  # into the next token's head
     assert g(q_out=q, Hq=1, qs=128, os=192) == 1           # in place with other token strides
     assert g(q_out=q, Hq=2, qs=256, os=256, oh=128) == 1   # or other head strides
+
+
+def test_append_refuses_inputs_that_it_writes(lib):        # noqa: F811
+    def g(**kw):
+        return _append(lib, **kw)
+    inside = A["pool"] + 64                                # 8 blocks of 16 rows of 1,152 bytes
+    last = A["pool"] + 8 * 16 * 1152 - 16
+    none = dict(q_rope=None, q_out=None)
+    for p in ("latent", "key", "weight", "cos_sin", "positions", "tables", "lens", "q_start"):
+        for at in (inside, last):
+            assert g(**{p: at}) == 1 and g(**none, **{p: at}) == 1, p
+    assert g(q_rope=inside) == 1 and g(q_out=last) == 1
+    assert g(latent=A["pool"] - 1024) == 1                 # its fifth row's end is in the pool
+    for p in ("weight", "cos_sin", "tables", "lens", "q_start"):
+        assert g(q_out=A[p]) == 1, p
+    assert g(positions=A["q_out"] + 64) == 1
+    assert g(q_out=A["weight"] + 2 * 512 - 16) == 1        # its last bytes
+    assert g(q_out=A["cos_sin"] + 64 * 64 * 4 - 16) == 1
