@@ -69,6 +69,11 @@ typedef enum pa_status {
 
 typedef enum pa_dtype { PA_FLOAT16 = 0, PA_BFLOAT16 = 1 } pa_dtype;
 
+/* May be added to the dtype of pa_decode_tree, pa_latent_decode and pa_latent_prefill: the
+ * softmax weights enter the product with V as two terms of the storage type whatever the
+ * shape, as in pa_decode and pa_prefill. */
+#define PA_TWO_TERMS 0x100
+
 /* Human-readable name of a status code (static string). */
 const char* pa_status_string(int status);
 
@@ -553,7 +558,7 @@ pa_status pa_expand_blocks_q8(void* k_pool, void* v_pool, const void* k_pool8, c
  * with V as two terms of the storage type (15 bits or more) where a KV head has at most 32
  * columns (max_q_len * num_q_heads / num_kv_heads), else rounded to it once (bf16 2^-8 of
  * the weight at most, fp16 2^-11): with more columns the second term is no longer hidden
- * behind the cache's bytes.
+ * behind the cache's bytes.  With PA_TWO_TERMS in dtype they are two terms in any case.
  * workspace: at least pa_decode_tree_workspace_bytes(...) bytes (0 for invalid
  * arguments), 256-byte aligned, contents arbitrary, not shared by calls that overlap on
  * the GPU.
@@ -677,7 +682,8 @@ pa_status pa_latent_decode(void* out, const void* q, const void* pool,
  * A sequence with n_b > m_b, n_b > max_q_len, or rows outside [0, total_q) or [0,
  * total_kv) is skipped (rows untouched; reported in checked mode).  Infinities and NaN of
  * tokens that a row does not see have no part in it.  fp32 sums and statistics; the
- * softmax weights enter the product rounded to the storage type.
+ * softmax weights enter the product rounded to the storage type, or as two terms of it
+ * with PA_TWO_TERMS in dtype.
  * Supported: fp16 / bf16, nope_dim 128, rope_dim 64, value_dim 128; scale > 0.  No
  * workspace.
  */

@@ -501,10 +501,13 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
                    q_start: Optional[torch.Tensor], scale: float,
                    tree_mask: Optional[torch.Tensor] = None, max_q_len: Optional[int] = None,
                    max_seq_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
-                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                   status: Optional[torch.Tensor] = None, stream=None,
+                   two_terms: bool = False) -> torch.Tensor:
     """Decode attention of each sequence's last n_b tokens, a chain or (tree_mask) a tree,
     split over the length (see include/pagedattn.h, pa_decode_tree).  max_q_len is read from
-    q_start, with a device sync, when omitted; max_seq_len and workspace as in pa_decode."""
+    q_start, with a device sync, when omitted; max_seq_len and workspace as in pa_decode.
+    two_terms keeps the softmax weights in two terms of the storage type, as pa_prefill does,
+    also above 32 columns a KV head."""
     most_q = _most_rows(q_start, max_q_len)
     if max_seq_len is None:
         max_seq_len = block_tables.shape[1] * k_pool.shape[1]
@@ -512,7 +515,7 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
         workspace = workspace_for_tree(q, k_pool, most_q, stream)
     st = (_native or _bind()).decode_tree(out, q, k_pool, v_pool, block_tables, seq_lens, q_start,
                                           tree_mask, scale, most_q, max_seq_len, workspace, status,
-                                          stream)
+                                          stream, two_terms)
     _check(st, "pa_decode_tree")
     return out
 
@@ -571,10 +574,11 @@ def pa_latent_decode(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor,
                      q_start: Optional[torch.Tensor] = None,
                      tree_mask: Optional[torch.Tensor] = None, max_q_len: Optional[int] = None,
                      max_seq_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
-                     status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                     status: Optional[torch.Tensor] = None, stream=None,
+                     two_terms: bool = False) -> torch.Tensor:
     """Attention in the absorbed form over the latent cache: q [T, Hq, R + 64], out [T, Hq, R],
     one new token per sequence or (q_start) several, a chain or a tree (see
-    include/pagedattn.h, pa_latent_decode).  Defaults as in pa_decode_tree."""
+    include/pagedattn.h, pa_latent_decode).  Defaults and two_terms as in pa_decode_tree."""
     most_q = _most_rows(q_start, max_q_len)
     if max_seq_len is None:
         max_seq_len = block_tables.shape[1] * pool.shape[1]
@@ -582,7 +586,7 @@ def pa_latent_decode(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor,
         workspace = workspace_for_latent(out, pool, most_q, stream)
     st = (_native or _bind()).latent_decode(out, q, pool, block_tables, seq_lens, q_start,
                                             tree_mask, scale, most_q, max_seq_len, workspace,
-                                            status, stream)
+                                            status, stream, two_terms)
     _check(st, "pa_latent_decode")
     return out
 
@@ -590,12 +594,15 @@ def pa_latent_decode(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor,
 def pa_latent_prefill(out: torch.Tensor, q: torch.Tensor, kv: torch.Tensor,
                       key_rope: torch.Tensor, q_start: torch.Tensor, kv_start: torch.Tensor,
                       scale: float, max_q_len: Optional[int] = None,
-                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                      status: Optional[torch.Tensor] = None, stream=None,
+                      two_terms: bool = False) -> torch.Tensor:
     """Causal attention in the expanded form: q [T, H, 128 + 64], kv [S, H, 128 + 128] (a head's
     key part, then its value), key_rope [S, 64] shared by the heads (see include/pagedattn.h,
-    pa_latent_prefill).  max_q_len is read from q_start, with a device sync, when omitted."""
+    pa_latent_prefill).  max_q_len is read from q_start, with a device sync, when omitted.
+    two_terms keeps the softmax weights in two terms of the storage type, as pa_prefill does."""
     st = (_native or _bind()).latent_prefill(out, q, kv, key_rope, q_start, kv_start, scale,
-                                             _most_rows(q_start, max_q_len), status, stream)
+                                             _most_rows(q_start, max_q_len), status, stream,
+                                             two_terms)
     _check(st, "pa_latent_prefill")
     return out
 

@@ -251,6 +251,13 @@ long expand_q8(Args a) {
                              a.dtype(kp), ptr_as<int32_t>(status), a.stream(8));
 }
 
+// The dtype of a call whose weights may be asked for as two terms.
+int dtype_of(const Args& a, const Tensor& t, int two_terms) {
+  const int two = PyObject_IsTrue(a.v[two_terms]);
+  if (two < 0) throw Bad("");
+  return a.dtype(t) | (two ? PA_TWO_TERMS : 0);
+}
+
 // A count given as a Python int.
 int64_t whole(const Args& a, int i, const char* what) {
   const int64_t n = PyLong_AsLongLong(a.v[i]);
@@ -280,7 +287,7 @@ int check_rows(const Args& a, int64_t T, const Tensor& tables, const Tensor& len
 }
 
 // out, q, k_pool, v_pool, block_tables, seq_lens, q_start, tree_mask, scale, max_q_len,
-// max_seq_len, workspace, status, stream.
+// max_seq_len, workspace, status, stream, two_terms.
 long decode_tree(Args a) {
   const Tensor& out = *a.packed(0);
   const Tensor& q = *a.packed(1);
@@ -307,12 +314,12 @@ long decode_tree(Args a) {
                         ptr_as<int32_t>(&lens), ptr_as<int32_t>(q_start), ptr_as<int32_t>(mask),
                         (int)tables.size(0), (int)q.size(0), (int)q.size(1), (int)k.size(2),
                         (int)q.size(2), (int)k.size(1), (int)tables.size(1), (int)k.size(0),
-                        most_q, words, most, (float)scale, a.dtype(q), ptr(&ws),
+                        most_q, words, most, (float)scale, dtype_of(a, q, 14), ptr(&ws),
                         ws.numel() * ws.element_size(), ptr_as<int32_t>(status), a.stream(13));
 }
 
 // out, q, pool, block_tables, seq_lens, q_start, tree_mask, scale, max_q_len, max_seq_len,
-// workspace, status, stream.
+// workspace, status, stream, two_terms.
 long latent_decode(Args a) {
   const Tensor& out = *a.packed(0);
   const Tensor& q = *a.packed(1);
@@ -338,7 +345,7 @@ long latent_decode(Args a) {
                           ptr_as<int32_t>(&lens), ptr_as<int32_t>(q_start), ptr_as<int32_t>(mask),
                           (int)tables.size(0), (int)q.size(0), (int)q.size(1), (int)out.size(2),
                           (int)(q.size(2) - out.size(2)), (int)pool.size(1), (int)tables.size(1),
-                          (int)pool.size(0), most_q, words, most, (float)scale, a.dtype(q),
+                          (int)pool.size(0), most_q, words, most, (float)scale, dtype_of(a, q, 13),
                           ptr(&ws), ws.numel() * ws.element_size(), ptr_as<int32_t>(status),
                           a.stream(12));
 }
@@ -425,7 +432,7 @@ long latent_gather(Args a) {
                           (int)pool.size(0), a.dtype(pool), ptr_as<int32_t>(status), a.stream(7));
 }
 
-// out, q, kv, key_rope, q_start, kv_start, scale, max_q_len, status, stream.
+// out, q, kv, key_rope, q_start, kv_start, scale, max_q_len, status, stream, two_terms.
 long latent_prefill(Args a) {
   const Tensor& out = *a.packed(0);
   const Tensor& q = *a.packed(1);
@@ -451,7 +458,7 @@ long latent_prefill(Args a) {
   return pa_latent_prefill(ptr(&out), ptr(&q), ptr(&kv), ptr(&k), ptr_as<int32_t>(&qs),
                            ptr_as<int32_t>(&ks), (int)qs.numel() - 1, (int)q.size(0),
                            (int)kv.size(0), stride, (int)q.size(1), (int)N, (int)P, (int)V, most,
-                           (float)scale, a.dtype(q), ptr_as<int32_t>(status), a.stream(9));
+                           (float)scale, dtype_of(a, q, 10), ptr_as<int32_t>(status), a.stream(9));
 }
 
 template <typename F>
@@ -483,10 +490,10 @@ PyObject* py_expand_q8(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return call("pa_expand_blocks_q8", v, n, 9, expand_q8);
 }
 PyObject* py_decode_tree(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return call("pa_decode_tree", v, n, 14, decode_tree);
+  return call("pa_decode_tree", v, n, 15, decode_tree);
 }
 PyObject* py_latent_decode(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return call("pa_latent_decode", v, n, 13, latent_decode);
+  return call("pa_latent_decode", v, n, 14, latent_decode);
 }
 PyObject* py_latent_append(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return call("pa_latent_append", v, n, 15, latent_append);
@@ -495,7 +502,7 @@ PyObject* py_latent_gather(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return call("pa_latent_gather", v, n, 8, latent_gather);
 }
 PyObject* py_latent_prefill(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return call("pa_latent_prefill", v, n, 10, latent_prefill);
+  return call("pa_latent_prefill", v, n, 11, latent_prefill);
 }
 
 PyMethodDef kMethods[] = {

@@ -8,12 +8,27 @@ namespace pa {
 namespace {
 
 // Up to 32 columns the second term of the weights costs nothing: the cache's bytes take longer.
-// With 64 it would cost 10% (16-token trees of 64 sequences, 125 us for 113) to 27% (a 60-token
-// tree over 50,001 tokens, 188 us for 148), its rows shared memory that tiles are on their way to.
+// With 64 it costs 11% (16-token trees of 64 sequences, 121 us for 108) to 26% (a 60-token tree
+// over 50,001 tokens, 185 us for 147), its rows shared memory that tiles are on their way to:
+// there the caller chooses.
 template <int N>
 using Tree128 = multi::Shape<128, 2, 2, false, N, N <= 32 ? 2 : 1>;
 template <int N>
 using Tree64 = multi::Shape<128, 1, 1, false, N, N <= 32 ? 2 : 1>;
+template <int N>
+using Exact128 = multi::Shape<128, 2, 2, false, N, 2>;
+template <int N>
+using Exact64 = multi::Shape<128, 1, 1, false, N, 2>;
+
+template <int DT, class... X>
+cudaError_t launch_tree(const multi::Call& c, int head_dim, int n, X&&... x) {
+  // up to 32 columns both are one shape
+  if (head_dim == 128)
+    return multi::two_terms(c) ? multi::launch_columns<Exact128, DT>(n, x...)
+                               : multi::launch_columns<Tree128, DT>(n, x...);
+  return multi::two_terms(c) ? multi::launch_columns<Exact64, DT>(n, x...)
+                             : multi::launch_columns<Tree64, DT>(n, x...);
+}
 
 }  // namespace
 }  // namespace pa
@@ -52,17 +67,14 @@ extern "C" pa_status pa_decode_tree(void* out, const void* q, const void* k_pool
                          num_seqs, total_q, num_q_heads, num_kv_heads, block_size, max_blocks,
                          num_blocks, max_q_len, mask_words, max_seq_len, scale, dtype, workspace,
                          workspace_bytes, status_dev, stream};
+  const bool bf16 = multi::storage(c) == PA_BFLOAT16;
   bool work;
   st = multi::check(c, pa_decode_tree_workspace_bytes(num_q_heads, num_kv_heads, head_dim,
                                                       max_q_len), &work);
   if (st != PA_OK || !work) return st;
-  return multi::run(c, Tree128<16>::TOK, head_dim, head_dim / 64, true,
+  return multi::run(c, Tree128<16>::TOK, head_dim, head_dim / 64, true, multi::kWidest,
                     [&](int n, auto&&... x) {
-    if (head_dim == 128)
-      return dtype == PA_BFLOAT16
-                 ? multi::launch_columns<Tree128, PA_BFLOAT16>(n, x..., stream)
-                 : multi::launch_columns<Tree128, PA_FLOAT16>(n, x..., stream);
-    return dtype == PA_BFLOAT16 ? multi::launch_columns<Tree64, PA_BFLOAT16>(n, x..., stream)
-                                : multi::launch_columns<Tree64, PA_FLOAT16>(n, x..., stream);
+    return bf16 ? launch_tree<PA_BFLOAT16>(c, head_dim, n, x..., stream)
+                : launch_tree<PA_FLOAT16>(c, head_dim, n, x..., stream);
   });
 }

@@ -9,11 +9,14 @@ namespace {
 
 // A tile of 64 tokens of 576 elements is 72 KB; two of them and 64 columns of q fill an SM's
 // shared memory, with the weights over the tile's rotated part, which S alone needs.  Up to 32
-// columns the second term of the weights costs nothing: the cache's bytes take longer.
+// columns the second term of the weights costs nothing: the cache's bytes take longer.  With 64
+// it has no room there, so that a caller who asks for it gets groups of 32 columns (128 heads of 64
+// sequences 129 us for 77; 48 columns over eight sequences to 131,072 tokens 255 us for 138).
+constexpr int kTwoTerms = 32;
 template <int N>
-using Latent512 = multi::Shape<64, 9, 8, true, N, N <= 32 ? 2 : 1>;
+using Latent512 = multi::Shape<64, 9, 8, true, N, N <= kTwoTerms ? 2 : 1>;
 template <int N>
-using Latent256 = multi::Shape<128, 5, 4, true, N, N <= 32 ? 2 : 1>;
+using Latent256 = multi::Shape<128, 5, 4, true, N, N <= kTwoTerms ? 2 : 1>;
 
 }  // namespace
 }  // namespace pa
@@ -50,17 +53,18 @@ extern "C" pa_status pa_latent_decode(void* out, const void* q, const void* pool
                          total_q, num_q_heads, 1, block_size, max_blocks, num_blocks, max_q_len,
                          mask_words, max_seq_len, scale, dtype, workspace, workspace_bytes,
                          status_dev, stream};
+  const bool bf16 = multi::storage(c) == PA_BFLOAT16;
   bool work;
   st = multi::check(c, pa_latent_decode_workspace_bytes(num_q_heads, latent_dim, rope_dim,
                                                         max_q_len), &work);
   if (st != PA_OK || !work) return st;
   return multi::run(c, latent_dim == 512 ? Latent512<16>::TOK : Latent256<16>::TOK, latent_dim,
-                    (latent_dim + rope_dim) / 64, false, [&](int n, auto&&... x) {
+                    (latent_dim + rope_dim) / 64, false,
+                    multi::two_terms(c) ? kTwoTerms : multi::kWidest, [&](int n, auto&&... x) {
     if (latent_dim == 512)
-      return dtype == PA_BFLOAT16
-                 ? multi::launch_columns<Latent512, PA_BFLOAT16>(n, x..., stream)
-                 : multi::launch_columns<Latent512, PA_FLOAT16>(n, x..., stream);
-    return dtype == PA_BFLOAT16 ? multi::launch_columns<Latent256, PA_BFLOAT16>(n, x..., stream)
-                                : multi::launch_columns<Latent256, PA_FLOAT16>(n, x..., stream);
+      return bf16 ? multi::launch_columns<Latent512, PA_BFLOAT16>(n, x..., stream)
+                  : multi::launch_columns<Latent512, PA_FLOAT16>(n, x..., stream);
+    return bf16 ? multi::launch_columns<Latent256, PA_BFLOAT16>(n, x..., stream)
+                : multi::launch_columns<Latent256, PA_FLOAT16>(n, x..., stream);
   });
 }

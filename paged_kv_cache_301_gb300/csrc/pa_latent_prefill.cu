@@ -8,7 +8,7 @@
 // 128 keys (48 KB: two slabs of the head's own part, one of the shared rotated part) and
 // their values (32 KB) serves both:
 //   S_k [128 x 128] = Q_k [128 x 192] . K^T    (TMEM, 128 columns)
-//   P_k over the columns of S_k it came from, in the storage type
+//   P_k over the columns of S_k it came from, in the storage type (a second term behind it)
 //   O_k [128 x 128] += P_k . V                  (P from TMEM, V from shared memory)
 // The tensor cores alternate between the tiles, P_A . V, S_A of the next keys, P_B . V, S_B,
 // while the softmax warps of the other tile work.  The running maximum is raised only where
@@ -17,8 +17,9 @@
 // Shared memory holds both query tiles (96 KB), two tiles of keys and one of values: keys are
 // asked for a tile ahead, values while S_B of the next keys runs.
 //
-// Weights are rounded to the storage type once (half a step: bf16 2^-8, fp16 2^-11 of each):
-// a second term would cost another product, as much as the first.
+// Weights are rounded to the storage type once (half a step: bf16 2^-8, fp16 2^-11 of each), or
+// with PA_TWO_TERMS kept as two terms, the second behind the first over the columns of S and with
+// a product of its own (331 us for the prompts below, 165 for the chunks).
 //
 // Bound: for 256 rows and 128 keys the tensor cores take 2,600 cycles and the exponentials
 // 2,050; a query tile's own chain (scores, softmax, product, and the waits between them) takes
@@ -150,7 +151,8 @@ __device__ __forceinline__ bool odd2(uint32_t w) {
   return (w & e) == e || (w >> 16 & e) == e;
 }
 
-template <int DT>
+// TERMS: storage-type terms of a softmax weight.
+template <int DT, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_kv,
@@ -284,8 +286,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       const uint32_t keep = t > 0 || *const_cast<volatile int*>(&tl->keep[k]);
 #pragma unroll
       for (int x = 0; x < kKeys / 16; ++x)
-        mma_ts_by_one(tmem + 256 + k * kDv, tmem + k * kKeys + x * 8,
-                      v_desc + (uint64_t)(x * 16 * 128 >> 4), idesc_o, x > 0 ? 1u : keep);
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+          mma_ts_by_one(tmem + 256 + k * kDv, tmem + k * kKeys + term * (kKeys / 2) + x * 8,
+                        v_desc + (uint64_t)(x * 16 * 128 >> 4), idesc_o,
+                        x > 0 || term > 0 ? 1u : keep);
       commit_by_one(&tl->pv_done[k]);
     };
     ok = wait(&tl->q_full, 0) && wait(&tl->k_full[0], 0);
@@ -381,7 +386,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
       uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
       for (int g = 0; g < kKeys; g += 32) {
-        uint32_t pw[16];
+        uint32_t pw[16], pl[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float x, y;
@@ -389,9 +394,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
           x = ex2_approx(x);
           y = ex2_approx(y);
           ls2[(e >> 1) & 1] = f2_add(ls2[(e >> 1) & 1], f2_pack(x, y));
-          pw[e >> 1] = pack2<DT>(x, y);
+          if (TERMS == 1) pw[e >> 1] = pack2<DT>(x, y);
+          else split2<DT>(x, y, &pw[e >> 1], &pl[e >> 1]);
         }
         tmem_st16_nowait(scol + g / 2, pw);      // over S columns already read
+        if (TERMS == 2) tmem_st16_nowait(scol + (kKeys + g) / 2, pl);
       }
       float ls4[4];
       f2_unpack(ls2[0], ls4[0], ls4[1]);
@@ -473,8 +480,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
             while (rows) {
               const int x = w * 32 + __ffs(rows) - 1;
               rows &= rows - 1;
-              const float2 p2 = widen2<DT>(tmem_ld1(scol + x / 2));
               const bool seen = kc + x <= pos;
+              float2 p2 = widen2<DT>(tmem_ld1(scol + x / 2));
+              if (TERMS == 2) {
+                const float2 rest = widen2<DT>(tmem_ld1(scol + (kKeys + x) / 2));
+                p2 = make_float2(p2.x + rest.x, p2.y + rest.y);
+              }
               const float p = x & 1 ? p2.y : p2.x;
               const uint32_t* v = static_cast<const uint32_t*>(a.kv) + (kDk - kRope) / 2 +
                                   ((int64_t)(ks + kc + x) * a.H + h) * (kKv / 2);
@@ -579,7 +590,7 @@ bool encode_rows(CUtensorMap* map, const void* x, int dtype, int64_t rows, int h
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DT>
+template <int DT, int TERMS>
 cudaError_t launch(const CUtensorMap (&m)[3], const Args& a, int ctas, int device,
                    cudaStream_t stream) {
   static std::mutex lock;
@@ -588,13 +599,13 @@ cudaError_t launch(const CUtensorMap (&m)[3], const Args& a, int ctas, int devic
     std::lock_guard<std::mutex> hold(lock);
     if (device >= 64 || !(done >> device & 1)) {
       const cudaError_t e = taken(cudaFuncSetAttribute(
-          latent_prefill_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+          latent_prefill_kernel<DT, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
       if (e != cudaSuccess) return e;
       if (device < 64) done |= 1ull << device;
     }
   }
-  return launch_pdl(latent_prefill_kernel<DT>, dim3((unsigned)ctas), kThreads, kSmem, stream, m[0],
-                    m[1], m[2], a);
+  return launch_pdl(latent_prefill_kernel<DT, TERMS>, dim3((unsigned)ctas), kThreads, kSmem, stream,
+                    m[0], m[1], m[2], a);
 }
 
 }  // namespace
@@ -609,6 +620,8 @@ extern "C" pa_status pa_latent_prefill(void* out, const void* q, const void* kv,
                                        int nope_dim, int rope_dim, int value_dim, int max_q_len,
                                        float scale, int dtype, int32_t* status_dev,
                                        cudaStream_t stream) {
+  const bool two = dtype & PA_TWO_TERMS;
+  dtype &= ~PA_TWO_TERMS;
   if (num_seqs < 0 || total_q < 0 || total_kv < 0 || num_heads <= 0 || max_q_len < 0 ||
       !(scale > 0.f) || !(scale < 3.0e38f) || (int64_t)total_q * num_heads >= (1ll << 31) ||
       (int64_t)total_kv * num_heads >= (1ll << 31))
@@ -652,8 +665,8 @@ extern "C" pa_status pa_latent_prefill(void* out, const void* q, const void* kv,
   a.pairs = (int)pairs;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.status_dev = status_dev;
-  const cudaError_t e = dtype == PA_BFLOAT16
-                            ? launch<PA_BFLOAT16>(m, a, (int)ctas, device, stream)
-                            : launch<PA_FLOAT16>(m, a, (int)ctas, device, stream);
+  const auto f = dtype == PA_BFLOAT16 ? (two ? launch<PA_BFLOAT16, 2> : launch<PA_BFLOAT16, 1>)
+                                      : (two ? launch<PA_FLOAT16, 2> : launch<PA_FLOAT16, 1>);
+  const cudaError_t e = f(m, a, (int)ctas, device, stream);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

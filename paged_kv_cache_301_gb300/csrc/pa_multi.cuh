@@ -71,6 +71,7 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 // cost of an item's ends, in quarters of a tile (16-token trees of 64 sequences: with 4 139 us,
 // 8 129, 12 127, 16 126)
 constexpr int kEnds = 12;
+constexpr int kWidest = 64;                    // columns of a product
 constexpr float kRaise = 8.f;                  // log2 by which a tile may exceed the maximum
 
 struct Args {
@@ -895,19 +896,7 @@ multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
                 uint32_t* lo = reinterpret_cast<uint32_t*>(
                     N > 32 ? prow + TOK * 128 + ((chunk ^ (row & 7)) << 4)
                            : prow + (((chunk + 4) ^ (row & 7)) << 4));
-                if (DT == PA_BFLOAT16) {
-                  // the top 16 bits of a weight, then of what they leave
-                  const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
-                  *hi = __byte_perm(ux, uy, 0x7632);
-                  *lo = __byte_perm(__float_as_uint(x - __uint_as_float(ux & 0xFFFF0000u)),
-                                    __float_as_uint(y - __uint_as_float(uy & 0xFFFF0000u)),
-                                    0x7632);
-                } else {
-                  const uint32_t w = pack2<DT>(x, y);
-                  const float2 f = widen2<DT>(w);
-                  *hi = w;
-                  *lo = pack2<DT>(x - f.x, y - f.y);
-                }
+                split2<DT>(x, y, hi, lo);
               }
             }
           }
@@ -1295,16 +1284,16 @@ inline bool encode_q(CUtensorMap* map, const void* q, int dtype, int64_t rows, i
 }
 
 // How the (new token, query head) pairs of a KV head become columns, by the most new tokens of
-// a sequence and the query heads of a KV head: n columns of a product, of gh heads of gn new
-// tokens; gs CTAs to a set.
+// a sequence and the query heads of a KV head: n columns of a product (at most `widest`), of gh
+// heads of gn new tokens; gs CTAs to a set.
 struct Columns {
   int n, gh, gn, chunks, gs;
 };
 
-inline Columns columns_for(int most, int G) {
+inline Columns columns_for(int most, int G, int widest = kWidest) {
   Columns c;
   const int64_t all = (int64_t)most * G;
-  c.n = all <= 16 ? 16 : (all <= 32 ? 32 : 64);
+  c.n = all <= 16 ? 16 : (all <= 32 ? 32 : widest);
   c.chunks = (G + c.n - 1) / c.n;
   c.gh = (G + c.chunks - 1) / c.chunks;
   c.gn = c.n / c.gh;
@@ -1375,12 +1364,15 @@ struct Call {
   const int32_t* mask;
   int B, total_q, Hq, H, bs, max_blocks, num_blocks, max_q, words, max_len;
   float scale;
-  int dtype;
+  int dtype;                     // with PA_TWO_TERMS or without
   void* workspace;
   size_t workspace_bytes;
   int32_t* status_dev;
   cudaStream_t stream;
 };
+
+inline int storage(const Call& c) { return c.dtype & ~PA_TWO_TERMS; }
+inline bool two_terms(const Call& c) { return c.dtype & PA_TWO_TERMS; }
 
 // Host checks; PA_OK and *work false: nothing to do.
 inline pa_status check(const Call& c, size_t workspace_needed, bool* work) {
@@ -1391,7 +1383,7 @@ inline pa_status check(const Call& c, size_t workspace_needed, bool* work) {
       (int64_t)c.num_blocks * c.bs >= (1ll << 31) || (int64_t)c.total_q * c.Hq >= (1ll << 31))
     return PA_ERR_INVALID_ARG;
   if ((c.bs != 8 && c.bs != 16 && c.bs != 32 && c.bs != 64) ||
-      (c.dtype != PA_FLOAT16 && c.dtype != PA_BFLOAT16))
+      (storage(c) != PA_FLOAT16 && storage(c) != PA_BFLOAT16))
     return PA_ERR_UNSUPPORTED;
   if (c.B == 0 || c.total_q == 0) return PA_OK;
   if (!c.out || !c.q || !c.k_pool || !c.v_pool || !c.tables || !c.lens) return PA_ERR_INVALID_ARG;
@@ -1403,11 +1395,12 @@ inline pa_status check(const Call& c, size_t workspace_needed, bool* work) {
   return PA_OK;
 }
 
-// Launches a checked call.  Launch: f(columns, maps, args, CTAs, items, cut, device).
+// Launches a checked call, with at most `widest` columns of a product.  Launch: f(columns, maps,
+// args, CTAs, items, cut, device).
 template <class F>
-pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f) {
+pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, int widest, const F& f) {
   const int max_q = c.q_start ? c.max_q : 1, G = c.Hq / c.H;
-  const Columns cols = columns_for(max_q, G);
+  const Columns cols = columns_for(max_q, G, widest);
   const int64_t groups =                       // pairs of column groups
       (((int64_t)max_q + cols.gn - 1) / cols.gn * cols.chunks + cols.gs - 1) / cols.gs;
   const int64_t nt = ((int64_t)c.max_len + tok - 1) / tok;
@@ -1423,9 +1416,9 @@ pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, const F& f)
   if ((items * nt) / sets >= (1ll << 30)) return PA_ERR_INVALID_ARG;
   if (items * nt < sets) sets = items * nt > 0 ? items * nt : 1;
   CUtensorMap maps[3];
-  if (!encode_blocks(&maps[0], c.k_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||
-      !encode_blocks(&maps[1], c.v_pool, c.dtype, c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||
-      !encode_q(&maps[2], c.q, c.dtype, c.total_q, c.Hq, slabs, cols.gh, cols.gn))
+  if (!encode_blocks(&maps[0], c.k_pool, storage(c), c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||
+      !encode_blocks(&maps[1], c.v_pool, storage(c), c.num_blocks, c.bs, heads ? c.H : 0, slabs) ||
+      !encode_q(&maps[2], c.q, storage(c), c.total_q, c.Hq, slabs, cols.gh, cols.gn))
     return PA_ERR_INVALID_ARG;
   const Layout y = layout_of(cols.n, dv);
   char* ws = static_cast<char*>(c.workspace);

@@ -60,4 +60,21 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// Two fp32 values as two terms each (15 bits or more): of bf16 the top 16 bits and the top 16 of
+// what they leave, of fp16 the nearest value and the nearest to what it leaves.
+template <int DT>
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
+  if (DT == PA_BFLOAT16) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    *hi = __byte_perm(ua, ub, 0x7632);
+    *lo = __byte_perm(__float_as_uint(a - __uint_as_float(ua & 0xFFFF0000u)),
+                      __float_as_uint(b - __uint_as_float(ub & 0xFFFF0000u)), 0x7632);
+  } else {
+    const uint32_t w = pack2<DT>(a, b);
+    const float2 f = widen2<DT>(w);
+    *hi = w;
+    *lo = pack2<DT>(a - f.x, b - f.y);
+  }
+}
+
 }  // namespace pa
