@@ -1112,25 +1112,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_q8_kernel(const Q8Args a
 
 // ------------------------------------------------------------------ host side --
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 // A pool as rows of 128 bytes; a box is one block of one head.
 bool encode_pool(CUtensorMap* map, const void* pool, int64_t rows, int block_rows) {
   const cuuint64_t dims[2] = {128, (cuuint64_t)rows}, strides[1] = {128};

@@ -102,18 +102,7 @@ __device__ __forceinline__ void tma_slab(void* dst, const CUtensorMap* map, uint
       : "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem], and with A in tensor memory, by one lane of a whole warp.
-__device__ __forceinline__ void mma_by_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
+// mma_by_one with A in tensor memory.
 __device__ __forceinline__ void mma_ts_by_one(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                               uint32_t accumulate) {
   asm volatile(
@@ -125,15 +114,6 @@ __device__ __forceinline__ void mma_ts_by_one(uint32_t d, uint32_t a, uint64_t b
       : "memory");
 }
 
-__device__ __forceinline__ void commit_by_one(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_addr(bar))
-      : "memory");
-}
-
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t t) {
   uint32_t r;
   asm volatile(
@@ -142,13 +122,6 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t t) {
       : "r"(t)
       : "memory");
   return r;
-}
-
-// Of two storage-type values in a word: is one infinite or NaN?
-template <int DT>
-__device__ __forceinline__ bool odd2(uint32_t w) {
-  constexpr uint32_t e = DT == PA_BFLOAT16 ? 0x7F80u : 0x7C00u;
-  return (w & e) == e || (w >> 16 & e) == e;
 }
 
 // TERMS: storage-type terms of a softmax weight.
@@ -554,25 +527,6 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
 }
 
 // [rows, heads, width], rows `stride` elements apart; a box is 128 rows of 64 elements of a head.

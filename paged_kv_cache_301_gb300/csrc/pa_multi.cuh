@@ -76,7 +76,6 @@ constexpr float kRaise = 8.f;                  // log2 by which a tile may excee
 
 struct Args {
   void* out;
-  const void* q;
   const void* v_src;             // the pool whose rows hold the values
   const int32_t* tables;
   const int32_t* lens;
@@ -341,30 +340,6 @@ __device__ __forceinline__ void tma_q(void* dst, const CUtensorMap* map, uint64_
       : "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem] by one lane of a whole warp.  With warp-uniform descriptors a
-// product is issued in 21 cycles, from a branch of one lane in 44 or more; a product takes 24
-// (64 rows, 16 columns) to 49 (128 rows, 64 columns).
-__device__ __forceinline__ void mma_by_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The lane that issues the products arrives on `bar` once all of them have completed.
-__device__ __forceinline__ void commit_by_one(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_addr(bar))
-      : "memory");
-}
-
 // Has the phase of this parity completed?  Does not wait.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -425,13 +400,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-
-// Of two storage-type values in a word: is one infinite or NaN?
-template <int DT>
-__device__ __forceinline__ bool odd2(uint32_t w) {
-  constexpr uint32_t e = DT == PA_BFLOAT16 ? 0x7F80u : 0x7C00u;
-  return (w & e) == e || (w >> 16 & e) == e;
 }
 
 template <class S, int DT>
@@ -1229,25 +1197,6 @@ join_kernel(const Args a, int sets, int items) {
 
 // ------------------------------------------------------------------ host side --
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-inline EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 // A pool [num_blocks, bs, heads, 64 slabs] as [heads][8-token groups][slabs][8 tokens][64]; a
 // box is one block of one head.  `heads` 0: of rows without heads.
 inline bool encode_blocks(CUtensorMap* map, const void* pool, int dtype, int64_t num_blocks, int bs,
@@ -1424,7 +1373,6 @@ pa_status run(const Call& c, int tok, int dv, int slabs, bool heads, int widest,
   char* ws = static_cast<char*>(c.workspace);
   Args a;
   a.out = c.out;
-  a.q = c.q;
   a.v_src = c.v_pool;
   a.tables = c.tables;
   a.lens = c.lens;

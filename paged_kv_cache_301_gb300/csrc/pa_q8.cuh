@@ -60,6 +60,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// Of two storage-type values in a word: is one infinite or NaN?
+template <int DT>
+__device__ __forceinline__ bool odd2(uint32_t w) {
+  constexpr uint32_t e = DT == PA_BFLOAT16 ? 0x7F80u : 0x7C00u;
+  return (w & e) == e || (w >> 16 & e) == e;
+}
+
 // Two fp32 values as two terms each (15 bits or more): of bf16 the top 16 bits and the top 16 of
 // what they leave, of fp16 the nearest value and the nearest to what it leaves.
 template <int DT>
