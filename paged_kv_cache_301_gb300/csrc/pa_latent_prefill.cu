@@ -26,9 +26,9 @@
 // 4,000 and two tiles overlap in part.
 //
 // Measured (GB300; cuBLAS 1,880 TFLOP/s): four prompts of 960 to 3,648 tokens, 32 heads, bf16
-// 269 us, 960 TFLOP/s; six chunks of 500 tokens over prefixes of up to 8,000, 16 heads, fp16
-// 125 us: the longest prefix's 64 tiles of keys are one CTA's chain.  Tried: values asked for in
-// halves (287 us for the prompts).
+// 265 us, 978 TFLOP/s; six chunks of 500 tokens, the longest of a sequence of 6,488, 16 heads,
+// fp16 123-127 us: that one's 51 tiles of keys are one CTA's chain.  Tried: values asked for in
+// halves (287 us for the prompts, 269 then).
 //
 // Values that a row does not see have no part in it: those behind the sequence's end are
 // zeroed in shared memory, and in the tiles that cut the diagonal so are rows that hold

@@ -37,14 +37,15 @@
 // PA_ERR_TIMEOUT is reported through status_dev.
 //
 // Measured (GB300, bf16; of a plain copy's 6.8 TB/s):
-//   pa_decode_tree, 64 sequences of 128..4,096, 16 drafted, 32/8 heads of 128: 107 us, 5.35
-//     TB/s, 0.79; one of 50,001, 60 drafted, 40/8: 148-152 us; 4 short ones of 4 heads: 8.0 us
-//   pa_latent_decode, 64 sequences of 128..4,096, 128 heads: 78-80 us; 8 of 32,768..131,072, 16
-//     heads, 3 drafted: 139 us, 5.4 TB/s, 0.80; 4 short ones of 16 heads, latent 256: 7.6 us
-// About 14,000 cycles pass from a CTA's start to its first tile, 6,000 from its last product to
-// its last store, and 10 us in the join of many parts; in between trees and long latent
-// sequences run at the memory's rate, 128 heads at 3,300 cycles a tile (the operands' reads from
-// shared memory: 2,000).
+//   pa_decode_tree, 64 sequences of 128..4,096, 16 drafted, 32/8 heads of 128: 106-108 us, 5.35
+//     TB/s, 0.79; one of 50,001, 60 drafted, 40/8: 147 us; 4 short ones of 4 heads: 7.7 us
+//   pa_latent_decode, 64 sequences of 128..4,096, 128 heads: 78 us; 8 of 32,768..131,072, 16
+//     heads, 3 drafted: 138 us, 5.5 TB/s, 0.80; 4 short ones of 16 heads, latent 256: 7.4 us
+// From its release a CTA takes 12,000 (trees) to 14,600 cycles (128 heads) to its first tile, 4,700
+// of them for its window; from its last product to its last store 900 (trees) to 4,500 (latent
+// 512); the join of many parts takes 6.5 to 11 us.  In between trees and long latent sequences
+// run at the memory's rate, 128 heads at 3,300 cycles a tile (the operands' reads from shared
+// memory: 2,000).  A call of few short sequences is 12,100 cycles in all.
 // Tried: tiles of 64 tokens for head_dim 128 (tree 138 us, was 125), a latent tile in halves (82,
 // was 80), the second product always first (218, was 190), polls of tile and weights at once
 // (they take the softmax's issue slots).
