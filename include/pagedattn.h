@@ -564,7 +564,10 @@ pa_status pa_expand_blocks_q8(void* k_pool, void* v_pool, const void* k_pool8, c
  * the GPU.
  * Supported: fp16 / bf16, head_dim 64 or 128, block_size 8/16/32/64, num_q_heads a
  * multiple of num_kv_heads; max_q_len * num_q_heads / num_kv_heads <= 65536,
- * max_seq_len < 2^30, a pool of less than 2^31 rows.
+ * max_seq_len < 2^30, a pool of less than 2^31 rows.  The bounds themselves may ask for
+ * 2^36 tiles at most: num_seqs * num_kv_heads * (64-column groups of max_q_len tokens) *
+ * (tiles of max_seq_len, of 64 tokens at latent_dim 512 and else 128), with num_seqs *
+ * num_kv_heads * (column groups) at most 2^31.
  */
 size_t pa_decode_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim,
                                       int max_q_len);
