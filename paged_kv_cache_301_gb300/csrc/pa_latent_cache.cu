@@ -344,6 +344,7 @@ pa_status check_append(const AppendArgs& a, int R) {
   const Rows latent = rows_of(a.latent, T, a.latent_stride, 1, 0, R);
   const Rows key = rows_of(a.key, T, a.key_stride, 1, 0, kRope);
   const int64_t pool_bytes = 2 * (int64_t)a.num_blocks * a.bs * (R + kRope);
+  const int64_t all = (int64_t)a.B * a.max_blocks, entries = all < 1ll << 60 ? all : 1ll << 60;
   // which rows of the pool are written only the GPU knows: none of it may be read
   auto in_pool = [&](const void* p, int64_t n) { return overlaps(a.pool, pool_bytes, p, n); };
   const struct {
@@ -352,7 +353,7 @@ pa_status check_append(const AppendArgs& a, int R) {
   } whole[] = {{a.weight, 2 * (int64_t)R},
                {a.cos_sin, 4 * (int64_t)a.max_position * kRope},
                {a.positions, 4 * T},
-               {a.tables, 4 * (int64_t)a.B * a.max_blocks},
+               {a.tables, 4 * entries},
                {a.lens, 4 * (int64_t)a.B},
                {a.q_start, 4 * ((int64_t)a.B + 1)}};
   if (in_pool(latent.base, latent.span()) || in_pool(key.base, key.span()))

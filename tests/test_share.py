@@ -105,3 +105,4 @@ def test_append_refuses_inputs_that_it_writes(lib):        # noqa: F811
     assert g(positions=A["q_out"] + 64) == 1
     assert g(q_out=A["weight"] + 2 * 512 - 16) == 1        # its last bytes
     assert g(q_out=A["cos_sin"] + 64 * 64 * 4 - 16) == 1
+    assert g(B=(1 << 31) - 1, MB=(1 << 31) - 1) == 1       # tables of 2^64 bytes: all of memory
